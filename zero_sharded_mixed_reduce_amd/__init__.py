@@ -1,7 +1,8 @@
 """Python binding of libzsmr.so, the ZeRO shard step on one MI355X (gfx950).
 
 Argument marshalling only: every function here has the name of a C entry
-point of ``include/zsmr.h`` and passes pointers (``tensor.data_ptr()`` or a
+point of ``include/zsmr.h`` (those of ``include/zsmr_ops.h`` are in ``ops``, and are found
+here under their names too) and passes pointers (``tensor.data_ptr()`` or a
 plain int), sizes and a HIP stream (default: torch's current stream) to it.
 All arithmetic runs in the library's HIP kernels.  There is no fallback: if
 ``libzsmr.so`` has not been built, importing the library raises.
@@ -489,3 +490,19 @@ XCD_BALANCE_DEFAULT = 1200
 
 def zsmr_set_xcd_balance(even_permille: int = XCD_BALANCE_DEFAULT) -> None:
     _check(_lib().zsmr_set_xcd_balance(int(even_permille)), "zsmr_set_xcd_balance")
+
+
+# The operators around the step need torch tensors, so their module imports
+# torch; this one does not, and a program that calls none of them need not.
+_OPS = ("zsmr_embed_lookup", "zsmr_embed_grad_workspace", "zsmr_embed_grad", "zsmr_xent_workspace",
+        "zsmr_xent_forward", "zsmr_xent_backward", "zsmr_norm_workspace", "zsmr_grad_norm",
+        "zsmr_clip_coef", "zsmr_clip_grads", "zsmr_clip_flatten", "zero_reduce_shard_sumsq",
+        "zero_clipped_step", "ZSMR_FP32")
+
+
+def __getattr__(name: str):
+    if name in _OPS:
+        from . import ops
+        globals().update({n: getattr(ops, n) for n in _OPS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

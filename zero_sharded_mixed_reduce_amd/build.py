@@ -1,7 +1,7 @@
 """Build the gfx950 shared libraries in-tree with hipcc.
 
 * ``zero_sharded_mixed_reduce_amd/libzsmr.so`` -- the ZeRO shard step (C ABI in
-  ``include/zsmr.h``).
+  ``include/zsmr.h``) and the operators around it (``include/zsmr_ops.h``).
 * ``synth/libzsmr_synth.so`` -- the GPU fill kernels of the seeded input
   generator (C ABI in ``include/zsmr_synth.h``).
 * ``ceiling/libzsmr_ceiling.so`` -- pure-read and pure-write reference
@@ -26,6 +26,8 @@ INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
 
 LIB = os.path.join(PKG, "libzsmr.so")
+LIB_SOURCES = ("zsmr_kernels.hip", "zsmr_api.cpp", "zsmr_norm.hip", "zsmr_embed.hip",
+               "zsmr_xent.hip", "zsmr_ops_api.cpp")
 SYNTH_LIB = os.path.join(ROOT, "synth", "libzsmr_synth.so")
 CEILING_LIB = os.path.join(ROOT, "ceiling", "libzsmr_ceiling.so")
 
@@ -58,7 +60,7 @@ def _build(out, sources, extra=()):
 
 
 def build_lib(extra=()):
-    _build(LIB, [os.path.join(CSRC, "zsmr_kernels.hip"), os.path.join(CSRC, "zsmr_api.cpp")], extra)
+    _build(LIB, [os.path.join(CSRC, f) for f in LIB_SOURCES], extra)
     return LIB
 
 

@@ -1,0 +1,335 @@
+// gfx950 kernels of the embedding lookup and of its gradient.
+//
+//   out[t] = rne16(scale * table[id_t]),
+//   dtable[v] = rne16([dtable[v] +] scale * sum over id_t = v of dout[t]).
+//
+// Both are bound by HBM.  The gradient's sum has to give the same bits each
+// time, so tokens are sorted by id (a stable radix sort: equal ids stay in
+// token order) and each run of equal ids is added up in that order; nothing
+// goes through atomics in global memory.  A run may be as long as the batch,
+// so it is cut at every 64 sorted tokens: a run inside one such chunk is
+// finished there, the parts of one that crosses chunks are kept in fp32 and
+// joined in order.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "zsmr_dev.h"
+#include "zsmr_ops_launch.h"
+
+#pragma clang fp contract(off)
+
+namespace zsmr {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ----------------------------------------------------------------- lookup --
+// One thread, eight elements of one row; a workgroup's threads walk along rows.
+template <int DT>
+__global__ __launch_bounds__(kThreads) void lookup_kernel(EmbedArgs a, uint32_t vecs) {
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t t = vecs == 1 ? i : i / vecs;
+    if (t >= a.tokens) return;
+    const int64_t j = (i - t * vecs) * 8;
+    const int32_t id = token_at(a.ids, a.id_bytes, t, a.vocab);
+    uint16_t* out = a.dst + t * a.dst_stride;
+    const uint16_t* row = a.src + (int64_t)(id < 0 ? 0 : id) * a.src_stride;
+    if (j + 8 <= a.width) {
+        f32x8 f = 0.f;
+        if (id >= 0) {
+            f = load8<DT>(row, j);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] *= a.scale;
+        }
+        store8<DT>(out, j, f);
+    } else {
+        for (int64_t k = j; k < a.width; ++k) store1<DT>(out, k, id < 0 ? 0.f : load1<DT>(row, k) * a.scale);
+    }
+}
+
+// ------------------------------------------------------------------- sort --
+// One pass of a stable radix sort on 9 bits.  A workgroup takes a contiguous
+// part of the keys; instead of a launch that counts and one that scans, every
+// workgroup counts all keys itself (the keys of a batch are a few hundred KB
+// in L2).  Padding is key vocab: last.
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+constexpr int kDigit = 9, kBins = 1 << kDigit;
+struct SortArgs {
+    const void* ids;
+    int32_t id_bytes;
+    int32_t tokens;
+    int64_t vocab;
+    const uint32_t *key_in, *pos_in;
+    uint32_t *key_out, *pos_out;
+    int32_t part;                   // keys of one workgroup
+    int32_t shift;
+};
+template <bool FIRST>
+__device__ __forceinline__ uint32_t sort_key(const SortArgs& a, int64_t i) {
+    if constexpr (!FIRST) return a.key_in[i];
+    const int32_t id = token_at(a.ids, a.id_bytes, i, a.vocab);
+    return id < 0 ? (uint32_t)a.vocab : (uint32_t)id;
+}
+template <bool FIRST>
+__global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a) {
+    __shared__ uint32_t total[kBins], before[kBins], cnt[kSortWaves][kBins];
+    const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
+    for (int i = tid; i < kBins; i += kSortThreads) total[i] = before[i] = 0;
+    for (int i = tid; i < kSortWaves * kBins; i += kSortThreads) (&cnt[0][0])[i] = 0;
+    __syncthreads();
+    const int64_t b0 = (int64_t)blockIdx.x * a.part;
+    const int64_t b1 = b0 + a.part < a.tokens ? b0 + a.part : a.tokens;
+#pragma unroll 4
+    for (int64_t i = tid; i < a.tokens; i += kSortThreads) {
+        const uint32_t d = (sort_key<FIRST>(a, i) >> a.shift) & (kBins - 1);
+        atomicAdd(&total[d], 1u);
+        if (i < b0) atomicAdd(&before[d], 1u);
+    }
+    // this workgroup's keys, a contiguous run for each wave
+    const int64_t run = (b1 - b0 + kSortThreads - 1) / kSortThreads * 64;
+    const int64_t w0 = b0 + wave * run;
+    const int64_t w1 = w0 + run < b1 ? w0 + run : b1;
+    for (int64_t i = w0 + lane; i < w1; i += 64) atomicAdd(&cnt[wave][(sort_key<FIRST>(a, i) >> a.shift) & (kBins - 1)], 1u);
+    __syncthreads();
+    // exclusive scan of the totals: a wave scans its 64 bins, then the waves' sums
+    __shared__ uint32_t wsum[kBins / 64];
+    uint32_t mine = 0, incl = 0;
+    if (tid < kBins) {
+        mine = incl = total[tid];
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t up = __shfl_up(incl, d);
+            if (lane >= d) incl += up;
+        }
+        if (lane == 63) wsum[wave] = incl;
+    }
+    __syncthreads();
+    if (tid < kBins) {
+        uint32_t at = incl - mine + before[tid];
+        for (int w = 0; w < wave; ++w) at += wsum[w];
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) {
+            const uint32_t c = cnt[w][tid];
+            cnt[w][tid] = at;
+            at += c;
+        }
+    }
+    __syncthreads();
+    for (int64_t i0 = w0; i0 < w1; i0 += 64) {
+        const int64_t i = i0 + lane;
+        const bool on = i < w1;
+        const uint32_t key = on ? sort_key<FIRST>(a, i) : 0u;
+        const uint32_t d = (key >> a.shift) & (kBins - 1);
+        uint64_t same = __ballot(on);
+#pragma unroll
+        for (int b = 0; b < kDigit; ++b) {
+            const uint64_t has = __ballot((d >> b) & 1);
+            same &= (d >> b) & 1 ? has : ~has;
+        }
+        const int rank = __popcll(same & ((1ull << lane) - 1));
+        uint32_t at = 0;
+        if (on) at = cnt[wave][d];
+        __builtin_amdgcn_wave_barrier();
+        if (on && rank == 0) cnt[wave][d] = at + __popcll(same);
+        __builtin_amdgcn_wave_barrier();
+        if (on) {
+            a.key_out[at + rank] = key;
+            a.pos_out[at + rank] = FIRST ? (uint32_t)i : a.pos_in[i];
+        }
+    }
+}
+
+// --------------------------------------------------------------- gradient --
+constexpr int kSorted = 64;         // sorted tokens of a chunk: one to a lane
+constexpr int kCols = 512;          // columns of a wave: eight to a lane
+constexpr int kBlockCols = kThreads / 64 * kCols;
+
+template <int DT>
+__device__ __forceinline__ void put_row(const EmbedArgs& a, uint32_t v, int64_t j, f32x8 f) {
+    uint16_t* row = a.dst + (int64_t)v * a.dst_stride;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] *= a.scale;
+    if (j + 8 <= a.width) {
+        if (a.accumulate) f += load8<DT>(row, j);
+        store8<DT>(row, j, f);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (j + k < a.width) store1<DT>(row, j + k, a.accumulate ? load1<DT>(row, j + k) + f[k] : f[k]);
+    }
+}
+__device__ __forceinline__ void put_part(float* p, int64_t j, int64_t width, f32x8 f) {
+    if (j + 8 <= width) {
+        store8<ZSMR_FP32>(p, j, f);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (j + k < width) p[j + k] = f[k];
+    }
+}
+template <int DT>
+__device__ __forceinline__ f32x8 get_row(const void* p, int64_t j, int64_t width) {
+    if (j + 8 <= width) return load8<DT>(p, j);
+    f32x8 f = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (j + k < width) f[k] = load1<DT>(p, j + k);
+    return f;
+}
+
+// part[chunk][0]: the sum of a run that came from the chunk before; [1]: of one
+// that starts here and goes on.
+template <int DT>
+__global__ __launch_bounds__(kThreads) void runs_kernel(EmbedArgs a, const uint32_t* key,
+                                                        const uint32_t* pos, float* part) {
+    const int lane = threadIdx.x % 64;
+    const int64_t j = (int64_t)blockIdx.y * kBlockCols + threadIdx.x * 8;
+    if (j - lane * 8 >= a.width) return;
+    const int64_t c = blockIdx.x, i0 = c * kSorted;
+    const int n = (int)(a.tokens - i0 < kSorted ? a.tokens - i0 : kSorted);
+    const uint32_t none = (uint32_t)a.vocab;
+    const uint32_t my_key = lane < n ? key[i0 + lane] : none;
+    const uint32_t my_pos = lane < n ? pos[i0 + lane] : 0;
+    const uint32_t prev = i0 > 0 ? key[i0 - 1] : none;
+    const uint32_t next = i0 + n < a.tokens ? key[i0 + n] : none;
+    f32x8 sum = 0.f;
+    bool first = true;                              // of the chunk
+    constexpr int kAhead = 8;
+    for (int b = 0; b < n; b += kAhead) {
+        f32x8 f[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = b + k < n ? b + k : n - 1;
+            f[k] = get_row<DT>(a.src + (int64_t)__builtin_amdgcn_readlane(my_pos, i) * a.src_stride, j, a.width);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = b + k;
+            if (i >= n) break;
+            const uint32_t v = __builtin_amdgcn_readlane(my_key, i);
+            if (v == none) return;                  // padding is last
+            sum += f[k];
+            const uint32_t after = i + 1 < n ? __builtin_amdgcn_readlane(my_key, i + 1) : next;
+            if (after == v && i + 1 < n) continue;
+            const bool came = first && prev == v, goes = after == v;
+            if (came) put_part(part + (2 * c) * a.width, j, a.width, sum);
+            else if (goes) put_part(part + (2 * c + 1) * a.width, j, a.width, sum);
+            else put_row<DT>(a, v, j, sum);
+            sum = 0.f;
+            first = false;
+        }
+    }
+}
+
+// One workgroup for each chunk whose last run starts in it and goes on.
+template <int DT>
+__global__ __launch_bounds__(kThreads) void join_runs_kernel(EmbedArgs a, const uint32_t* key,
+                                                             const float* part) {
+    const int64_t c = blockIdx.x, last = c * kSorted + kSorted - 1;
+    if (last + 1 >= a.tokens) return;
+    const uint32_t v = key[last];
+    if (v == (uint32_t)a.vocab || key[last + 1] != v) return;
+    if (c > 0 && key[c * kSorted - 1] == v) return;       // it started before this chunk
+    int64_t lo = last + 1, hi = a.tokens;                 // the run's end
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) / 2;
+        if (key[mid] == v) lo = mid + 1;
+        else hi = mid;
+    }
+    const int64_t end = (lo - 1) / kSorted;
+    const int64_t j = (int64_t)blockIdx.y * kBlockCols + threadIdx.x * 8;
+    if (j >= a.width) return;
+    f32x8 sum = get_row<ZSMR_FP32>(part + (2 * c + 1) * a.width, j, a.width);
+#pragma unroll 4
+    for (int64_t k = c + 1; k <= end; ++k) sum += get_row<ZSMR_FP32>(part + 2 * k * a.width, j, a.width);
+    put_row<DT>(a, v, j, sum);
+}
+
+// Zeros in the rows of absent tokens.
+constexpr int kZeroRows = 16;
+__global__ __launch_bounds__(kThreads) void zero_rows_kernel(EmbedArgs a, const uint32_t* key) {
+    __shared__ int present[kZeroRows];
+    const int64_t v0 = (int64_t)blockIdx.x * kZeroRows;
+    if (threadIdx.x < kZeroRows) {
+        const uint32_t v = (uint32_t)(v0 + threadIdx.x);
+        int64_t lo = 0, hi = a.tokens;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) / 2;
+            if (key[mid] < v) lo = mid + 1;
+            else hi = mid;
+        }
+        present[threadIdx.x] = lo < a.tokens && key[lo] == v;
+    }
+    __syncthreads();
+    for (int r = 0; r < kZeroRows && v0 + r < a.vocab; ++r) {
+        if (present[r]) continue;
+        uint16_t* row = a.dst + (v0 + r) * a.dst_stride;
+        for (int64_t j = threadIdx.x * 8; j < a.width; j += kThreads * 8) {
+            if (j + 8 <= a.width) *reinterpret_cast<u16x8_any*>(row + j) = u16x8(0);
+            else for (int64_t k = j; k < a.width; ++k) row[k] = 0;
+        }
+    }
+}
+
+int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
+int64_t chunks_of(int64_t tokens) { return (tokens + kSorted - 1) / kSorted; }
+
+template <int DT>
+void grad_launches(const EmbedArgs& a, const uint32_t* key, const uint32_t* pos, float* part,
+                   hipStream_t stream) {
+    if (!a.accumulate)
+        zero_rows_kernel<<<(unsigned)((a.vocab + kZeroRows - 1) / kZeroRows), kThreads, 0, stream>>>(a, key);
+    if (!a.tokens) return;
+    const dim3 grid((unsigned)chunks_of(a.tokens), (unsigned)((a.width + kBlockCols - 1) / kBlockCols));
+    runs_kernel<DT><<<grid, kThreads, 0, stream>>>(a, key, pos, part);
+    if (grid.x > 1) join_runs_kernel<DT><<<grid, kThreads, 0, stream>>>(a, key, part);
+}
+
+}  // namespace
+
+hipError_t launch_embed_lookup(const EmbedArgs& a, hipStream_t stream) {
+    const int64_t vecs = (a.width + 7) / 8, grid = (a.tokens * vecs + kThreads - 1) / kThreads;
+    if (a.dtype == ZSMR_BF16) lookup_kernel<ZSMR_BF16><<<(unsigned)grid, kThreads, 0, stream>>>(a, (uint32_t)vecs);
+    else lookup_kernel<ZSMR_FP16><<<(unsigned)grid, kThreads, 0, stream>>>(a, (uint32_t)vecs);
+    return hipGetLastError();
+}
+
+int64_t embed_grad_bytes(int64_t, int64_t width, int64_t tokens) {
+    return 4 * up16(tokens * 4) + chunks_of(tokens) * 2 * width * 4;
+}
+
+hipError_t launch_embed_grad(const EmbedArgs& a, void* ws, hipStream_t stream) {
+    const int64_t each = up16(a.tokens * 4) / 4;
+    uint32_t* key[2] = {static_cast<uint32_t*>(ws), static_cast<uint32_t*>(ws) + each};
+    uint32_t* pos[2] = {key[1] + each, key[1] + 2 * each};
+    float* part = reinterpret_cast<float*>(pos[1] + each);
+    int at = 0;
+    if (a.tokens) {
+        SortArgs s{};
+        s.ids = a.ids;
+        s.id_bytes = a.id_bytes;
+        s.tokens = (int32_t)a.tokens;
+        s.vocab = a.vocab;
+        s.part = (int32_t)std::max<int64_t>(2048, (a.tokens + 32 * 1024 - 1) / (32 * 1024) * 1024);
+        const unsigned grid = (unsigned)((a.tokens + s.part - 1) / s.part);
+        int bits = 1;
+        while (a.vocab >> bits) ++bits;                 // the largest key is vocab
+        for (int shift = 0; shift < bits; shift += kDigit, at ^= 1) {
+            s.shift = shift;
+            s.key_in = key[at ^ 1];
+            s.pos_in = pos[at ^ 1];
+            s.key_out = key[at];
+            s.pos_out = pos[at];
+            if (shift == 0) sort_kernel<true><<<grid, kSortThreads, 0, stream>>>(s);
+            else sort_kernel<false><<<grid, kSortThreads, 0, stream>>>(s);
+        }
+        at ^= 1;                                        // where the last pass wrote
+    }
+    if (a.dtype == ZSMR_BF16) grad_launches<ZSMR_BF16>(a, key[at], pos[at], part, stream);
+    else grad_launches<ZSMR_FP16>(a, key[at], pos[at], part, stream);
+    return hipGetLastError();
+}
+
+}  // namespace zsmr

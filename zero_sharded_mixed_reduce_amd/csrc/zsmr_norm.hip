@@ -1,0 +1,270 @@
+// gfx950 kernels of the global gradient norm, of clipping and of the clipped
+// shard step.
+//
+//   total = sum g^2,  norm = sqrt(total),  coef = min(1, max_norm / (norm + eps))
+//
+// All of it is bound by HBM.  Squares are taken and summed in fp64: the square
+// of an fp32 value is exact there, and neither a large nor a tiny gradient
+// leaves the range.  Each workgroup leaves one partial sum and a last small
+// launch adds them in order, so the result does not depend on timing.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "zsmr_dev.h"
+#include "zsmr_ops_launch.h"
+
+#pragma clang fp contract(off)
+
+namespace zsmr {
+namespace {
+
+constexpr int kThreads = 256;
+
+// The item whose chunks hold chunk b (uniform over the workgroup).
+template <typename A>
+__device__ __forceinline__ int item_of(const A& a, int b) {
+    int lo = 0, hi = a.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (a.it[mid].chunk0 <= b) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+template <int DT>
+__device__ __forceinline__ double chunk_sumsq(const void* p, int64_t e0, int64_t e1) {
+    double s0 = 0, s1 = 0;
+    const int64_t body = e0 + (e1 - e0) / 8 * 8;
+#pragma unroll 4
+    for (int64_t e = e0 + threadIdx.x * 8; e < body; e += kThreads * 8) {
+        const f32x8 f = load8<DT>(p, e);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            s0 = __builtin_fma((double)f[i], (double)f[i], s0);
+            s1 = __builtin_fma((double)f[i + 1], (double)f[i + 1], s1);
+        }
+    }
+    const int64_t e = body + threadIdx.x;
+    if (e < e1) {
+        const double f = load1<DT>(p, e);
+        s0 = __builtin_fma(f, f, s0);
+    }
+    return s0 + s1;
+}
+
+__global__ __launch_bounds__(kThreads) void sumsq_kernel(NormArgs a, double* partial) {
+    const int b = blockIdx.x, k = item_of(a, b);
+    const void* p = a.it[k].p;
+    const int64_t e0 = (int64_t)(b - a.it[k].chunk0) * kChunk, n = a.it[k].n;
+    const int64_t e1 = e0 + kChunk < n ? e0 + kChunk : n;
+    double s;
+    if (a.it[k].dtype == ZSMR_FP32) s = chunk_sumsq<ZSMR_FP32>(p, e0, e1);
+    else if (a.it[k].dtype == ZSMR_BF16) s = chunk_sumsq<ZSMR_BF16>(p, e0, e1);
+    else s = chunk_sumsq<ZSMR_FP16>(p, e0, e1);
+    s = block_sum<kThreads>(s);
+    if (threadIdx.x == 0) partial[b] = s;
+}
+
+constexpr int kJoinThreads = 1024;
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(const double* partial, int64_t n,
+                                                            double* sumsq, double max_norm,
+                                                            double eps, float* norm_coef) {
+    double s = 0;
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < n; i += kJoinThreads) s += partial[i];
+    s = block_sum<kJoinThreads>(s);
+    if (threadIdx.x != 0) return;
+    if (sumsq) *sumsq = s;
+    if (norm_coef) {
+        const double norm = sqrt(s), c = max_norm / (norm + eps);
+        norm_coef[0] = (float)norm;
+        norm_coef[1] = c > 1.0 ? 1.0f : (float)c;       // NaN stays
+    }
+}
+
+template <int S, int D>
+__device__ __forceinline__ void chunk_clip(const ClipItem& t, int64_t e0, int64_t e1, float c) {
+    const int64_t body = e0 + (e1 - e0) / 8 * 8;
+#pragma unroll 4
+    for (int64_t e = e0 + threadIdx.x * 8; e < body; e += kThreads * 8) {
+        f32x8 f = load8<S>(t.src, e);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= c;
+        store8<D>(t.dst, e, f);
+    }
+    const int64_t e = body + threadIdx.x;
+    if (e < e1) store1<D>(t.dst, e, load1<S>(t.src, e) * c);
+}
+template <int D>
+__device__ __forceinline__ void chunk_zero(const ClipItem& t, int64_t e0, int64_t e1) {
+    for (int64_t e = e0 + threadIdx.x; e < e1; e += kThreads) store1<D>(t.dst, e, 0.f);
+}
+
+__global__ __launch_bounds__(kThreads) void clip_kernel(ClipArgs a) {
+    const float c = a.coef ? *a.coef : 1.0f;
+    if (a.in_place && c == 1.0f) return;
+    const int b = blockIdx.x;
+    const ClipItem t = a.it[item_of(a, b)];
+    const int64_t e0 = (int64_t)(b - t.chunk0) * kChunk;
+    const int64_t e1 = e0 + kChunk < t.n ? e0 + kChunk : t.n;
+    const int s = t.src_dtype, d = t.dst_dtype;
+    if (!t.src) {
+        chunk_zero<ZSMR_BF16>(t, e0, e1);               // +0 is the same bits in both formats
+    } else if (d == ZSMR_FP32) {
+        chunk_clip<ZSMR_FP32, ZSMR_FP32>(t, e0, e1, c);  // in place only
+    } else if (d == ZSMR_BF16) {
+        if (s == ZSMR_FP32) chunk_clip<ZSMR_FP32, ZSMR_BF16>(t, e0, e1, c);
+        else if (s == ZSMR_BF16) chunk_clip<ZSMR_BF16, ZSMR_BF16>(t, e0, e1, c);
+        else chunk_clip<ZSMR_FP16, ZSMR_BF16>(t, e0, e1, c);
+    } else {
+        if (s == ZSMR_FP32) chunk_clip<ZSMR_FP32, ZSMR_FP16>(t, e0, e1, c);
+        else if (s == ZSMR_BF16) chunk_clip<ZSMR_BF16, ZSMR_FP16>(t, e0, e1, c);
+        else chunk_clip<ZSMR_FP16, ZSMR_FP16>(t, e0, e1, c);
+    }
+}
+
+// ------------------------------------------------------ the clipped step --
+__device__ __forceinline__ float mean_of(const StepArgs& a, float sum) {
+    if (!a.mean) return sum;
+    return a.inv_pow2 ? sum * a.inv_nf : sum / a.nf;
+}
+
+// One lane's eight elements: rows summed in fp32 strictly in rank order, kRows
+// loads in flight.
+constexpr int kRows = 8;
+template <int DT>
+__global__ __launch_bounds__(kThreads) void reduce_sumsq_kernel(StepArgs a, double* partial) {
+    const int64_t e = (int64_t)blockIdx.x * kTile + threadIdx.x * 8;
+    double s = 0;
+    if (e + 8 <= a.n) {
+        const uint16_t* p = a.grads + e;
+        // -0 + x is x for every x, so the sum starts at row 0 with its own bits
+        f32x8 g = -0.0f;
+        int r = 0;
+        for (; r + kRows <= a.nrows; r += kRows) {
+            u16x8 h[kRows];
+#pragma unroll
+            for (int k = 0; k < kRows; ++k)
+                h[k] = __builtin_nontemporal_load(reinterpret_cast<const u16x8_any*>(p + (int64_t)(r + k) * a.row_stride));
+#pragma unroll
+            for (int k = 0; k < kRows; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g[i] += widen16<DT>(h[k][i]);
+        }
+        for (; r < a.nrows; ++r) {
+            const u16x8 h = *reinterpret_cast<const u16x8_any*>(p + (int64_t)r * a.row_stride);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] += widen16<DT>(h[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            g[i] = mean_of(a, g[i]);
+            s = __builtin_fma((double)g[i], (double)g[i], s);
+        }
+        store8<ZSMR_FP32>(a.g_out, e, g);
+    } else {
+        for (int64_t j = e; j < a.n && j < e + 8; ++j) {
+            float g = widen16<DT>(a.grads[j]);
+            for (int r = 1; r < a.nrows; ++r) g += widen16<DT>(a.grads[(int64_t)r * a.row_stride + j]);
+            g = mean_of(a, g);
+            a.g_out[j] = g;
+            s = __builtin_fma((double)g, (double)g, s);
+        }
+    }
+    s = block_sum<kThreads>(s);
+    if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+// Adam with one fp32 rounding per operation, as zero_adam_step has it ("The
+// four schemes", Base._adam).
+__device__ __forceinline__ void adam(const AdamK& k, float g, float& w, float& m, float& v) {
+    m = k.c1 * m + k.c1m * g;
+    v = k.c2 * v + (k.c2m * g) * g;
+    const float mh = m / k.bc1;
+    const float vh = v / k.bc2;
+    w = w - (k.lr * mh) / (__builtin_sqrtf(vh) + k.eps);
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void clipped_kernel(StepArgs a, const float* coef) {
+    const float c = coef ? *coef : 1.0f;
+    // two groups of four elements a lane: each instruction of a wave covers
+    // one contiguous KB of fp32
+    const int64_t t0 = (int64_t)blockIdx.x * kTile + (threadIdx.x / 64) * 512 + (threadIdx.x % 64) * 4;
+    if (t0 + 260 <= a.n) {
+        f32x4 g[2], w[2], m[2], v[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int64_t e = t0 + j * 256;
+            g[j] = *reinterpret_cast<const f32x4_any*>(a.g_in + e);
+            w[j] = *reinterpret_cast<const f32x4_any*>(a.master + e);
+            m[j] = *reinterpret_cast<const f32x4_any*>(a.m + e);
+            v[j] = *reinterpret_cast<const f32x4_any*>(a.v + e);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int64_t e = t0 + j * 256;
+            u16x4 h;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float wi = w[j][i], mi = m[j][i], vi = v[j][i];
+                adam(a.k, g[j][i] * c, wi, mi, vi);
+                w[j][i] = wi;
+                m[j][i] = mi;
+                v[j][i] = vi;
+                h[i] = narrow16<DT>(wi);
+            }
+            *reinterpret_cast<f32x4_any*>(a.master + e) = w[j];
+            *reinterpret_cast<f32x4_any*>(a.m + e) = m[j];
+            *reinterpret_cast<f32x4_any*>(a.v + e) = v[j];
+            *reinterpret_cast<u16x4_any*>(a.p16 + e) = h;
+        }
+    } else {
+        for (int j = 0; j < 2; ++j)
+            for (int i = 0; i < 4; ++i) {
+                const int64_t e = t0 + j * 256 + i;
+                if (e >= a.n) continue;
+                float w = a.master[e], m = a.m[e], v = a.v[e];
+                adam(a.k, a.g_in[e] * c, w, m, v);
+                a.master[e] = w;
+                a.m[e] = m;
+                a.v[e] = v;
+                a.p16[e] = narrow16<DT>(w);
+            }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_sumsq(const NormArgs& a, double* partial, hipStream_t stream) {
+    sumsq_kernel<<<a.chunks, kThreads, 0, stream>>>(a, partial);
+    return hipGetLastError();
+}
+
+hipError_t launch_clip(const ClipArgs& a, hipStream_t stream) {
+    clip_kernel<<<a.chunks, kThreads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_join(const double* partial, int64_t n, double* sumsq, double max_norm,
+                       double eps, float* norm_coef, hipStream_t stream) {
+    join_kernel<<<1, kJoinThreads, 0, stream>>>(partial, n, sumsq, max_norm, eps, norm_coef);
+    return hipGetLastError();
+}
+
+hipError_t launch_reduce_sumsq(int dtype, const StepArgs& a, double* partial, hipStream_t stream) {
+    const dim3 grid((unsigned)((a.n + kTile - 1) / kTile));
+    if (dtype == ZSMR_BF16) reduce_sumsq_kernel<ZSMR_BF16><<<grid, kThreads, 0, stream>>>(a, partial);
+    else reduce_sumsq_kernel<ZSMR_FP16><<<grid, kThreads, 0, stream>>>(a, partial);
+    return hipGetLastError();
+}
+
+hipError_t launch_clipped(int dtype, const StepArgs& a, const float* coef, hipStream_t stream) {
+    const dim3 grid((unsigned)((a.n + kTile - 1) / kTile));
+    if (dtype == ZSMR_BF16) clipped_kernel<ZSMR_BF16><<<grid, kThreads, 0, stream>>>(a, coef);
+    else clipped_kernel<ZSMR_FP16><<<grid, kThreads, 0, stream>>>(a, coef);
+    return hipGetLastError();
+}
+
+}  // namespace zsmr

@@ -1,0 +1,682 @@
+// gfx950 kernels of the softmax cross entropy of a large output head.
+//
+//   s = x w^T,  lse_t = log sum_v exp s[t, v],  loss_t = lse_t - s[t, label_t]
+//   G = (exp(s - lse) - onehot) * grad,  dx = scale G w,  dw = scale G^T x
+//
+// All three products are matrix products on MFMA (16x16x32, 16-bit operands,
+// fp32 sums).  The logits never reach memory: the forward epilogue reduces a
+// tile to one (maximum, sum of exponentials) pair a token, and the backward
+// pass computes them again, a piece of the vocabulary at a time, with an
+// epilogue that leaves G in 16 bits as the operand of the other two products.
+// So a training step does 8 T V H operations where the mathematics needs 6.
+//
+// One main loop serves all products: D[m, n] = sum_k A[m, k] B[n, k] over a
+// 256 x BN tile, 64 k a step, by 8 waves.  An operand whose k is contiguous in
+// memory and one whose k is the row index both go to LDS as they lie there, by
+// loads that write LDS directly; the second kind is transposed on the way to
+// the registers by the transposing LDS read, so no operand is ever copied to
+// another layout.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "zsmr_dev.h"
+#include "zsmr_ops_launch.h"
+
+#pragma clang fp contract(off)
+
+namespace zsmr {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+constexpr int kWaves = 8, kThreads = kWaves * 64;
+constexpr int BM = 256, BK = 64;
+
+template <int DT>
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+    if constexpr (DT == ZSMR_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------- operands --
+// A matrix in memory as an operand of a product: `rows` of `cols` elements,
+// ld elements apart.  OUTER: k is the row index (rows of the tile are k),
+// otherwise k runs along a row.
+struct Mat {
+    const uint16_t* p;
+    int64_t ld, rows, cols;
+};
+
+// A tile of R (rows or columns of the product) x BK, in LDS.
+//  k along rows: R rows of 128 bytes; the 16-byte chunk c of row r sits in slot
+//    c ^ (r & 7), so that the 8 rows a read touches at a time lie in different
+//    banks.
+//  k outer: BK rows of R elements; the 32-byte unit u of row k sits in slot
+//    u ^ f(k), f = k's bits 0, 1 and 3: the transposing read of a wave takes a
+//    32-byte unit of 16 rows, which then fall in all banks evenly.
+// The loads that fill it read through a buffer descriptor whose bound makes
+// rows past the operand's end zero.
+template <int R, bool OUTER>
+struct Tile {
+    static constexpr int kBytes = R * BK * 2;
+    static constexpr int kLoads = R / 64;           // of each thread
+    uint32_t off[kLoads];                           // byte offsets of its loads from the tile's corner
+    const char* base;                               // the tile's corner at the next step
+    int64_t left;                                   // bytes from there to the operand's end
+    int64_t step;
+    int k_left;                                     // k of the operand still to load
+
+    __device__ __forceinline__ static int swizzle(int k) { return ((k & 3) | ((k >> 3 & 1) << 2)) << 1; }
+
+    // at: the tile's first row (or column) of the product; k0: first k
+    __device__ __forceinline__ void init(const Mat& m, int64_t at, int64_t k0) {
+        const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+        if constexpr (OUTER) {
+            static_assert(!OUTER || R == 256, "k-outer tiles are 256 wide");
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int k = (wave + kWaves * i) * 2 + lane / 32;
+                const int chunk = (lane % 32) ^ swizzle(k);
+                // columns past the end are no part of any result, but their
+                // addresses must stay inside the operand
+                off[i] = at + chunk * 8 < m.cols ? (uint32_t)(k * m.ld * 2 + chunk * 16) : 0x80000000u;
+            }
+            base = reinterpret_cast<const char*>(m.p + k0 * m.ld + at);
+            left = ((m.rows - k0 - 1) * m.ld + (m.cols - at)) * 2;
+            step = BK * m.ld * 2;
+            k_left = (int)(m.rows - k0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int row = (wave + kWaves * i) * 8 + lane / 8;
+                const int chunk = (lane % 8) ^ (row & 7);
+                off[i] = at + row < m.rows ? (uint32_t)(row * m.ld * 2 + chunk * 16) : 0x80000000u;
+            }
+            base = reinterpret_cast<const char*>(m.p + at * m.ld + k0);
+            left = ((m.rows - at - 1) * m.ld + (m.cols - k0)) * 2;
+            step = BK * 2;
+            k_left = (int)(m.cols - k0);
+        }
+    }
+    // Start the loads of one step into `to` (kBytes of LDS) and move on.
+    __device__ __forceinline__ void load(char* to) {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+        const int bound = left < 0 ? 0 : left > 0x7fffffff ? 0x7fffffff : (int)left;
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, bound, 0x00027000);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            uint32_t o = off[i];
+            if constexpr (!OUTER) {
+                // the last step of a row whose length is no multiple of BK:
+                // the next row's values must not come in as k
+                if (k_left < BK) {
+                    const int row = (threadIdx.x / 64 + kWaves * i) * 8 + threadIdx.x % 64 / 8;
+                    if ((((int)threadIdx.x % 8) ^ (row & 7)) * 8 >= k_left) o = 0x80000000u;
+                }
+            }
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(to + (wave + kWaves * i) * 1024), 16, o, 0, 0, 0);
+        }
+        base += step;
+        left -= step;
+        k_left -= BK;
+    }
+    // The operand registers of a lane for the 16 rows (columns) from `at` of the
+    // tile and k = 32 * kk + 8 * (lane / 16) + 0..7.
+    __device__ __forceinline__ static u32x4 read(const char* t, int at, int kk) {
+        const int lane = threadIdx.x % 64;
+        if constexpr (OUTER) {
+            const int k = kk * 32 + lane / 16 * 8 + (lane % 16) / 4;
+            const int chunk = (at / 8 + (lane % 4) / 2) ^ swizzle(k);
+            const char* p = t + k * (R * 2) + chunk * 16 + (lane & 1) * 8;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p + 4 * (R * 2)));
+            u32x4 r;
+            const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
+            r[0] = a[0];
+            r[1] = a[1];
+            r[2] = b[0];
+            r[3] = b[1];
+            return r;
+        } else {
+            const int row = at + lane % 16;
+            const int slot = (kk * 4 + lane / 16) ^ (row & 7);
+            return *reinterpret_cast<const u32x4*>(t + row * 128 + slot * 16);
+        }
+    }
+};
+
+// vmcnt(n) and lgkmcnt(0)
+#define ZSMR_WAIT(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | 0x70 | ((n) >> 4 << 14))
+
+// ------------------------------------------------------------------ product --
+enum : int { E_STATS, E_GRAD, E_DX, E_DW };
+
+struct Product {
+    Mat a, b;
+    int64_t k;                      // of the product
+    int32_t m_tiles, n_tiles, splits, k_split;      // k_split: k of one split, a multiple of BK
+    // epilogues
+    int64_t v0, vocab, tokens, width;
+    const void* labels;
+    int32_t id_bytes;
+    float2* stats;                  // E_STATS: [part][token]
+    float* target;                  // E_STATS: [token]
+    const float* lse;               // E_GRAD
+    const float* grad;              // E_GRAD: [token] or NULL
+    const float* mul;               // {factor of G, factor of the results}
+    uint16_t* g;                    // E_GRAD: [token][ldg]
+    int64_t ldg;
+    float* sum;                     // E_DX: [split][token][lds], fp32 between pieces
+    int64_t lds;
+    int32_t sum_in, sum_out;        // E_DX: add what sum holds; leave the result there
+    uint16_t* out;                  // E_DX, E_DW
+    int64_t ldo;
+    int32_t accumulate;             // E_DW
+};
+
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+
+// Column n of the result, rows m..m+3: 4 consecutive elements for a lane.
+template <int DT>
+__device__ __forceinline__ void put4(uint16_t* p, int64_t at, int64_t width, f32x4 f, bool add) {
+    if (at + 4 <= width) {
+        if (add) {
+            const u16x4 o = *reinterpret_cast<const u16x4_any*>(p + at);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) f[r] += widen16<DT>(o[r]);
+        }
+        u16x4 h;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) h[r] = narrow16<DT>(f[r]);
+        *reinterpret_cast<u16x4_any*>(p + at) = h;
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (at + r < width) p[at + r] = narrow16<DT>(add ? f[r] + widen16<DT>(p[at + r]) : f[r]);
+    }
+}
+
+template <int DT, int EPI, int BN, int WM, int STAGES>
+__global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
+    constexpr bool A_OUTER = EPI == E_DX || EPI == E_DW, B_OUTER = EPI == E_DW;
+    constexpr int WN = kWaves / WM, TM = BM / WM / 16, TN = BN / WN / 16;
+    typedef Tile<BM, A_OUTER> TA;
+    typedef Tile<BN, B_OUTER> TB;
+    constexpr int kLoads = TA::kLoads + TB::kLoads, kStage = TA::kBytes + TB::kBytes;
+    __shared__ __attribute__((aligned(1024))) char smem[STAGES * kStage];
+
+    // Consecutive workgroups go to the eight XCDs in turn; each XCD takes a
+    // contiguous run of tiles, in groups of 8 in m, so that the tiles it works
+    // on at a time share operands in its L2.
+    const int tiles = p.m_tiles * p.n_tiles * p.splits;
+    const int xcd = blockIdx.x % 8, q = tiles / 8, rem = tiles % 8;
+    int tile = xcd * q + min(xcd, rem) + (int)blockIdx.x / 8;
+    const int split = tile / (p.m_tiles * p.n_tiles);
+    tile -= split * p.m_tiles * p.n_tiles;
+    constexpr int kGroup = 8;
+    const int group = tile / (kGroup * p.n_tiles), in_group = tile - group * kGroup * p.n_tiles;
+    const int height = min(kGroup, p.m_tiles - group * kGroup);
+    const int mt = group * kGroup + in_group % height, nt = in_group / height;
+
+    const int64_t k0 = (int64_t)split * p.k_split;
+    const int64_t kn = p.k - k0 < p.k_split ? p.k - k0 : p.k_split;
+    const int steps = (int)((kn + BK - 1) / BK);
+
+    TA ta;
+    TB tb;
+    ta.init(p.a, (int64_t)mt * BM, k0);
+    tb.init(p.b, (int64_t)nt * BN, k0);
+
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int wm = wave % WM, wn = wave / WM;
+    f32x4 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = 0.f;
+
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s)
+        if (s < steps) {
+            ta.load(smem + s * kStage);
+            tb.load(smem + s * kStage + TA::kBytes);
+        }
+    int at = 0, to = STAGES - 1;
+    for (int s = 0; s < steps; ++s) {
+        // this step's tile has arrived; the steps after it may be in flight
+        if (s + STAGES - 2 < steps) ZSMR_WAIT((STAGES - 2) * kLoads);
+        else ZSMR_WAIT(0);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        // every wave is done with the stage before: refill it
+        if (s + STAGES - 1 < steps) {
+            ta.load(smem + to * kStage);
+            tb.load(smem + to * kStage + TA::kBytes);
+        }
+        const char* sa = smem + at * kStage;
+        const char* sb = sa + TA::kBytes;
+#pragma unroll
+        for (int kk = 0; kk < BK / 32; ++kk) {
+            u32x4 b[TN];
+#pragma unroll
+            for (int j = 0; j < TN; ++j) b[j] = TB::read(sb, (wn * TN + j) * 16, kk);
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const u32x4 a = TA::read(sa, (wm * TM + i) * 16, kk);
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[i][j] = mfma<DT>(a, b[j], acc[i][j]);
+            }
+        }
+        at = at + 1 == STAGES ? 0 : at + 1;
+        to = to + 1 == STAGES ? 0 : to + 1;
+    }
+
+    // acc[i][j][r] is D at m = m0 + 16 i + r, n = n0 + 16 j
+    const int64_t m0 = (int64_t)mt * BM + wm * TM * 16 + lane / 16 * 4;
+    const int64_t n0 = (int64_t)nt * BN + wn * TN * 16 + lane % 16;
+    if constexpr (EPI == E_STATS) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int64_t t = n0 + j * 16;
+            const int32_t label = t < p.tokens ? token_at(p.labels, p.id_bytes, t, p.vocab) : -1;
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int64_t v = p.v0 + m0 + i * 16 + r;
+                    if (v < p.vocab) top = fmaxf(top, acc[i][j][r]);
+                    if (v == label) p.target[t] = acc[i][j][r];
+                }
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (p.v0 + m0 + i * 16 + r < p.vocab) sum += exp_of(acc[i][j][r] - top);
+            // the four lane groups hold other rows of the same column
+#pragma unroll
+            for (int d = 16; d < 64; d <<= 1) {
+                const float top2 = __shfl_xor(top, d), sum2 = __shfl_xor(sum, d);
+                const float big = fmaxf(top, top2);
+                sum = (sum == 0.f ? 0.f : sum * exp_of(top - big)) + (sum2 == 0.f ? 0.f : sum2 * exp_of(top2 - big));
+                top = big;
+            }
+            if (lane < 16 && t < p.tokens)
+                p.stats[((p.v0 / BM + mt) * WM + wm) * p.tokens + t] = make_float2(top, sum);
+        }
+    } else if constexpr (EPI == E_GRAD) {
+        const float mul = p.mul[0];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int64_t t = n0 + j * 16;
+            if (t >= p.tokens) continue;
+            const int32_t label = token_at(p.labels, p.id_bytes, t, p.vocab);
+            const float lse = p.lse[t], weight = label < 0 ? 0.f : (p.grad ? p.grad[t] : 1.f) * mul;
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const int64_t v = p.v0 + m0 + i * 16;
+                u16x4 h;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float g = exp_of(acc[i][j][r] - lse) - (v + r == label ? 1.f : 0.f);
+                    h[r] = label >= 0 && v + r < p.vocab ? narrow16<DT>(g * weight) : (uint16_t)0;
+                }
+                if (v - p.v0 < p.ldg) *reinterpret_cast<u16x4*>(p.g + t * p.ldg + (v - p.v0)) = h;
+            }
+        }
+    } else if constexpr (EPI == E_DX) {
+        const float mul = p.mul[1];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int64_t t = n0 + j * 16;
+            if (t >= p.tokens) continue;
+            float* s = p.sum + ((int64_t)split * p.tokens + t) * p.lds;
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const int64_t h = m0 + i * 16;
+                if (h >= p.width) continue;
+                f32x4 f = acc[i][j];
+                if (p.sum_in) f += *reinterpret_cast<const f32x4*>(s + h);
+                if (p.sum_out) *reinterpret_cast<f32x4*>(s + h) = f;
+                else put4<DT>(p.out + t * p.ldo, h, p.width, f * mul, false);
+            }
+        }
+    } else {
+        const float mul = p.mul[1];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int64_t v = p.v0 + n0 + j * 16;
+            if (v >= p.vocab) continue;
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const int64_t h = m0 + i * 16;
+                if (h < p.width) put4<DT>(p.out + v * p.ldo, h, p.width, acc[i][j] * mul, p.accumulate);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------ small kernels --
+// Join the parts of a token's softmax: 64 tokens of a workgroup, its waves
+// share the parts.
+constexpr int kJoinWaves = 16;
+__global__ __launch_bounds__(kJoinWaves * 64) void stats_kernel(const float2* stats, const float* target,
+                                                                const void* labels, int32_t id_bytes,
+                                                                int64_t tokens, int64_t vocab, int32_t parts,
+                                                                float* loss, float* lse) {
+    __shared__ float2 part[kJoinWaves][64];
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int64_t t = (int64_t)blockIdx.x * 64 + lane;
+    float top = -INFINITY, sum = 0.f;
+    if (t < tokens) {
+#pragma unroll 4
+        for (int i = wave; i < parts; i += kJoinWaves) {
+            const float2 s = stats[(int64_t)i * tokens + t];
+            const float big = fmaxf(top, s.x);
+            sum = (sum == 0.f ? 0.f : sum * exp_of(top - big)) + (s.y == 0.f ? 0.f : s.y * exp_of(s.x - big));
+            top = big;
+        }
+    }
+    part[wave][lane] = make_float2(top, sum);
+    __syncthreads();
+    if (wave != 0 || t >= tokens) return;
+    for (int w = 1; w < kJoinWaves; ++w) top = fmaxf(top, part[w][lane].x);
+    sum = 0.f;
+    for (int w = 0; w < kJoinWaves; ++w) {
+        const float2 s = part[w][lane];
+        if (s.y != 0.f) sum += s.y * exp_of(s.x - top);
+    }
+    const float l = top + logf(sum);
+    lse[t] = l;
+    loss[t] = token_at(labels, id_bytes, t, vocab) < 0 ? 0.f : l - target[t];
+}
+
+constexpr int kMeanThreads = 1024;
+__global__ __launch_bounds__(kMeanThreads) void mean_kernel(const float* loss, const void* labels,
+                                                            int32_t id_bytes, int64_t tokens,
+                                                            int64_t vocab, float* summary) {
+    double sum = 0, count = 0;
+    for (int64_t t = threadIdx.x; t < tokens; t += kMeanThreads) {
+        sum += loss[t];
+        count += token_at(labels, id_bytes, t, vocab) >= 0 ? 1.0 : 0.0;
+    }
+    sum = block_sum<kMeanThreads>(sum);
+    __syncthreads();
+    count = block_sum<kMeanThreads>(count);
+    if (threadIdx.x == 0) {
+        summary[0] = count > 0 ? (float)(sum / count) : 0.f;
+        summary[1] = count > 0 ? (float)(1.0 / count) : 0.f;
+        summary[2] = (float)count;
+    }
+}
+
+// mul[0]: what G is multiplied by before it is rounded to 16 bits, a power of
+// two; mul[1] = scale / mul[0].  fp16 keeps 10 bits down to 2^-14 only, and most
+// probabilities of a large vocabulary are below that, so there G is moved up to
+// just below fp16's largest value: |G| <= max |grad|, which lands in [2^14, 2^15).
+constexpr int kMulThreads = 1024;
+__global__ __launch_bounds__(kMulThreads) void mul_kernel(const float* grad, int64_t tokens, int32_t fp16,
+                                                          const float* scale, float* mul) {
+    __shared__ float part[kMulThreads / 64];
+    float top = grad ? 0.f : 1.f;
+    if (grad && fp16) {
+        for (int64_t t = threadIdx.x; t < tokens; t += kMulThreads) {
+            const float g = fabsf(grad[t]);
+            if (g < INFINITY) top = fmaxf(top, g);
+        }
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+        if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = top;
+        __syncthreads();
+        for (int i = 0; i < kMulThreads / 64; ++i) top = fmaxf(top, part[i]);
+    }
+    if (threadIdx.x != 0) return;
+    // an exponent that neither factor can leave fp32 with
+    int e = 0;
+    if (fp16) e = max(-60, min(60, top > 0.f ? 14 - ilogbf(top) : 0));
+    mul[0] = ldexpf(1.f, e);
+    mul[1] = ldexpf(scale ? *scale : 1.f, -e);
+}
+
+// Rows of any length, stride and alignment to rows of a multiple of 8 elements,
+// zero-filled: what the products' 16-byte loads need.
+__global__ __launch_bounds__(256) void pack_kernel(const uint16_t* src, int64_t stride, int64_t rows,
+                                                   int64_t width, uint16_t* dst, int64_t ld) {
+    const int64_t vecs = ld / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t row = i / vecs, j = (i - row * vecs) * 8;
+    if (row >= rows) return;
+    u16x8 h = 0;
+    if (j + 8 <= width) {
+        h = *reinterpret_cast<const u16x8_any*>(src + row * stride + j);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (j + k < width) h[k] = src[row * stride + j + k];
+    }
+    *reinterpret_cast<u16x8*>(dst + row * ld + j) = h;
+}
+
+// dx = rne16(mul * sum over the splits, in order)
+template <int DT>
+__global__ __launch_bounds__(256) void splits_kernel(const float* sum, int64_t lds, int32_t splits,
+                                                     int64_t tokens, int64_t width, const float* mul,
+                                                     uint16_t* out, int64_t ldo) {
+    const int64_t vecs = lds / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t t = i / vecs, h = (i - t * vecs) * 4;
+    if (t >= tokens) return;
+    f32x4 f = 0.f;
+    for (int s = 0; s < splits; ++s) f += *reinterpret_cast<const f32x4*>(sum + ((int64_t)s * tokens + t) * lds + h);
+    put4<DT>(out + t * ldo, h, width, f * mul[1], false);
+}
+
+// --------------------------------------------------------------------- host --
+int64_t ceil_to(int64_t n, int64_t k) { return (n + k - 1) / k * k; }
+int64_t tiles_of(int64_t n, int64_t k) { return (n + k - 1) / k; }
+
+// Tokens of a tile: as few as hold all of them, at most 256.
+int token_tile(int64_t tokens) { return tokens <= 64 ? 64 : tokens <= 128 ? 128 : 256; }
+int vocab_waves(int64_t tokens) { return tokens <= 64 ? 8 : tokens <= 128 ? 4 : 2; }
+
+// The vocabulary's pieces: G of one takes about 512 MB at most.
+int64_t piece_of(int64_t tokens, int64_t vocab) {
+    const int64_t most = std::max<int64_t>(BM, (int64_t(1) << 28) / std::max<int64_t>(tokens, 1) / BM * BM);
+    const int64_t pieces = tiles_of(vocab, most);
+    return ceil_to(tiles_of(vocab, pieces), BM);
+}
+// k splits of the dx product: enough to give every CU a tile.
+int splits_of(int64_t tokens, int64_t width, int64_t piece) {
+    const int64_t tiles = tiles_of(width, BM) * tiles_of(std::max<int64_t>(tokens, 1), token_tile(tokens));
+    const int64_t want = 512 / tiles, most = piece / 1024;
+    return (int)std::max<int64_t>(1, std::min(want, most));
+}
+
+struct Space {
+    float2* stats;
+    float *target, *mul, *sum;
+    uint16_t *x, *w, *g;
+    int64_t bytes;
+};
+Space space_of(char* ws, int64_t tokens, int64_t vocab, int64_t width, bool backward) {
+    Space s{};
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        char* p = ws + at;
+        at += ceil_to(bytes, 256);
+        return p;
+    };
+    const int64_t piece = piece_of(tokens, vocab), packed = ceil_to(width, 8);
+    s.stats = reinterpret_cast<float2*>(take(tiles_of(vocab, BM) * vocab_waves(tokens) * tokens * 8));
+    s.target = reinterpret_cast<float*>(take(tokens * 4));
+    s.x = reinterpret_cast<uint16_t*>(take(tokens * packed * 2));
+    s.w = reinterpret_cast<uint16_t*>(take(piece * packed * 2));
+    if (backward) {
+        s.mul = reinterpret_cast<float*>(take(8));
+        s.g = reinterpret_cast<uint16_t*>(take(tokens * piece * 2));
+        s.sum = reinterpret_cast<float*>(take(tokens * ceil_to(width, 4) * 4 * splits_of(tokens, width, piece)));
+    }
+    s.bytes = at;
+    return s;
+}
+
+template <int DT, int EPI>
+void launch_product(const Product& p, int bn, hipStream_t stream) {
+    const unsigned grid = (unsigned)(p.m_tiles * p.n_tiles * p.splits);
+    if constexpr (EPI == E_DW) {
+        product_kernel<DT, EPI, 256, 2, 2><<<grid, kThreads, 0, stream>>>(p);
+    } else {
+        if (bn == 64) product_kernel<DT, EPI, 64, 8, 3><<<grid, kThreads, 0, stream>>>(p);
+        else if (bn == 128) product_kernel<DT, EPI, 128, 4, 3><<<grid, kThreads, 0, stream>>>(p);
+        else product_kernel<DT, EPI, 256, 2, 2><<<grid, kThreads, 0, stream>>>(p);
+    }
+}
+
+bool loads16(const uint16_t* p, int64_t stride, int64_t width) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0 && width % 8 == 0;
+}
+void pack(const uint16_t* src, int64_t stride, int64_t rows, int64_t width, uint16_t* dst, int64_t ld,
+          hipStream_t stream) {
+    if (!rows) return;
+    pack_kernel<<<(unsigned)tiles_of(rows * (ld / 8), 256), 256, 0, stream>>>(src, stride, rows, width, dst, ld);
+}
+
+// The operands of the products over the vocabulary from v0 on.  Operands that
+// 16-byte loads cannot read are packed first: x once, w piece by piece.
+struct Operands {
+    Mat x, w;
+};
+void pack_x(const XentArgs& a, const Space& s, Operands* o, hipStream_t stream) {
+    o->x = Mat{a.x, a.x_stride, a.tokens, a.width};
+    if (loads16(a.x, a.x_stride, a.width)) return;
+    const int64_t ld = ceil_to(a.width, 8);
+    pack(a.x, a.x_stride, a.tokens, a.width, s.x, ld, stream);
+    o->x = Mat{s.x, ld, a.tokens, ld};
+}
+void pack_w(const XentArgs& a, const Space& s, int64_t v0, int64_t rows, Operands* o, hipStream_t stream) {
+    o->w = Mat{a.w + v0 * a.w_stride, a.w_stride, rows, a.width};
+    if (loads16(a.w, a.w_stride, a.width)) return;
+    const int64_t ld = ceil_to(a.width, 8);
+    pack(a.w + v0 * a.w_stride, a.w_stride, rows, a.width, s.w, ld, stream);
+    o->w = Mat{s.w, ld, rows, ld};
+}
+
+Product logits_of(const XentArgs& a, const Operands& o, int64_t v0, int bn) {
+    Product p{};
+    p.a = o.w;
+    p.b = o.x;
+    p.k = std::min(o.w.cols, o.x.cols);
+    p.a.cols = p.b.cols = p.k;
+    p.m_tiles = (int32_t)tiles_of(o.w.rows, BM);
+    p.n_tiles = (int32_t)tiles_of(a.tokens, bn);
+    p.splits = 1;
+    p.k_split = (int32_t)ceil_to(p.k, BK);
+    p.v0 = v0;
+    p.vocab = a.vocab;
+    p.tokens = a.tokens;
+    p.width = a.width;
+    p.labels = a.labels;
+    p.id_bytes = a.id_bytes;
+    return p;
+}
+
+template <int DT>
+hipError_t forward(const XentArgs& a, void* ws, hipStream_t stream) {
+    const Space s = space_of(static_cast<char*>(ws), a.tokens, a.vocab, a.width, false);
+    const int bn = token_tile(a.tokens);
+    if (a.tokens) {
+        Operands o;
+        pack_x(a, s, &o, stream);
+        const int64_t piece = loads16(a.w, a.w_stride, a.width) ? a.vocab : piece_of(a.tokens, a.vocab);
+        for (int64_t v0 = 0; v0 < a.vocab; v0 += piece) {
+            pack_w(a, s, v0, std::min(piece, a.vocab - v0), &o, stream);
+            Product p = logits_of(a, o, v0, bn);
+            p.stats = s.stats;
+            p.target = s.target;
+            launch_product<DT, E_STATS>(p, bn, stream);
+        }
+        const int32_t parts = (int32_t)tiles_of(a.vocab, BM) * vocab_waves(a.tokens);
+        stats_kernel<<<(unsigned)tiles_of(a.tokens, 64), kJoinWaves * 64, 0, stream>>>(
+            s.stats, s.target, a.labels, a.id_bytes, a.tokens, a.vocab, parts, a.loss, a.lse);
+    }
+    mean_kernel<<<1, kMeanThreads, 0, stream>>>(a.loss, a.labels, a.id_bytes, a.tokens, a.vocab, a.summary);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t backward(const XentArgs& a, void* ws, hipStream_t stream) {
+    const Space s = space_of(static_cast<char*>(ws), a.tokens, a.vocab, a.width, true);
+    const int bn = token_tile(a.tokens);
+    const int64_t piece = piece_of(a.tokens, a.vocab);
+    const int splits = splits_of(a.tokens, a.width, piece);
+    mul_kernel<<<1, kMulThreads, 0, stream>>>(a.grad, a.tokens, DT == ZSMR_FP16, a.scale, s.mul);
+    Operands o;
+    pack_x(a, s, &o, stream);
+    for (int64_t v0 = 0; v0 < a.vocab; v0 += piece) {
+        const int64_t rows = std::min(piece, a.vocab - v0);
+        if (a.tokens) pack_w(a, s, v0, rows, &o, stream);
+        else o.w = Mat{a.w, a.w_stride, rows, a.width};     // no token: dw is zero, nothing is read
+        Product p = logits_of(a, o, v0, bn);
+        p.lse = a.lse;
+        p.grad = a.grad;
+        p.mul = s.mul;
+        p.g = s.g;
+        p.ldg = piece;
+        if (a.tokens) launch_product<DT, E_GRAD>(p, bn, stream);
+        const int64_t padded = ceil_to(rows, 8);        // G is zero past the vocabulary
+        if (a.dx && a.tokens) {
+            Product d = p;
+            d.a = o.w;
+            d.b = Mat{s.g, piece, a.tokens, padded};
+            d.k = padded;
+            d.m_tiles = (int32_t)tiles_of(a.width, BM);
+            d.splits = splits;
+            d.k_split = (int32_t)ceil_to(tiles_of(padded, splits), BK);
+            d.sum = s.sum;
+            d.lds = ceil_to(a.width, 4);
+            d.sum_in = v0 > 0;
+            d.sum_out = splits > 1 || v0 + piece < a.vocab;
+            d.out = a.dx;
+            d.ldo = a.dx_stride;
+            launch_product<DT, E_DX>(d, bn, stream);
+        }
+        if (a.dw) {
+            Product d = p;
+            d.a = o.x;
+            d.b = Mat{s.g, piece, a.tokens, padded};
+            d.k = a.tokens;
+            d.m_tiles = (int32_t)tiles_of(a.width, BM);
+            d.n_tiles = (int32_t)tiles_of(rows, 256);
+            d.k_split = (int32_t)ceil_to(a.tokens, BK);
+            d.out = a.dw;
+            d.ldo = a.dw_stride;
+            d.accumulate = a.accumulate;
+            launch_product<DT, E_DW>(d, 256, stream);
+        }
+    }
+    if (a.dx && a.tokens && splits > 1) {
+        const int64_t lds = ceil_to(a.width, 4);
+        splits_kernel<DT><<<(unsigned)tiles_of(a.tokens * (lds / 4), 256), 256, 0, stream>>>(
+            s.sum, lds, splits, a.tokens, a.width, s.mul, a.dx, a.dx_stride);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t xent_bytes(int64_t tokens, int64_t vocab, int64_t width, bool backward) {
+    return space_of(nullptr, tokens, vocab, width, backward).bytes;
+}
+
+hipError_t launch_xent_forward(const XentArgs& a, void* ws, hipStream_t stream) {
+    return a.dtype == ZSMR_BF16 ? forward<ZSMR_BF16>(a, ws, stream) : forward<ZSMR_FP16>(a, ws, stream);
+}
+hipError_t launch_xent_backward(const XentArgs& a, void* ws, hipStream_t stream) {
+    return a.dtype == ZSMR_BF16 ? backward<ZSMR_BF16>(a, ws, stream) : backward<ZSMR_FP16>(a, ws, stream);
+}
+
+}  // namespace zsmr
