@@ -74,18 +74,26 @@ __device__ __forceinline__ uint32_t sort_key(const SortArgs& a, int64_t i) {
 }
 template <bool FIRST>
 __global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a) {
-    __shared__ uint32_t total[kBins], before[kBins], cnt[kSortWaves][kBins];
+    __shared__ uint32_t hist[2][kBins], cnt[kSortWaves][kBins];     // hist: keys before this part; the others
     const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
-    for (int i = tid; i < kBins; i += kSortThreads) total[i] = before[i] = 0;
+    for (int i = tid; i < 2 * kBins; i += kSortThreads) (&hist[0][0])[i] = 0;
     for (int i = tid; i < kSortWaves * kBins; i += kSortThreads) (&cnt[0][0])[i] = 0;
     __syncthreads();
     const int64_t b0 = (int64_t)blockIdx.x * a.part;
     const int64_t b1 = b0 + a.part < a.tokens ? b0 + a.part : a.tokens;
-#pragma unroll 4
-    for (int64_t i = tid; i < a.tokens; i += kSortThreads) {
-        const uint32_t d = (sort_key<FIRST>(a, i) >> a.shift) & (kBins - 1);
-        atomicAdd(&total[d], 1u);
-        if (i < b0) atomicAdd(&before[d], 1u);
+    constexpr int kAhead = 16;
+    for (int64_t i0 = tid; i0 < a.tokens; i0 += kSortThreads * kAhead) {
+        uint32_t key[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t i = i0 + k * kSortThreads;
+            key[k] = sort_key<FIRST>(a, i < a.tokens ? i : a.tokens - 1);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t i = i0 + k * kSortThreads;
+            if (i < a.tokens) atomicAdd(&hist[i >= b0][(key[k] >> a.shift) & (kBins - 1)], 1u);
+        }
     }
     // this workgroup's keys, a contiguous run for each wave
     const int64_t run = (b1 - b0 + kSortThreads - 1) / kSortThreads * 64;
@@ -97,7 +105,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a) {
     __shared__ uint32_t wsum[kBins / 64];
     uint32_t mine = 0, incl = 0;
     if (tid < kBins) {
-        mine = incl = total[tid];
+        mine = incl = hist[0][tid] + hist[1][tid];
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const uint32_t up = __shfl_up(incl, d);
@@ -107,7 +115,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a) {
     }
     __syncthreads();
     if (tid < kBins) {
-        uint32_t at = incl - mine + before[tid];
+        uint32_t at = incl - mine + hist[0][tid];
         for (int w = 0; w < wave; ++w) at += wsum[w];
 #pragma unroll
         for (int w = 0; w < kSortWaves; ++w) {
@@ -142,7 +150,6 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a) {
 }
 
 // --------------------------------------------------------------- gradient --
-constexpr int kSorted = 64;         // sorted tokens of a chunk: one to a lane
 constexpr int kCols = 512;          // columns of a wave: eight to a lane
 constexpr int kBlockCols = kThreads / 64 * kCols;
 
@@ -179,16 +186,43 @@ __device__ __forceinline__ f32x8 get_row(const void* p, int64_t j, int64_t width
     return f;
 }
 
+// Zeros in the rows of absent tokens, kZeroRows to a workgroup.
+constexpr int kZeroRows = 16;
+__device__ __forceinline__ void zero_rows(const EmbedArgs& a, const uint32_t* key, int64_t v0) {
+    __shared__ int present[kZeroRows];
+    // 16 lanes a row narrow down its place among the sorted keys 17 ways a step
+    const int lane = threadIdx.x % 16, group = threadIdx.x % 64 / 16;
+    const uint32_t v = (uint32_t)v0 + threadIdx.x / 16;
+    int64_t lo = 0, hi = a.tokens;
+    while (lo < hi) {
+        const int64_t n = hi - lo, at = lo + n * (lane + 1) / 17;
+        const int below = __popc((uint32_t)(__ballot(key[at] < v) >> (group * 16)) & 0xffff);
+        const int64_t last = lo + n * below / 17;       // the highest pivot below v
+        if (below < 16) hi = lo + n * (below + 1) / 17;
+        if (below > 0) lo = last + 1;
+    }
+    if (lane == 0) present[threadIdx.x / 16] = lo < a.tokens && key[lo] == v;
+    __syncthreads();
+    for (int r = 0; r < kZeroRows && v0 + r < a.vocab; ++r) {
+        if (present[r]) continue;
+        uint16_t* row = a.dst + (v0 + r) * a.dst_stride;
+        for (int64_t j = threadIdx.x * 8; j < a.width; j += kThreads * 8) {
+            if (j + 8 <= a.width) __builtin_nontemporal_store(u16x8(0), reinterpret_cast<u16x8_any*>(row + j));
+            else for (int64_t k = j; k < a.width; ++k) row[k] = 0;
+        }
+    }
+}
+
+// The runs of one chunk of sorted tokens in one column block.
 // part[chunk][0]: the sum of a run that came from the chunk before; [1]: of one
 // that starts here and goes on.
 template <int DT>
-__global__ __launch_bounds__(kThreads) void runs_kernel(EmbedArgs a, const uint32_t* key,
-                                                        const uint32_t* pos, float* part) {
+__device__ __forceinline__ void add_runs(const EmbedArgs& a, const uint32_t* key, const uint32_t* pos,
+                                         float* part, int64_t c, int chunk, int64_t j) {
     const int lane = threadIdx.x % 64;
-    const int64_t j = (int64_t)blockIdx.y * kBlockCols + threadIdx.x * 8;
     if (j - lane * 8 >= a.width) return;
-    const int64_t c = blockIdx.x, i0 = c * kSorted;
-    const int n = (int)(a.tokens - i0 < kSorted ? a.tokens - i0 : kSorted);
+    const int64_t i0 = c * chunk;
+    const int n = (int)(a.tokens - i0 < chunk ? a.tokens - i0 : chunk);
     const uint32_t none = (uint32_t)a.vocab;
     const uint32_t my_key = lane < n ? key[i0 + lane] : none;
     const uint32_t my_pos = lane < n ? pos[i0 + lane] : 0;
@@ -223,68 +257,65 @@ __global__ __launch_bounds__(kThreads) void runs_kernel(EmbedArgs a, const uint3
     }
 }
 
+// The first workgroups add up runs, the others write zeros meanwhile.
+template <int DT>
+__global__ __launch_bounds__(kThreads) void grad_kernel(EmbedArgs a, const uint32_t* key, const uint32_t* pos,
+                                                        float* part, int chunk, int64_t chunks, int col_blocks) {
+    const int64_t b = blockIdx.x, runs = chunks * col_blocks;
+    if (b < runs) add_runs<DT>(a, key, pos, part, b / col_blocks, chunk, b % col_blocks * kBlockCols + threadIdx.x * 8);
+    else zero_rows(a, key, (b - runs) * kZeroRows);
+}
+
 // One workgroup for each chunk whose last run starts in it and goes on.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void join_runs_kernel(EmbedArgs a, const uint32_t* key,
-                                                             const float* part) {
-    const int64_t c = blockIdx.x, last = c * kSorted + kSorted - 1;
+                                                             const float* part, int chunk) {
+    const int64_t c = blockIdx.x, last = c * chunk + chunk - 1;
     if (last + 1 >= a.tokens) return;
     const uint32_t v = key[last];
     if (v == (uint32_t)a.vocab || key[last + 1] != v) return;
-    if (c > 0 && key[c * kSorted - 1] == v) return;       // it started before this chunk
+    if (c > 0 && key[c * chunk - 1] == v) return;         // it started before this chunk
     int64_t lo = last + 1, hi = a.tokens;                 // the run's end
     while (lo < hi) {
         const int64_t mid = (lo + hi) / 2;
         if (key[mid] == v) lo = mid + 1;
         else hi = mid;
     }
-    const int64_t end = (lo - 1) / kSorted;
+    const int64_t end = (lo - 1) / chunk;
     const int64_t j = (int64_t)blockIdx.y * kBlockCols + threadIdx.x * 8;
     if (j >= a.width) return;
     f32x8 sum = get_row<ZSMR_FP32>(part + (2 * c + 1) * a.width, j, a.width);
-#pragma unroll 4
-    for (int64_t k = c + 1; k <= end; ++k) sum += get_row<ZSMR_FP32>(part + 2 * k * a.width, j, a.width);
+    constexpr int kAhead = 8;
+    for (int64_t k = c + 1; k <= end; k += kAhead) {
+        f32x8 f[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (k + i <= end) f[i] = get_row<ZSMR_FP32>(part + 2 * (k + i) * a.width, j, a.width);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (k + i <= end) sum += f[i];
+    }
     put_row<DT>(a, v, j, sum);
 }
 
-// Zeros in the rows of absent tokens.
-constexpr int kZeroRows = 16;
-__global__ __launch_bounds__(kThreads) void zero_rows_kernel(EmbedArgs a, const uint32_t* key) {
-    __shared__ int present[kZeroRows];
-    const int64_t v0 = (int64_t)blockIdx.x * kZeroRows;
-    if (threadIdx.x < kZeroRows) {
-        const uint32_t v = (uint32_t)(v0 + threadIdx.x);
-        int64_t lo = 0, hi = a.tokens;
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) / 2;
-            if (key[mid] < v) lo = mid + 1;
-            else hi = mid;
-        }
-        present[threadIdx.x] = lo < a.tokens && key[lo] == v;
-    }
-    __syncthreads();
-    for (int r = 0; r < kZeroRows && v0 + r < a.vocab; ++r) {
-        if (present[r]) continue;
-        uint16_t* row = a.dst + (v0 + r) * a.dst_stride;
-        for (int64_t j = threadIdx.x * 8; j < a.width; j += kThreads * 8) {
-            if (j + 8 <= a.width) *reinterpret_cast<u16x8_any*>(row + j) = u16x8(0);
-            else for (int64_t k = j; k < a.width; ++k) row[k] = 0;
-        }
-    }
-}
-
 int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
-int64_t chunks_of(int64_t tokens) { return (tokens + kSorted - 1) / kSorted; }
+int64_t col_blocks_of(int64_t width) { return (width + kBlockCols - 1) / kBlockCols; }
+// Sorted tokens of a chunk: a wave reads them one after another, so a few
+// tokens go to shorter chunks until there are about 2,048 waves.
+int chunk_of(int64_t tokens, int64_t width) {
+    int chunk = 64;
+    while (chunk > 8 && (tokens / chunk) * ((width + kCols - 1) / kCols) < 2048) chunk /= 2;
+    return chunk;
+}
 
 template <int DT>
 void grad_launches(const EmbedArgs& a, const uint32_t* key, const uint32_t* pos, float* part,
                    hipStream_t stream) {
-    if (!a.accumulate)
-        zero_rows_kernel<<<(unsigned)((a.vocab + kZeroRows - 1) / kZeroRows), kThreads, 0, stream>>>(a, key);
-    if (!a.tokens) return;
-    const dim3 grid((unsigned)chunks_of(a.tokens), (unsigned)((a.width + kBlockCols - 1) / kBlockCols));
-    runs_kernel<DT><<<grid, kThreads, 0, stream>>>(a, key, pos, part);
-    if (grid.x > 1) join_runs_kernel<DT><<<grid, kThreads, 0, stream>>>(a, key, part);
+    const int chunk = chunk_of(a.tokens, a.width), cols = (int)col_blocks_of(a.width);
+    const int64_t chunks = (a.tokens + chunk - 1) / chunk;
+    const int64_t zeros = a.accumulate ? 0 : (a.vocab + kZeroRows - 1) / kZeroRows;
+    grad_kernel<DT><<<(unsigned)(chunks * cols + zeros), kThreads, 0, stream>>>(a, key, pos, part, chunk, chunks, cols);
+    if (chunks > 1) join_runs_kernel<DT><<<dim3((unsigned)chunks, cols), kThreads, 0, stream>>>(a, key, part, chunk);
 }
 
 }  // namespace
@@ -297,7 +328,8 @@ hipError_t launch_embed_lookup(const EmbedArgs& a, hipStream_t stream) {
 }
 
 int64_t embed_grad_bytes(int64_t, int64_t width, int64_t tokens) {
-    return 4 * up16(tokens * 4) + chunks_of(tokens) * 2 * width * 4;
+    const int chunk = chunk_of(tokens, width);
+    return 4 * up16(tokens * 4) + (tokens + chunk - 1) / chunk * 2 * width * 4;
 }
 
 hipError_t launch_embed_grad(const EmbedArgs& a, void* ws, hipStream_t stream) {

@@ -10,6 +10,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "zsmr_dev.h"
 #include "zsmr_ops_launch.h"
 
@@ -19,6 +21,7 @@ namespace zsmr {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kSumsqGrid = 2048;
 
 // The item whose chunks hold chunk b (uniform over the workgroup).
 template <typename A>
@@ -53,17 +56,20 @@ __device__ __forceinline__ double chunk_sumsq(const void* p, int64_t e0, int64_t
     return s0 + s1;
 }
 
+// A workgroup takes every gridDim.x-th chunk and leaves one sum.
 __global__ __launch_bounds__(kThreads) void sumsq_kernel(NormArgs a, double* partial) {
-    const int b = blockIdx.x, k = item_of(a, b);
-    const void* p = a.it[k].p;
-    const int64_t e0 = (int64_t)(b - a.it[k].chunk0) * kChunk, n = a.it[k].n;
-    const int64_t e1 = e0 + kChunk < n ? e0 + kChunk : n;
-    double s;
-    if (a.it[k].dtype == ZSMR_FP32) s = chunk_sumsq<ZSMR_FP32>(p, e0, e1);
-    else if (a.it[k].dtype == ZSMR_BF16) s = chunk_sumsq<ZSMR_BF16>(p, e0, e1);
-    else s = chunk_sumsq<ZSMR_FP16>(p, e0, e1);
+    double s = 0;
+    for (int b = blockIdx.x; b < a.chunks; b += gridDim.x) {
+        const int k = item_of(a, b);
+        const void* p = a.it[k].p;
+        const int64_t e0 = (int64_t)(b - a.it[k].chunk0) * kChunk, n = a.it[k].n;
+        const int64_t e1 = e0 + kChunk < n ? e0 + kChunk : n;
+        if (a.it[k].dtype == ZSMR_FP32) s += chunk_sumsq<ZSMR_FP32>(p, e0, e1);
+        else if (a.it[k].dtype == ZSMR_BF16) s += chunk_sumsq<ZSMR_BF16>(p, e0, e1);
+        else s += chunk_sumsq<ZSMR_FP16>(p, e0, e1);
+    }
     s = block_sum<kThreads>(s);
-    if (threadIdx.x == 0) partial[b] = s;
+    if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
 constexpr int kJoinThreads = 1024;
@@ -104,7 +110,9 @@ __device__ __forceinline__ void chunk_zero(const ClipItem& t, int64_t e0, int64_
 __global__ __launch_bounds__(kThreads) void clip_kernel(ClipArgs a) {
     const float c = a.coef ? *a.coef : 1.0f;
     if (a.in_place && c == 1.0f) return;
-    const int b = blockIdx.x;
+    // from the end: the norm's pass read the list from its start, so what the
+    // Infinity Cache still holds is its end
+    const int b = a.chunks - 1 - (int)blockIdx.x;
     const ClipItem t = a.it[item_of(a, b)];
     const int64_t e0 = (int64_t)(b - t.chunk0) * kChunk;
     const int64_t e1 = e0 + kChunk < t.n ? e0 + kChunk : t.n;
@@ -130,39 +138,46 @@ __device__ __forceinline__ float mean_of(const StepArgs& a, float sum) {
     return a.inv_pow2 ? sum * a.inv_nf : sum / a.nf;
 }
 
-// One lane's eight elements: rows summed in fp32 strictly in rank order, kRows
-// loads in flight.
+// The sum of rows [0, nrows) at one lane's eight elements, in fp32 strictly in
+// rank order, kRows loads in flight.
 constexpr int kRows = 8;
 template <int DT>
-__global__ __launch_bounds__(kThreads) void reduce_sumsq_kernel(StepArgs a, double* partial) {
-    const int64_t e = (int64_t)blockIdx.x * kTile + threadIdx.x * 8;
+__device__ __forceinline__ f32x8 sum_rows(const StepArgs& a, int64_t e) {
+    const uint16_t* p = a.grads + e;
+    // -0 + x is x for every x, so the sum starts at row 0 with its own bits
+    f32x8 g = -0.0f;
+    int r = 0;
+    for (; r + kRows <= a.nrows; r += kRows) {
+        u16x8 h[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k)
+            h[k] = __builtin_nontemporal_load(reinterpret_cast<const u16x8_any*>(p + (int64_t)(r + k) * a.row_stride));
+#pragma unroll
+        for (int k = 0; k < kRows; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] += widen16<DT>(h[k][i]);
+    }
+    for (; r < a.nrows; ++r) {
+        const u16x8 h = *reinterpret_cast<const u16x8_any*>(p + (int64_t)r * a.row_stride);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] += widen16<DT>(h[i]);
+    }
+    return g;
+}
+// The mean and the squares of a lane's eight elements.
+__device__ __forceinline__ f32x8 mean_sumsq(const StepArgs& a, f32x8 g, double* s) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        g[i] = mean_of(a, g[i]);
+        *s = __builtin_fma((double)g[i], (double)g[i], *s);
+    }
+    return g;
+}
+template <int DT>
+__device__ __forceinline__ double reduce_some(const StepArgs& a, int64_t e) {
     double s = 0;
     if (e + 8 <= a.n) {
-        const uint16_t* p = a.grads + e;
-        // -0 + x is x for every x, so the sum starts at row 0 with its own bits
-        f32x8 g = -0.0f;
-        int r = 0;
-        for (; r + kRows <= a.nrows; r += kRows) {
-            u16x8 h[kRows];
-#pragma unroll
-            for (int k = 0; k < kRows; ++k)
-                h[k] = __builtin_nontemporal_load(reinterpret_cast<const u16x8_any*>(p + (int64_t)(r + k) * a.row_stride));
-#pragma unroll
-            for (int k = 0; k < kRows; ++k)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) g[i] += widen16<DT>(h[k][i]);
-        }
-        for (; r < a.nrows; ++r) {
-            const u16x8 h = *reinterpret_cast<const u16x8_any*>(p + (int64_t)r * a.row_stride);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] += widen16<DT>(h[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            g[i] = mean_of(a, g[i]);
-            s = __builtin_fma((double)g[i], (double)g[i], s);
-        }
-        store8<ZSMR_FP32>(a.g_out, e, g);
+        store8<ZSMR_FP32>(a.g_out, e, mean_sumsq(a, sum_rows<DT>(a, e), &s));
     } else {
         for (int64_t j = e; j < a.n && j < e + 8; ++j) {
             float g = widen16<DT>(a.grads[j]);
@@ -172,6 +187,109 @@ __global__ __launch_bounds__(kThreads) void reduce_sumsq_kernel(StepArgs a, doub
             s = __builtin_fma((double)g, (double)g, s);
         }
     }
+    return s;
+}
+template <int DT>
+__global__ __launch_bounds__(kThreads) void reduce_sumsq_kernel(StepArgs a, double* partial) {
+    const double s = block_sum<kThreads>(reduce_some<DT>(a, (int64_t)blockIdx.x * kTile + threadIdx.x * 8));
+    if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+// A small piece in one workgroup, which leaves the whole sum: one launch
+// instead of two.
+constexpr int kSmall = 1024;
+template <int DT>
+__global__ __launch_bounds__(kSmall) void reduce_sumsq_small_kernel(StepArgs a, double* sumsq) {
+    double s = 0;
+    for (int64_t e = threadIdx.x * 8; e < a.n; e += kSmall * 8) s += reduce_some<DT>(a, e);
+    s = block_sum<kSmall>(s);
+    if (threadIdx.x == 0) *sumsq = s;
+}
+
+// Many rows of a large piece.  The g that is written is a thirtieth of the
+// bytes, but written as it comes it takes a seventh of the time: HBM loses far
+// more to turning between reads and writes than to the writes.  So a wave
+// keeps the sums of up to kRing tiles of 512 elements in LDS and stores them
+// in short windows that all waves of the chip take at the same time, read from
+// the constant-rate clock (100 MHz); no loads are issued in a window until
+// kLead before its end.  A ring that fills before its window is stored at once.
+// Measured on MI355X, 64 rows of 117,187,500: as they come 2.84-2.93 ms, no
+// writes at all 2.35, windows 2.54 (4 us in every 100; 60 us 2.55, 160 us 2.56;
+// windows of 8 us the same, 15 us 2.59-2.86; two workgroups a CU with half the
+// ring 2.61-2.85).
+constexpr int kRing = 18;
+constexpr uint32_t kCycle = 10000, kWindow = 400, kLead = 133;      // ticks of 10 ns
+constexpr int kWindowRows = 16;
+__device__ __forceinline__ void wait_clock(uint64_t t) {
+    for (int i = 0; i < (1 << 16); ++i) {           // bounded: a wave always goes on
+        if (__builtin_amdgcn_s_memrealtime() >= t) break;
+        __builtin_amdgcn_s_sleep(1);
+    }
+}
+template <int DT>
+__global__ __launch_bounds__(kThreads) void reduce_sumsq_windows_kernel(StepArgs a, double* partial) {
+    constexpr int kWaves = kThreads / 64;
+    __shared__ f32x4 ring[kWaves][kRing][2][64];    // a lane reads back only its own values
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int64_t tiles = a.n / 512, waves = (int64_t)gridDim.x * kWaves;
+    const int64_t me = (int64_t)blockIdx.x * kWaves + wave;
+    double s = 0;
+    int64_t done = 0, stored = 0;                   // tiles of this wave
+    uint64_t taken = ~0ull;                         // the cycle whose window was taken
+    auto flush = [&]() {
+        for (; stored < done; ++stored) {
+            const int64_t e = (me + stored * waves) * 512 + lane * 8;
+            const f32x4 lo = ring[wave][stored % kRing][0][lane], hi = ring[wave][stored % kRing][1][lane];
+            __builtin_nontemporal_store(lo, reinterpret_cast<f32x4_any*>(a.g_out + e));
+            __builtin_nontemporal_store(hi, reinterpret_cast<f32x4_any*>(a.g_out + e + 4));
+        }
+    };
+    for (int64_t tile = me; tile < tiles; tile += waves) {
+        const uint16_t* p = a.grads + tile * 512 + lane * 8;
+        f32x8 g = -0.0f;
+        u16x8 x[kRows], y[kRows];
+        auto load = [&](u16x8* h, int r) {
+#pragma unroll
+            for (int k = 0; k < kRows; ++k)
+                if (r + k < a.nrows)
+                    h[k] = __builtin_nontemporal_load(reinterpret_cast<const u16x8_any*>(p + (int64_t)(r + k) * a.row_stride));
+        };
+        auto add = [&](const u16x8* h, int r) {
+#pragma unroll
+            for (int k = 0; k < kRows; ++k)
+                if (r + k < a.nrows) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) g[i] += widen16<DT>(h[k][i]);
+                }
+        };
+        load(x, 0);
+        for (int r = 0; r < a.nrows; r += 2 * kRows) {
+            const uint64_t now = __builtin_amdgcn_s_memrealtime(), cycle = now / kCycle;
+            if (now - cycle * kCycle + kWindow >= kCycle && cycle != taken) {
+                flush();
+                taken = cycle;
+                wait_clock((cycle + 1) * kCycle - kLead);
+            }
+            load(y, r + kRows);
+            add(x, r);
+            load(x, r + 2 * kRows);
+            add(y, r + kRows);
+        }
+        g = mean_sumsq(a, g, &s);
+        if (done - stored == kRing) flush();
+        f32x4 lo, hi;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lo[i] = g[i];
+            hi[i] = g[4 + i];
+        }
+        ring[wave][done % kRing][0][lane] = lo;
+        ring[wave][done % kRing][1][lane] = hi;
+        ++done;
+    }
+    flush();
+    if (blockIdx.x == 0 && threadIdx.x * 8 < a.n - tiles * 512)     // the elements past the last tile
+        s += reduce_some<DT>(a, tiles * 512 + threadIdx.x * 8);
     s = block_sum<kThreads>(s);
     if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
@@ -197,10 +315,10 @@ __global__ __launch_bounds__(kThreads) void clipped_kernel(StepArgs a, const flo
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int64_t e = t0 + j * 256;
-            g[j] = *reinterpret_cast<const f32x4_any*>(a.g_in + e);
-            w[j] = *reinterpret_cast<const f32x4_any*>(a.master + e);
-            m[j] = *reinterpret_cast<const f32x4_any*>(a.m + e);
-            v[j] = *reinterpret_cast<const f32x4_any*>(a.v + e);
+            g[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_any*>(a.g_in + e));
+            w[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_any*>(a.master + e));
+            m[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_any*>(a.m + e));
+            v[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_any*>(a.v + e));
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -215,10 +333,10 @@ __global__ __launch_bounds__(kThreads) void clipped_kernel(StepArgs a, const flo
                 v[j][i] = vi;
                 h[i] = narrow16<DT>(wi);
             }
-            *reinterpret_cast<f32x4_any*>(a.master + e) = w[j];
-            *reinterpret_cast<f32x4_any*>(a.m + e) = m[j];
-            *reinterpret_cast<f32x4_any*>(a.v + e) = v[j];
-            *reinterpret_cast<u16x4_any*>(a.p16 + e) = h;
+            __builtin_nontemporal_store(w[j], reinterpret_cast<f32x4_any*>(a.master + e));
+            __builtin_nontemporal_store(m[j], reinterpret_cast<f32x4_any*>(a.m + e));
+            __builtin_nontemporal_store(v[j], reinterpret_cast<f32x4_any*>(a.v + e));
+            __builtin_nontemporal_store(h, reinterpret_cast<u16x4_any*>(a.p16 + e));
         }
     } else {
         for (int j = 0; j < 2; ++j)
@@ -237,8 +355,10 @@ __global__ __launch_bounds__(kThreads) void clipped_kernel(StepArgs a, const flo
 
 }  // namespace
 
+int sumsq_grid(int64_t chunks) { return (int)std::min<int64_t>(chunks, kSumsqGrid); }
+
 hipError_t launch_sumsq(const NormArgs& a, double* partial, hipStream_t stream) {
-    sumsq_kernel<<<a.chunks, kThreads, 0, stream>>>(a, partial);
+    sumsq_kernel<<<sumsq_grid(a.chunks), kThreads, 0, stream>>>(a, partial);
     return hipGetLastError();
 }
 
@@ -253,10 +373,33 @@ hipError_t launch_join(const double* partial, int64_t n, double* sumsq, double m
     return hipGetLastError();
 }
 
-hipError_t launch_reduce_sumsq(int dtype, const StepArgs& a, double* partial, hipStream_t stream) {
-    const dim3 grid((unsigned)((a.n + kTile - 1) / kTile));
-    if (dtype == ZSMR_BF16) reduce_sumsq_kernel<ZSMR_BF16><<<grid, kThreads, 0, stream>>>(a, partial);
-    else reduce_sumsq_kernel<ZSMR_FP16><<<grid, kThreads, 0, stream>>>(a, partial);
+namespace {
+template <int DT>
+void reduce_launches(const StepArgs& a, double* partial, double* sumsq, hipStream_t stream) {
+    // one workgroup: 8 elements a lane, or twice that
+    if (a.n <= 2 * kSmall * 8) {
+        reduce_sumsq_small_kernel<DT><<<1, kSmall, 0, stream>>>(a, sumsq);
+        return;
+    }
+    int64_t parts = (a.n + kTile - 1) / kTile;
+    int device = 0, cus = 0;
+    // windows pay once every wave fills its ring
+    if (a.nrows >= kWindowRows && hipGetDevice(&device) == hipSuccess &&
+        hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device) == hipSuccess &&
+        a.n / 512 >= (int64_t)cus * (kThreads / 64) * kRing) {
+        parts = cus;
+        reduce_sumsq_windows_kernel<DT><<<cus, kThreads, 0, stream>>>(a, partial);
+    } else {
+        reduce_sumsq_kernel<DT><<<(unsigned)parts, kThreads, 0, stream>>>(a, partial);
+    }
+    join_kernel<<<1, kJoinThreads, 0, stream>>>(partial, parts, sumsq, 0, 0, nullptr);
+}
+}  // namespace
+
+hipError_t launch_reduce_sumsq(int dtype, const StepArgs& a, double* partial, double* sumsq,
+                               hipStream_t stream) {
+    if (dtype == ZSMR_BF16) reduce_launches<ZSMR_BF16>(a, partial, sumsq, stream);
+    else reduce_launches<ZSMR_FP16>(a, partial, sumsq, stream);
     return hipGetLastError();
 }
 

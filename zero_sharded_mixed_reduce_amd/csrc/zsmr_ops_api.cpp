@@ -67,7 +67,6 @@ int32_t check_list(const void* const* ptrs, const int64_t* numels, const int32_t
 template <int BATCH, typename A, typename Item, typename F>
 struct Batches {
     A a{};
-    int64_t chunks = 0;
     F flush;
     hipError_t err = hipSuccess;
     explicit Batches(F f) : flush(f) {}
@@ -81,7 +80,6 @@ struct Batches {
     }
     void go() {
         if (a.count && err == hipSuccess) err = flush(a);
-        chunks += a.chunks;
         a.count = a.chunks = 0;
     }
 };
@@ -265,7 +263,7 @@ int32_t zsmr_grad_norm(const void* const* ptrs, const int64_t* numels, const int
     int64_t at = 0;
     auto launch = [&](const NormArgs& a) {
         const hipError_t e = launch_sumsq(a, partial + at, stream);
-        at += a.chunks;
+        at += sumsq_grid(a.chunks);
         return e;
     };
     Batches<kNormBatch, NormArgs, NormItem, decltype(launch)> b(launch);
@@ -277,7 +275,7 @@ int32_t zsmr_grad_norm(const void* const* ptrs, const int64_t* numels, const int
     }
     b.go();
     if (b.err != hipSuccess) return hip_fail(b.err);
-    return done(launch_join(partial, chunks, nullptr, max_norm, eps, norm_coef, stream));
+    return done(launch_join(partial, at, nullptr, max_norm, eps, norm_coef, stream));
 }
 
 int32_t zsmr_clip_coef(const double* sums, int64_t n, double max_norm, double eps,
@@ -335,12 +333,10 @@ int32_t zero_reduce_shard_sumsq(zsmr_ctx* c, int32_t rank, int32_t unit, const v
     set_mean_divisor(a, c->world);
     a.g_out = g_out;
     a.n = len;
+    // a rank without a part of this unit leaves a sum of zero
     double* partial = static_cast<double*>(ws);
-    if (len > 0) {
-        const hipError_t e = launch_reduce_sumsq(c->gdt, a, partial, stream);
-        if (e != hipSuccess) return hip_fail(e);
-    }
-    const hipError_t e = launch_join(partial, tiles, sumsq, 0, 0, nullptr, stream);
+    const hipError_t e = len > 0 ? launch_reduce_sumsq(c->gdt, a, partial, sumsq, stream)
+                                 : launch_join(partial, 0, sumsq, 0, 0, nullptr, stream);
     if (e != hipSuccess) return hip_fail(e);
     count_reduce(c, rank, len);
     return ZSMR_OK;

@@ -37,13 +37,15 @@ struct ClipArgs {
     const float* coef;
     int32_t in_place;
 };
+int sumsq_grid(int64_t chunks);     // partial sums a launch of so many chunks leaves
 hipError_t launch_sumsq(const NormArgs& a, double* partial, hipStream_t stream);
 hipError_t launch_clip(const ClipArgs& a, hipStream_t stream);
 // total = partial[0..n): sumsq (if not NULL) = total; norm_coef (if not NULL)
 hipError_t launch_join(const double* partial, int64_t n, double* sumsq, double max_norm,
                        double eps, float* norm_coef, hipStream_t stream);
 // grads, row_stride, nrows, mean, nf, inv_nf, inv_pow2, g_out and n of StepArgs
-hipError_t launch_reduce_sumsq(int dtype, const StepArgs& a, double* partial, hipStream_t stream);
+hipError_t launch_reduce_sumsq(int dtype, const StepArgs& a, double* partial, double* sumsq,
+                               hipStream_t stream);
 // g_in, master, m, v, p16, n and k of StepArgs
 hipError_t launch_clipped(int dtype, const StepArgs& a, const float* coef, hipStream_t stream);
 

@@ -169,7 +169,9 @@ struct Product {
     float* target;                  // E_STATS: [token]
     const float* lse;               // E_GRAD
     const float* grad;              // E_GRAD: [token] or NULL
-    const float* mul;               // {factor of G, factor of the results}
+    const float* mul;               // {factor of G, factor of the results}, or NULL:
+    float g_mul, out_mul;           // these, the latter
+    const float* scale;             // times this (NULL: 1)
     uint16_t* g;                    // E_GRAD: [token][ldg]
     int64_t ldg;
     float* sum;                     // E_DX: [split][token][lds], fp32 between pieces
@@ -180,6 +182,9 @@ struct Product {
     int32_t accumulate;             // E_DW
 };
 
+__device__ __forceinline__ float out_mul(const Product& p) {
+    return p.mul ? p.mul[1] : p.scale ? p.out_mul * *p.scale : p.out_mul;
+}
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 
 // Column n of the result, rows m..m+3: 4 consecutive elements for a lane.
@@ -311,7 +316,7 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
                 p.stats[((p.v0 / BM + mt) * WM + wm) * p.tokens + t] = make_float2(top, sum);
         }
     } else if constexpr (EPI == E_GRAD) {
-        const float mul = p.mul[0];
+        const float mul = p.mul ? p.mul[0] : p.g_mul;
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
             const int64_t t = n0 + j * 16;
@@ -331,7 +336,7 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
             }
         }
     } else if constexpr (EPI == E_DX) {
-        const float mul = p.mul[1];
+        const float mul = out_mul(p);
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
             const int64_t t = n0 + j * 16;
@@ -348,7 +353,7 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
             }
         }
     } else {
-        const float mul = p.mul[1];
+        const float mul = out_mul(p);
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
             const int64_t v = p.v0 + n0 + j * 16;
@@ -363,38 +368,62 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
 }
 
 // ------------------------------------------------------------ small kernels --
-// Join the parts of a token's softmax: 64 tokens of a workgroup, its waves
-// share the parts.
-constexpr int kJoinWaves = 16;
-__global__ __launch_bounds__(kJoinWaves * 64) void stats_kernel(const float2* stats, const float* target,
-                                                                const void* labels, int32_t id_bytes,
-                                                                int64_t tokens, int64_t vocab, int32_t parts,
-                                                                float* loss, float* lse) {
-    __shared__ float2 part[kJoinWaves][64];
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    const int64_t t = (int64_t)blockIdx.x * 64 + lane;
-    float top = -INFINITY, sum = 0.f;
+// Two parts of a softmax: (maximum, sum of exponentials relative to it).
+__device__ __forceinline__ float2 join_parts(float2 a, float2 b) {
+    const float top = fmaxf(a.x, b.x);
+    return make_float2(top, (a.y == 0.f ? 0.f : a.y * exp_of(a.x - top)) + (b.y == 0.f ? 0.f : b.y * exp_of(b.x - top)));
+}
+__device__ __forceinline__ void put_summary(double sum, double count, float* summary) {
+    summary[0] = count > 0 ? (float)(sum / count) : 0.f;
+    summary[1] = count > 0 ? (float)(1.0 / count) : 0.f;
+    summary[2] = (float)count;
+}
+
+// Join the parts of each token's softmax: `lanes` tokens of a workgroup (a power
+// of two, at most 64), its groups of lanes share the parts.  A lone workgroup
+// has all tokens and leaves the summary too.
+constexpr int kStatsThreads = 1024;
+__global__ __launch_bounds__(kStatsThreads) void stats_kernel(const float2* stats, const float* target,
+                                                              const void* labels, int32_t id_bytes,
+                                                              int64_t tokens, int64_t vocab, int32_t parts,
+                                                              int32_t lanes, float* loss, float* lse, float* summary) {
+    __shared__ float2 part[kStatsThreads];
+    const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes, groups = kStatsThreads / lanes;
+    const int64_t t = (int64_t)blockIdx.x * lanes + lane;
+    float2 s = make_float2(-INFINITY, 0.f);
     if (t < tokens) {
-#pragma unroll 4
-        for (int i = wave; i < parts; i += kJoinWaves) {
-            const float2 s = stats[(int64_t)i * tokens + t];
-            const float big = fmaxf(top, s.x);
-            sum = (sum == 0.f ? 0.f : sum * exp_of(top - big)) + (s.y == 0.f ? 0.f : s.y * exp_of(s.x - big));
-            top = big;
+        constexpr int kAhead = 8;
+        for (int i = group; i < parts; i += groups * kAhead) {
+            float2 p[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                p[k] = i + k * groups < parts ? stats[(int64_t)(i + k * groups) * tokens + t] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) s = join_parts(s, p[k]);
         }
     }
-    part[wave][lane] = make_float2(top, sum);
+    part[threadIdx.x] = s;
     __syncthreads();
-    if (wave != 0 || t >= tokens) return;
-    for (int w = 1; w < kJoinWaves; ++w) top = fmaxf(top, part[w][lane].x);
-    sum = 0.f;
-    for (int w = 0; w < kJoinWaves; ++w) {
-        const float2 s = part[w][lane];
-        if (s.y != 0.f) sum += s.y * exp_of(s.x - top);
+    for (int half = groups / 2; half > 0; half /= 2) {
+        if (group < half) part[threadIdx.x] = s = join_parts(s, part[threadIdx.x + half * lanes]);
+        __syncthreads();
     }
-    const float l = top + logf(sum);
-    lse[t] = l;
-    loss[t] = token_at(labels, id_bytes, t, vocab) < 0 ? 0.f : l - target[t];
+    if (threadIdx.x >= 64) return;
+    const bool on = threadIdx.x < lanes && t < tokens;
+    const bool counts = on && token_at(labels, id_bytes, t, vocab) >= 0;
+    float out = 0.f;
+    if (on) {
+        const float l = s.x + logf(s.y);
+        if (counts) out = l - target[t];
+        lse[t] = l;
+        loss[t] = out;
+    }
+    if (gridDim.x > 1) return;
+    double sum = out;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) sum += __shfl_down(sum, d);
+    const int count = __popcll(__ballot(counts));
+    if (threadIdx.x == 0) put_summary(sum, count, summary);
 }
 
 constexpr int kMeanThreads = 1024;
@@ -409,37 +438,32 @@ __global__ __launch_bounds__(kMeanThreads) void mean_kernel(const float* loss, c
     sum = block_sum<kMeanThreads>(sum);
     __syncthreads();
     count = block_sum<kMeanThreads>(count);
-    if (threadIdx.x == 0) {
-        summary[0] = count > 0 ? (float)(sum / count) : 0.f;
-        summary[1] = count > 0 ? (float)(1.0 / count) : 0.f;
-        summary[2] = (float)count;
-    }
+    if (threadIdx.x == 0) put_summary(sum, count, summary);
 }
 
-// mul[0]: what G is multiplied by before it is rounded to 16 bits, a power of
-// two; mul[1] = scale / mul[0].  fp16 keeps 10 bits down to 2^-14 only, and most
-// probabilities of a large vocabulary are below that, so there G is moved up to
-// just below fp16's largest value: |G| <= max |grad|, which lands in [2^14, 2^15).
+// What G is multiplied by before it is rounded to 16 bits, a power of two that
+// the results are divided by again.  bf16 has fp32's range and needs none.  fp16
+// has all its bits down to 2^-14 only, and most probabilities of a large
+// vocabulary are below that: there |G| <= max |grad| is moved to [2^14, 2^15),
+// just below fp16's largest value.
+constexpr float kFp16Mul = 16384.f;
 constexpr int kMulThreads = 1024;
-__global__ __launch_bounds__(kMulThreads) void mul_kernel(const float* grad, int64_t tokens, int32_t fp16,
-                                                          const float* scale, float* mul) {
+__global__ __launch_bounds__(kMulThreads) void mul_kernel(const float* grad, int64_t tokens, const float* scale,
+                                                          float* mul) {
     __shared__ float part[kMulThreads / 64];
-    float top = grad ? 0.f : 1.f;
-    if (grad && fp16) {
-        for (int64_t t = threadIdx.x; t < tokens; t += kMulThreads) {
-            const float g = fabsf(grad[t]);
-            if (g < INFINITY) top = fmaxf(top, g);
-        }
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-        if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = top;
-        __syncthreads();
-        for (int i = 0; i < kMulThreads / 64; ++i) top = fmaxf(top, part[i]);
+    float top = 0.f;
+    for (int64_t t = threadIdx.x; t < tokens; t += kMulThreads) {
+        const float g = fabsf(grad[t]);
+        if (g < INFINITY) top = fmaxf(top, g);
     }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+    if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = top;
+    __syncthreads();
     if (threadIdx.x != 0) return;
+    for (int i = 0; i < kMulThreads / 64; ++i) top = fmaxf(top, part[i]);
     // an exponent that neither factor can leave fp32 with
-    int e = 0;
-    if (fp16) e = max(-60, min(60, top > 0.f ? 14 - ilogbf(top) : 0));
+    const int e = top > 0.f ? max(-60, min(60, 14 - ilogbf(top))) : 0;
     mul[0] = ldexpf(1.f, e);
     mul[1] = ldexpf(scale ? *scale : 1.f, -e);
 }
@@ -464,15 +488,22 @@ __global__ __launch_bounds__(256) void pack_kernel(const uint16_t* src, int64_t 
 
 // dx = rne16(mul * sum over the splits, in order)
 template <int DT>
-__global__ __launch_bounds__(256) void splits_kernel(const float* sum, int64_t lds, int32_t splits,
-                                                     int64_t tokens, int64_t width, const float* mul,
-                                                     uint16_t* out, int64_t ldo) {
-    const int64_t vecs = lds / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__global__ __launch_bounds__(256) void splits_kernel(Product p) {
+    const int64_t vecs = p.lds / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t t = i / vecs, h = (i - t * vecs) * 4;
-    if (t >= tokens) return;
+    if (t >= p.tokens) return;
     f32x4 f = 0.f;
-    for (int s = 0; s < splits; ++s) f += *reinterpret_cast<const f32x4*>(sum + ((int64_t)s * tokens + t) * lds + h);
-    put4<DT>(out + t * ldo, h, width, f * mul[1], false);
+    constexpr int kAhead = 8;
+    for (int s = 0; s < p.splits; s += kAhead) {
+        f32x4 x[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (s + k < p.splits) x[k] = *reinterpret_cast<const f32x4*>(p.sum + ((int64_t)(s + k) * p.tokens + t) * p.lds + h);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (s + k < p.splits) f += x[k];
+    }
+    put4<DT>(p.out + t * p.ldo, h, p.width, f * out_mul(p), false);
 }
 
 // --------------------------------------------------------------------- host --
@@ -600,8 +631,12 @@ hipError_t forward(const XentArgs& a, void* ws, hipStream_t stream) {
             launch_product<DT, E_STATS>(p, bn, stream);
         }
         const int32_t parts = (int32_t)tiles_of(a.vocab, BM) * vocab_waves(a.tokens);
-        stats_kernel<<<(unsigned)tiles_of(a.tokens, 64), kJoinWaves * 64, 0, stream>>>(
-            s.stats, s.target, a.labels, a.id_bytes, a.tokens, a.vocab, parts, a.loss, a.lse);
+        int lanes = 64;
+        while (lanes / 2 >= a.tokens) lanes /= 2;
+        const unsigned grid = (unsigned)tiles_of(a.tokens, lanes);
+        stats_kernel<<<grid, kStatsThreads, 0, stream>>>(s.stats, s.target, a.labels, a.id_bytes, a.tokens,
+                                                         a.vocab, parts, lanes, a.loss, a.lse, a.summary);
+        if (grid == 1) return hipGetLastError();
     }
     mean_kernel<<<1, kMeanThreads, 0, stream>>>(a.loss, a.labels, a.id_bytes, a.tokens, a.vocab, a.summary);
     return hipGetLastError();
@@ -613,7 +648,8 @@ hipError_t backward(const XentArgs& a, void* ws, hipStream_t stream) {
     const int bn = token_tile(a.tokens);
     const int64_t piece = piece_of(a.tokens, a.vocab);
     const int splits = splits_of(a.tokens, a.width, piece);
-    mul_kernel<<<1, kMulThreads, 0, stream>>>(a.grad, a.tokens, DT == ZSMR_FP16, a.scale, s.mul);
+    const bool fp16 = DT == ZSMR_FP16, weighted = fp16 && a.grad;
+    if (weighted) mul_kernel<<<1, kMulThreads, 0, stream>>>(a.grad, a.tokens, a.scale, s.mul);
     Operands o;
     pack_x(a, s, &o, stream);
     for (int64_t v0 = 0; v0 < a.vocab; v0 += piece) {
@@ -623,7 +659,10 @@ hipError_t backward(const XentArgs& a, void* ws, hipStream_t stream) {
         Product p = logits_of(a, o, v0, bn);
         p.lse = a.lse;
         p.grad = a.grad;
-        p.mul = s.mul;
+        p.mul = weighted ? s.mul : nullptr;
+        p.g_mul = fp16 ? kFp16Mul : 1.f;
+        p.out_mul = fp16 ? 1.f / kFp16Mul : 1.f;
+        p.scale = a.scale;
         p.g = s.g;
         p.ldg = piece;
         if (a.tokens) launch_product<DT, E_GRAD>(p, bn, stream);
@@ -643,6 +682,8 @@ hipError_t backward(const XentArgs& a, void* ws, hipStream_t stream) {
             d.out = a.dx;
             d.ldo = a.dx_stride;
             launch_product<DT, E_DX>(d, bn, stream);
+            if (splits > 1 && v0 + piece >= a.vocab)
+                splits_kernel<DT><<<(unsigned)tiles_of(a.tokens * (d.lds / 4), 256), 256, 0, stream>>>(d);
         }
         if (a.dw) {
             Product d = p;
@@ -657,11 +698,6 @@ hipError_t backward(const XentArgs& a, void* ws, hipStream_t stream) {
             d.accumulate = a.accumulate;
             launch_product<DT, E_DW>(d, 256, stream);
         }
-    }
-    if (a.dx && a.tokens && splits > 1) {
-        const int64_t lds = ceil_to(a.width, 4);
-        splits_kernel<DT><<<(unsigned)tiles_of(a.tokens * (lds / 4), 256), 256, 0, stream>>>(
-            s.sum, lds, splits, a.tokens, a.width, s.mul, a.dx, a.dx_stride);
     }
     return hipGetLastError();
 }
