@@ -53,6 +53,13 @@ struct Mat {
     int64_t ld, rows, cols;
 };
 
+// The transposing LDS read of four 16-bit elements.  __restrict__ tells the
+// compiler that no load in flight writes what it reads (the waits of the main
+// loop see to that); without it, it waits for all of them before each read.
+__device__ __forceinline__ u32x2 read_transposed(const char* __restrict__ p) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p)));
+}
+
 // A tile of R (rows or columns of the product) x BK, in LDS.
 //  k along rows: R rows of 128 bytes; the 16-byte chunk c of row r sits in slot
 //    c ^ (r & 7), so that the 8 rows a read touches at a time lie in different
@@ -104,24 +111,20 @@ struct Tile {
             k_left = (int)(m.cols - k0);
         }
     }
-    // Start the loads of one step into `to` (kBytes of LDS) and move on.
-    __device__ __forceinline__ void load(char* to) {
+    // Start the loads of one step into `to` (kBytes of LDS) and move on; `on`
+    // false: the same instructions, which read nothing and write zeros.
+    __device__ __forceinline__ void load(char* to, bool on) {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-        const int bound = left < 0 ? 0 : left > 0x7fffffff ? 0x7fffffff : (int)left;
+        const int bound = !on || left < 0 ? 0 : left > 0x7fffffff ? 0x7fffffff : (int)left;
         const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, bound, 0x00027000);
+        // the last step of rows whose length is no multiple of BK: the next
+        // row's values must not come in as k
+        const int lane = threadIdx.x % 64;
+        const bool past = !OUTER && ((lane % 8) ^ (lane / 8)) * 8 >= k_left;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            uint32_t o = off[i];
-            if constexpr (!OUTER) {
-                // the last step of a row whose length is no multiple of BK:
-                // the next row's values must not come in as k
-                if (k_left < BK) {
-                    const int row = (threadIdx.x / 64 + kWaves * i) * 8 + threadIdx.x % 64 / 8;
-                    if ((((int)threadIdx.x % 8) ^ (row & 7)) * 8 >= k_left) o = 0x80000000u;
-                }
-            }
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(to + (wave + kWaves * i) * 1024), 16, o, 0, 0, 0);
-        }
+        for (int i = 0; i < kLoads; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(to + (wave + kWaves * i) * 1024), 16,
+                                                     past ? 0x80000000u : off[i], 0, 0, 0);
         base += step;
         left -= step;
         k_left -= BK;
@@ -134,10 +137,8 @@ struct Tile {
             const int k = kk * 32 + lane / 16 * 8 + (lane % 16) / 4;
             const int chunk = (at / 8 + (lane % 4) / 2) ^ swizzle(k);
             const char* p = t + k * (R * 2) + chunk * 16 + (lane & 1) * 8;
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p + 4 * (R * 2)));
+            const u32x2 a = read_transposed(p), b = read_transposed(p + 4 * (R * 2));
             u32x4 r;
-            const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
             r[0] = a[0];
             r[1] = a[1];
             r[2] = b[0];
@@ -150,6 +151,19 @@ struct Tile {
         }
     }
 };
+
+// Spread a block's LDS reads and loads evenly among its matrix instructions.
+template <int READS, int LOADS, int MFMA>
+__device__ __forceinline__ void interleave() {
+    constexpr int kOps = READS + LOADS, kEach = kOps < MFMA ? MFMA / kOps : 1;
+    constexpr int kRounds = kOps < MFMA ? kOps : MFMA;
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        if (i < LOADS) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);      // vector memory read
+        else __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                // LDS read
+        __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);                 // matrix
+    }
+}
 
 // vmcnt(n) and lgkmcnt(0)
 #define ZSMR_WAIT(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | 0x70 | ((n) >> 4 << 14))
@@ -207,14 +221,15 @@ __device__ __forceinline__ void put4(uint16_t* p, int64_t at, int64_t width, f32
     }
 }
 
-template <int DT, int EPI, int BN, int WM, int STAGES>
+template <int DT, int EPI, int BN, int WM>
 __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
+#if defined(__HIP_DEVICE_COMPILE__)     // the scheduling hints have no host form
     constexpr bool A_OUTER = EPI == E_DX || EPI == E_DW, B_OUTER = EPI == E_DW;
     constexpr int WN = kWaves / WM, TM = BM / WM / 16, TN = BN / WN / 16;
     typedef Tile<BM, A_OUTER> TA;
     typedef Tile<BN, B_OUTER> TB;
     constexpr int kLoads = TA::kLoads + TB::kLoads, kStage = TA::kBytes + TB::kBytes;
-    __shared__ __attribute__((aligned(1024))) char smem[STAGES * kStage];
+    __shared__ __attribute__((aligned(1024))) char smem[2 * kStage];
 
     // Consecutive workgroups go to the eight XCDs in turn; each XCD takes a
     // contiguous run of tiles, in groups of 8 in m, so that the tiles it works
@@ -246,41 +261,53 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = 0.f;
 
+    // Two stages of LDS and two sets of operand registers: the second half's
+    // operands of a step (k 32..63) are read while its first half is
+    // multiplied, the next step's first half while the second is.  The barrier
+    // between the halves is the only one of a step: behind it every wave has the
+    // stage's operands in registers, so its LDS is refilled (with the step after
+    // the next), and the next step's loads, which had a whole step to arrive,
+    // are there.
+    constexpr int kReads = TM * (A_OUTER ? 2 : 1) + TN * (B_OUTER ? 2 : 1), kMfma = TM * TN;
+    u32x4 a0[TM], b0[TN], a1[TM], b1[TN];
+    auto read = [&](u32x4* a, u32x4* b, const char* stage, int kk) {
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s)
-        if (s < steps) {
-            ta.load(smem + s * kStage);
-            tb.load(smem + s * kStage + TA::kBytes);
-        }
-    int at = 0, to = STAGES - 1;
-    for (int s = 0; s < steps; ++s) {
-        // this step's tile has arrived; the steps after it may be in flight
-        if (s + STAGES - 2 < steps) ZSMR_WAIT((STAGES - 2) * kLoads);
-        else ZSMR_WAIT(0);
+        for (int j = 0; j < TN; ++j) b[j] = TB::read(stage + TA::kBytes, (wn * TN + j) * 16, kk);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) a[i] = TA::read(stage, (wm * TM + i) * 16, kk);
+    };
+    auto multiply = [&](const u32x4* a, const u32x4* b) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = mfma<DT>(a[i], b[j], acc[i][j]);
+    };
+    if (steps > 0) {
+        ta.load(smem, true);
+        tb.load(smem + TA::kBytes, true);
+        ZSMR_WAIT(0);
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        // every wave is done with the stage before: refill it
-        if (s + STAGES - 1 < steps) {
-            ta.load(smem + to * kStage);
-            tb.load(smem + to * kStage + TA::kBytes);
-        }
-        const char* sa = smem + at * kStage;
-        const char* sb = sa + TA::kBytes;
-#pragma unroll
-        for (int kk = 0; kk < BK / 32; ++kk) {
-            u32x4 b[TN];
-#pragma unroll
-            for (int j = 0; j < TN; ++j) b[j] = TB::read(sb, (wn * TN + j) * 16, kk);
-#pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                const u32x4 a = TA::read(sa, (wm * TM + i) * 16, kk);
-#pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = mfma<DT>(a, b[j], acc[i][j]);
-            }
-        }
-        at = at + 1 == STAGES ? 0 : at + 1;
-        to = to + 1 == STAGES ? 0 : to + 1;
+        ta.load(smem + kStage, steps > 1);
+        tb.load(smem + kStage + TA::kBytes, steps > 1);
+        read(a0, b0, smem, 0);
     }
+    for (int s = 0; s < steps; ++s) {
+        char* cur = smem + (s & 1) * kStage;
+        char* next = smem + (~s & 1) * kStage;
+        read(a1, b1, cur, 1);
+        multiply(a0, b0);
+        interleave<kReads, 0, kMfma>();
+        ZSMR_WAIT(0);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        ta.load(cur, s + 2 < steps);
+        tb.load(cur + TA::kBytes, s + 2 < steps);
+        read(a0, b0, next, 0);
+        multiply(a1, b1);
+        interleave<kReads, kLoads, kMfma>();
+    }
+    ZSMR_WAIT(0);           // no load may still be on its way to this LDS when the workgroup ends
 
     // acc[i][j][r] is D at m = m0 + 16 i + r, n = n0 + 16 j
     const int64_t m0 = (int64_t)mt * BM + wm * TM * 16 + lane / 16 * 4;
@@ -365,6 +392,7 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
             }
         }
     }
+#endif
 }
 
 // ------------------------------------------------------------ small kernels --
@@ -559,11 +587,11 @@ template <int DT, int EPI>
 void launch_product(const Product& p, int bn, hipStream_t stream) {
     const unsigned grid = (unsigned)(p.m_tiles * p.n_tiles * p.splits);
     if constexpr (EPI == E_DW) {
-        product_kernel<DT, EPI, 256, 2, 2><<<grid, kThreads, 0, stream>>>(p);
+        product_kernel<DT, EPI, 256, 2><<<grid, kThreads, 0, stream>>>(p);
     } else {
-        if (bn == 64) product_kernel<DT, EPI, 64, 8, 3><<<grid, kThreads, 0, stream>>>(p);
-        else if (bn == 128) product_kernel<DT, EPI, 128, 4, 3><<<grid, kThreads, 0, stream>>>(p);
-        else product_kernel<DT, EPI, 256, 2, 2><<<grid, kThreads, 0, stream>>>(p);
+        if (bn == 64) product_kernel<DT, EPI, 64, 8><<<grid, kThreads, 0, stream>>>(p);
+        else if (bn == 128) product_kernel<DT, EPI, 128, 4><<<grid, kThreads, 0, stream>>>(p);
+        else product_kernel<DT, EPI, 256, 2><<<grid, kThreads, 0, stream>>>(p);
     }
 }
 
