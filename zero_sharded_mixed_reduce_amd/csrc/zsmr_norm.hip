@@ -248,16 +248,17 @@ __global__ __launch_bounds__(kThreads) void reduce_sumsq_windows_kernel(StepArgs
         const uint16_t* p = a.grads + tile * 512 + lane * 8;
         f32x8 g = -0.0f;
         u16x8 x[kRows], y[kRows];
+        // rows past the last are that row again, and are not added
         auto load = [&](u16x8* h, int r) {
 #pragma unroll
             for (int k = 0; k < kRows; ++k)
-                if (r + k < a.nrows)
-                    h[k] = __builtin_nontemporal_load(reinterpret_cast<const u16x8_any*>(p + (int64_t)(r + k) * a.row_stride));
+                h[k] = __builtin_nontemporal_load(reinterpret_cast<const u16x8_any*>(
+                    p + (int64_t)(r + k < a.nrows ? r + k : a.nrows - 1) * a.row_stride));
         };
         auto add = [&](const u16x8* h, int r) {
 #pragma unroll
             for (int k = 0; k < kRows; ++k)
-                if (r + k < a.nrows) {
+                if (r + kRows <= a.nrows || r + k < a.nrows) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) g[i] += widen16<DT>(h[k][i]);
                 }
@@ -270,10 +271,10 @@ __global__ __launch_bounds__(kThreads) void reduce_sumsq_windows_kernel(StepArgs
                 taken = cycle;
                 wait_clock((cycle + 1) * kCycle - kLead);
             }
-            load(y, r + kRows);
+            if (r + kRows < a.nrows) load(y, r + kRows);
             add(x, r);
-            load(x, r + 2 * kRows);
-            add(y, r + kRows);
+            if (r + 2 * kRows < a.nrows) load(x, r + 2 * kRows);
+            if (r + kRows < a.nrows) add(y, r + kRows);
         }
         g = mean_sumsq(a, g, &s);
         if (done - stored == kRing) flush();

@@ -56,6 +56,7 @@ struct Mat {
 // The transposing LDS read of four 16-bit elements.  __restrict__ tells the
 // compiler that no load in flight writes what it reads (the waits of the main
 // loop see to that); without it, it waits for all of them before each read.
+template <typename = void>
 __device__ __forceinline__ u32x2 read_transposed(const char* __restrict__ p) {
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p)));
 }
@@ -199,7 +200,19 @@ struct Product {
 __device__ __forceinline__ float out_mul(const Product& p) {
     return p.mul ? p.mul[1] : p.scale ? p.out_mul * *p.scale : p.out_mul;
 }
-__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+// Exponentials are powers of two of arguments times log2 e, which one fused
+// multiply-add moves by the maximum (or by lse): 2^(s log2 e - shift).
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.69314718f;
+template <typename = void>
+__device__ __forceinline__ float exp2_of(float s, float shift) {
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(s, kLog2e, -shift));
+}
+// Two parts of a softmax: (shift, sum of the powers relative to it).
+__device__ __forceinline__ float2 join_parts(float2 a, float2 b) {
+    const float top = fmaxf(a.x, b.x);
+    return make_float2(top, (a.y == 0.f ? 0.f : a.y * __builtin_amdgcn_exp2f(a.x - top)) +
+                                (b.y == 0.f ? 0.f : b.y * __builtin_amdgcn_exp2f(b.x - top)));
+}
 
 // Column n of the result, rows m..m+3: 4 consecutive elements for a lane.
 template <int DT>
@@ -312,35 +325,52 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
     // acc[i][j][r] is D at m = m0 + 16 i + r, n = n0 + 16 j
     const int64_t m0 = (int64_t)mt * BM + wm * TM * 16 + lane / 16 * 4;
     const int64_t n0 = (int64_t)nt * BN + wn * TN * 16 + lane % 16;
+    // The rows that a lane holds as 16 i + r, up to `rows`, belong to the
+    // vocabulary; only the last tile's waves have fewer than all.
+    const int64_t left = p.vocab - p.v0 - m0;
+    const int rows = left > TM * 16 ? TM * 16 : (int)left;
+    const bool whole = p.vocab - p.v0 - ((int64_t)mt * BM + wm * TM * 16) >= TM * 16;       // of the wave
     if constexpr (EPI == E_STATS) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
             const int64_t t = n0 + j * 16;
             const int32_t label = t < p.tokens ? token_at(p.labels, p.id_bytes, t, p.vocab) : -1;
-            float top = -INFINITY, sum = 0.f;
+            // the label's row among the lane's
+            const int64_t far = label - p.v0 - m0;
+            const int mine = label >= 0 && far >= 0 && far < rows && (far & 12) == 0 ? (int)far : -1;
+            if (__any(mine >= 0)) {
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
+                for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int64_t v = p.v0 + m0 + i * 16 + r;
-                    if (v < p.vocab) top = fmaxf(top, acc[i][j][r]);
-                    if (v == label) p.target[t] = acc[i][j][r];
-                }
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (p.v0 + m0 + i * 16 + r < p.vocab) sum += exp_of(acc[i][j][r] - top);
-            // the four lane groups hold other rows of the same column
-#pragma unroll
-            for (int d = 16; d < 64; d <<= 1) {
-                const float top2 = __shfl_xor(top, d), sum2 = __shfl_xor(sum, d);
-                const float big = fmaxf(top, top2);
-                sum = (sum == 0.f ? 0.f : sum * exp_of(top - big)) + (sum2 == 0.f ? 0.f : sum2 * exp_of(top2 - big));
-                top = big;
+                    for (int r = 0; r < 4; ++r)
+                        if (i * 16 + r == mine) p.target[t] = acc[i][j][r];
             }
+            if (!whole) {
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (i * 16 + r >= rows) acc[i][j][r] = -INFINITY;
+            }
+            float top = acc[0][j][0];
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) top = fmaxf(top, acc[i][j][r]);
+            // the four lane groups hold other rows of the same column; the
+            // power's argument must not become -inf + inf where no row is left
+#pragma unroll
+            for (int d = 16; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+            const float shift = top == -INFINITY ? 0.f : top * kLog2e;
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sum += exp2_of(acc[i][j][r], shift);
+#pragma unroll
+            for (int d = 16; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
             if (lane < 16 && t < p.tokens)
-                p.stats[((p.v0 / BM + mt) * WM + wm) * p.tokens + t] = make_float2(top, sum);
+                p.stats[((p.v0 / BM + mt) * WM + wm) * p.tokens + t] = make_float2(sum == 0.f ? -INFINITY : shift, sum);
         }
     } else if constexpr (EPI == E_GRAD) {
         const float mul = p.mul ? p.mul[0] : p.g_mul;
@@ -349,17 +379,32 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
             const int64_t t = n0 + j * 16;
             if (t >= p.tokens) continue;
             const int32_t label = token_at(p.labels, p.id_bytes, t, p.vocab);
-            const float lse = p.lse[t], weight = label < 0 ? 0.f : (p.grad ? p.grad[t] : 1.f) * mul;
+            const int64_t far = label - p.v0 - m0;
+            const int mine = label >= 0 && far >= 0 && far < rows && (far & 12) == 0 ? (int)far : -1;
+            const bool none = label < 0;
+            const float shift = p.lse[t] * kLog2e, weight = (p.grad ? p.grad[t] : 1.f) * mul;
+            uint16_t* g = p.g + t * p.ldg + m0;
+            const bool has = __any(mine >= 0);
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
-                const int64_t v = p.v0 + m0 + i * 16;
+                f32x4 f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) f[r] = exp2_of(acc[i][j][r], shift);
+                if (has) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (i * 16 + r == mine) f[r] -= 1.f;
+                }
                 u16x4 h;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float g = exp_of(acc[i][j][r] - lse) - (v + r == label ? 1.f : 0.f);
-                    h[r] = label >= 0 && v + r < p.vocab ? narrow16<DT>(g * weight) : (uint16_t)0;
+                for (int r = 0; r < 4; ++r) h[r] = narrow16<DT>(f[r] * weight);
+                if (none) h = 0;
+                if (!whole) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (i * 16 + r >= rows) h[r] = 0;
                 }
-                if (v - p.v0 < p.ldg) *reinterpret_cast<u16x4*>(p.g + t * p.ldg + (v - p.v0)) = h;
+                *reinterpret_cast<u16x4*>(g + i * 16) = h;      // ldg is a multiple of the tile
             }
         }
     } else if constexpr (EPI == E_DX) {
@@ -396,11 +441,6 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
 }
 
 // ------------------------------------------------------------ small kernels --
-// Two parts of a softmax: (maximum, sum of exponentials relative to it).
-__device__ __forceinline__ float2 join_parts(float2 a, float2 b) {
-    const float top = fmaxf(a.x, b.x);
-    return make_float2(top, (a.y == 0.f ? 0.f : a.y * exp_of(a.x - top)) + (b.y == 0.f ? 0.f : b.y * exp_of(b.x - top)));
-}
 __device__ __forceinline__ void put_summary(double sum, double count, float* summary) {
     summary[0] = count > 0 ? (float)(sum / count) : 0.f;
     summary[1] = count > 0 ? (float)(1.0 / count) : 0.f;
@@ -441,7 +481,7 @@ __global__ __launch_bounds__(kStatsThreads) void stats_kernel(const float2* stat
     const bool counts = on && token_at(labels, id_bytes, t, vocab) >= 0;
     float out = 0.f;
     if (on) {
-        const float l = s.x + logf(s.y);
+        const float l = kLn2 * (s.x + log2f(s.y));
         if (counts) out = l - target[t];
         lse[t] = l;
         loss[t] = out;
@@ -538,20 +578,28 @@ __global__ __launch_bounds__(256) void splits_kernel(Product p) {
 int64_t ceil_to(int64_t n, int64_t k) { return (n + k - 1) / k * k; }
 int64_t tiles_of(int64_t n, int64_t k) { return (n + k - 1) / k; }
 
-// Tokens of a tile: as few as hold all of them, at most 256.
-int token_tile(int64_t tokens) { return tokens <= 64 ? 64 : tokens <= 128 ? 128 : 256; }
+// Tokens of a tile: as few as hold all of them.
+int token_tile(int64_t tokens) {
+    if (tokens <= 128) return tokens <= 64 ? 64 : 128;
+    // 192 where it pads less
+    return tiles_of(tokens, 192) * 192 < tiles_of(tokens, 256) * 256 ? 192 : 256;
+}
 int vocab_waves(int64_t tokens) { return tokens <= 64 ? 8 : tokens <= 128 ? 4 : 2; }
 
-// The vocabulary's pieces: G of one takes about 512 MB at most.
-int64_t piece_of(int64_t tokens, int64_t vocab) {
-    const int64_t most = std::max<int64_t>(BM, (int64_t(1) << 28) / std::max<int64_t>(tokens, 1) / BM * BM);
-    const int64_t pieces = tiles_of(vocab, most);
-    return ceil_to(tiles_of(vocab, pieces), BM);
+// The vocabulary's pieces: G of one takes about 512 MB at most, and the tiles of
+// dw over one fill the 256 CUs a whole number of times if it has that many.
+constexpr int64_t kCus = 256;
+int64_t piece_of(int64_t tokens, int64_t vocab, int64_t width) {
+    int64_t tiles = std::max<int64_t>(1, (int64_t(1) << 28) / std::max<int64_t>(tokens, 1) / BM);
+    if (tiles >= tiles_of(vocab, BM)) return ceil_to(vocab, BM);
+    const int64_t across = tiles_of(width, BM), rounds = tiles * across / kCus;
+    if (rounds > 0) tiles = rounds * kCus / across;
+    return tiles * BM;
 }
 // k splits of the dx product: enough to give every CU a tile.
 int splits_of(int64_t tokens, int64_t width, int64_t piece) {
     const int64_t tiles = tiles_of(width, BM) * tiles_of(std::max<int64_t>(tokens, 1), token_tile(tokens));
-    const int64_t want = 512 / tiles, most = piece / 1024;
+    const int64_t want = 2 * kCus / tiles, most = piece / 1024;
     return (int)std::max<int64_t>(1, std::min(want, most));
 }
 
@@ -569,7 +617,7 @@ Space space_of(char* ws, int64_t tokens, int64_t vocab, int64_t width, bool back
         at += ceil_to(bytes, 256);
         return p;
     };
-    const int64_t piece = piece_of(tokens, vocab), packed = ceil_to(width, 8);
+    const int64_t piece = piece_of(tokens, vocab, width), packed = ceil_to(width, 8);
     s.stats = reinterpret_cast<float2*>(take(tiles_of(vocab, BM) * vocab_waves(tokens) * tokens * 8));
     s.target = reinterpret_cast<float*>(take(tokens * 4));
     s.x = reinterpret_cast<uint16_t*>(take(tokens * packed * 2));
@@ -591,6 +639,7 @@ void launch_product(const Product& p, int bn, hipStream_t stream) {
     } else {
         if (bn == 64) product_kernel<DT, EPI, 64, 8><<<grid, kThreads, 0, stream>>>(p);
         else if (bn == 128) product_kernel<DT, EPI, 128, 4><<<grid, kThreads, 0, stream>>>(p);
+        else if (bn == 192) product_kernel<DT, EPI, 192, 2><<<grid, kThreads, 0, stream>>>(p);
         else product_kernel<DT, EPI, 256, 2><<<grid, kThreads, 0, stream>>>(p);
     }
 }
@@ -650,7 +699,7 @@ hipError_t forward(const XentArgs& a, void* ws, hipStream_t stream) {
     if (a.tokens) {
         Operands o;
         pack_x(a, s, &o, stream);
-        const int64_t piece = loads16(a.w, a.w_stride, a.width) ? a.vocab : piece_of(a.tokens, a.vocab);
+        const int64_t piece = loads16(a.w, a.w_stride, a.width) ? a.vocab : piece_of(a.tokens, a.vocab, a.width);
         for (int64_t v0 = 0; v0 < a.vocab; v0 += piece) {
             pack_w(a, s, v0, std::min(piece, a.vocab - v0), &o, stream);
             Product p = logits_of(a, o, v0, bn);
@@ -674,7 +723,7 @@ template <int DT>
 hipError_t backward(const XentArgs& a, void* ws, hipStream_t stream) {
     const Space s = space_of(static_cast<char*>(ws), a.tokens, a.vocab, a.width, true);
     const int bn = token_tile(a.tokens);
-    const int64_t piece = piece_of(a.tokens, a.vocab);
+    const int64_t piece = piece_of(a.tokens, a.vocab, a.width);
     const int splits = splits_of(a.tokens, a.width, piece);
     const bool fp16 = DT == ZSMR_FP16, weighted = fp16 && a.grad;
     if (weighted) mul_kernel<<<1, kMulThreads, 0, stream>>>(a.grad, a.tokens, a.scale, s.mul);
