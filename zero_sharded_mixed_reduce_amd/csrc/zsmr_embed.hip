@@ -72,6 +72,69 @@ __device__ __forceinline__ uint32_t sort_key(const SortArgs& a, int64_t i) {
     const int32_t id = token_at(a.ids, a.id_bytes, i, a.vocab);
     return id < 0 ? (uint32_t)a.vocab : (uint32_t)id;
 }
+// The lanes of the wave that hold the same digit; d of a lane that is off does
+// not matter.
+__device__ __forceinline__ uint64_t same_digit(uint32_t d, bool on) {
+    uint64_t same = __ballot(on);
+#pragma unroll
+    for (int b = 0; b < kDigit; ++b) {
+        const uint64_t has = __ballot((d >> b) & 1);
+        same &= (d >> b) & 1 ? has : ~has;
+    }
+    return same;
+}
+__device__ __forceinline__ int rank_in(uint64_t same) { return __popcll(same & ((1ull << (threadIdx.x % 64)) - 1)); }
+// Count a wave's digits: one add if all are the same (a frequent token's keys
+// come together after the first pass, and 64 adds to one counter queue up).
+__device__ __forceinline__ void count_digits(uint32_t* bins, uint32_t d, bool on) {
+    if (!on) return;
+    const uint32_t first = __builtin_amdgcn_readfirstlane(d);
+    const uint64_t lanes = __ballot(true);
+    if (__ballot(d == first) == lanes) {
+        if (rank_in(lanes) == 0) atomicAdd(&bins[d], (uint32_t)__popcll(lanes));
+    } else {
+        atomicAdd(&bins[d], 1u);
+    }
+}
+// cnt[w][d]: the keys of digit d in wave w's part, on return where the first of
+// them goes: after those of smaller digits (all: their number), those of other
+// workgroups before this one (before) and those of the waves before.
+__device__ __forceinline__ void places(uint32_t (*cnt)[kBins], uint32_t all, uint32_t before) {
+    __shared__ uint32_t wave_sum[kBins / 64];
+    const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
+    uint32_t upto = all;
+    if (tid < kBins) {
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t up = __shfl_up(upto, d);
+            if (lane >= d) upto += up;
+        }
+        if (lane == 63) wave_sum[wave] = upto;
+    }
+    __syncthreads();
+    if (tid < kBins) {
+        uint32_t at = upto - all + before;
+        for (int w = 0; w < wave; ++w) at += wave_sum[w];
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) {
+            const uint32_t c = cnt[w][tid];
+            cnt[w][tid] = at;
+            at += c;
+        }
+    }
+    __syncthreads();
+}
+// This lane's key's place; takes it from the wave's row of places.
+__device__ __forceinline__ uint32_t take_place(uint32_t* row, uint32_t d, bool on) {
+    const uint64_t same = same_digit(d, on);
+    const int rank = rank_in(same);
+    const uint32_t at = on ? row[d] : 0;
+    __builtin_amdgcn_wave_barrier();
+    if (on && rank == 0) row[d] = at + __popcll(same);
+    __builtin_amdgcn_wave_barrier();
+    return at + rank;
+}
+
 template <bool FIRST>
 __global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a) {
     __shared__ uint32_t hist[2][kBins], cnt[kSortWaves][kBins];     // hist: keys before this part; the others
@@ -79,6 +142,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a) {
     for (int i = tid; i < 2 * kBins; i += kSortThreads) (&hist[0][0])[i] = 0;
     for (int i = tid; i < kSortWaves * kBins; i += kSortThreads) (&cnt[0][0])[i] = 0;
     __syncthreads();
+    // parts and a wave's 64 keys both start at multiples of 64
     const int64_t b0 = (int64_t)blockIdx.x * a.part;
     const int64_t b1 = b0 + a.part < a.tokens ? b0 + a.part : a.tokens;
     constexpr int kAhead = 16;
@@ -92,60 +156,73 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             const int64_t i = i0 + k * kSortThreads;
-            if (i < a.tokens) atomicAdd(&hist[i >= b0][(key[k] >> a.shift) & (kBins - 1)], 1u);
+            count_digits(hist[i >= b0], (key[k] >> a.shift) & (kBins - 1), i < a.tokens);
         }
     }
     // this workgroup's keys, a contiguous run for each wave
     const int64_t run = (b1 - b0 + kSortThreads - 1) / kSortThreads * 64;
     const int64_t w0 = b0 + wave * run;
     const int64_t w1 = w0 + run < b1 ? w0 + run : b1;
-    for (int64_t i = w0 + lane; i < w1; i += 64) atomicAdd(&cnt[wave][(sort_key<FIRST>(a, i) >> a.shift) & (kBins - 1)], 1u);
-    __syncthreads();
-    // exclusive scan of the totals: a wave scans its 64 bins, then the waves' sums
-    __shared__ uint32_t wsum[kBins / 64];
-    uint32_t mine = 0, incl = 0;
-    if (tid < kBins) {
-        mine = incl = hist[0][tid] + hist[1][tid];
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const uint32_t up = __shfl_up(incl, d);
-            if (lane >= d) incl += up;
-        }
-        if (lane == 63) wsum[wave] = incl;
+    for (int64_t i0 = w0; i0 < w1; i0 += 64) {
+        const bool on = i0 + lane < w1;
+        count_digits(cnt[wave], on ? (sort_key<FIRST>(a, i0 + lane) >> a.shift) & (kBins - 1) : 0, on);
     }
     __syncthreads();
-    if (tid < kBins) {
-        uint32_t at = incl - mine + hist[0][tid];
-        for (int w = 0; w < wave; ++w) at += wsum[w];
-#pragma unroll
-        for (int w = 0; w < kSortWaves; ++w) {
-            const uint32_t c = cnt[w][tid];
-            cnt[w][tid] = at;
-            at += c;
-        }
-    }
-    __syncthreads();
+    places(cnt, tid < kBins ? hist[0][tid] + hist[1][tid] : 0, tid < kBins ? hist[0][tid] : 0);
     for (int64_t i0 = w0; i0 < w1; i0 += 64) {
         const int64_t i = i0 + lane;
         const bool on = i < w1;
         const uint32_t key = on ? sort_key<FIRST>(a, i) : 0u;
-        const uint32_t d = (key >> a.shift) & (kBins - 1);
-        uint64_t same = __ballot(on);
-#pragma unroll
-        for (int b = 0; b < kDigit; ++b) {
-            const uint64_t has = __ballot((d >> b) & 1);
-            same &= (d >> b) & 1 ? has : ~has;
-        }
-        const int rank = __popcll(same & ((1ull << lane) - 1));
-        uint32_t at = 0;
-        if (on) at = cnt[wave][d];
-        __builtin_amdgcn_wave_barrier();
-        if (on && rank == 0) cnt[wave][d] = at + __popcll(same);
-        __builtin_amdgcn_wave_barrier();
+        const uint32_t at = take_place(cnt[wave], (key >> a.shift) & (kBins - 1), on);
         if (on) {
-            a.key_out[at + rank] = key;
-            a.pos_out[at + rank] = FIRST ? (uint32_t)i : a.pos_in[i];
+            a.key_out[at] = key;
+            a.pos_out[at] = FIRST ? (uint32_t)i : a.pos_in[i];
         }
+    }
+}
+
+// All passes over a few tokens in one workgroup, between two buffers in LDS.
+constexpr int kSmallSort = 4096;
+__global__ __launch_bounds__(kSortThreads) void sort_small_kernel(SortArgs a, int bits) {
+    __shared__ uint32_t key[2][kSmallSort], cnt[kSortWaves][kBins];
+    __shared__ uint16_t pos[2][kSmallSort];
+    const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
+    const int n = a.tokens, run = (n + kSortThreads - 1) / kSortThreads * 64;
+    const int w0 = wave * run, w1 = w0 + run < n ? w0 + run : n;
+    for (int i = tid; i < n; i += kSortThreads) {
+        key[0][i] = sort_key<true>(a, i);
+        pos[0][i] = (uint16_t)i;
+    }
+    int from = 0;
+    for (int shift = 0; shift < bits; shift += kDigit, from ^= 1) {
+        for (int i = tid; i < kSortWaves * kBins; i += kSortThreads) (&cnt[0][0])[i] = 0;
+        __syncthreads();
+        for (int i0 = w0; i0 < w1; i0 += 64) {
+            const bool on = i0 + lane < w1;
+            count_digits(cnt[wave], on ? (key[from][i0 + lane] >> shift) & (kBins - 1) : 0, on);
+        }
+        __syncthreads();
+        uint32_t all = 0;
+        if (tid < kBins) {
+#pragma unroll
+            for (int w = 0; w < kSortWaves; ++w) all += cnt[w][tid];
+        }
+        places(cnt, all, 0);
+        for (int i0 = w0; i0 < w1; i0 += 64) {
+            const int i = i0 + lane;
+            const bool on = i < w1;
+            const uint32_t k = on ? key[from][i] : 0u;
+            const uint32_t at = take_place(cnt[wave], (k >> shift) & (kBins - 1), on);
+            if (on) {
+                key[from ^ 1][at] = k;
+                pos[from ^ 1][at] = pos[from][i];
+            }
+        }
+        __syncthreads();
+    }
+    for (int i = tid; i < n; i += kSortThreads) {
+        a.key_out[i] = key[from][i];
+        a.pos_out[i] = pos[from][i];
     }
 }
 
@@ -348,7 +425,10 @@ hipError_t launch_embed_grad(const EmbedArgs& a, void* ws, hipStream_t stream) {
         const unsigned grid = (unsigned)((a.tokens + s.part - 1) / s.part);
         int bits = 1;
         while (a.vocab >> bits) ++bits;                 // the largest key is vocab
-        for (int shift = 0; shift < bits; shift += kDigit, at ^= 1) {
+        s.key_out = key[0];
+        s.pos_out = pos[0];
+        if (a.tokens <= kSmallSort) sort_small_kernel<<<1, kSortThreads, 0, stream>>>(s, bits);
+        for (int shift = a.tokens <= kSmallSort ? bits : 0; shift < bits; shift += kDigit, at ^= 1) {
             s.shift = shift;
             s.key_in = key[at ^ 1];
             s.pos_in = pos[at ^ 1];
@@ -357,7 +437,7 @@ hipError_t launch_embed_grad(const EmbedArgs& a, void* ws, hipStream_t stream) {
             if (shift == 0) sort_kernel<true><<<grid, kSortThreads, 0, stream>>>(s);
             else sort_kernel<false><<<grid, kSortThreads, 0, stream>>>(s);
         }
-        at ^= 1;                                        // where the last pass wrote
+        if (a.tokens > kSmallSort) at ^= 1;             // where the last pass wrote
     }
     if (a.dtype == ZSMR_BF16) grad_launches<ZSMR_BF16>(a, key[at], pos[at], part, stream);
     else grad_launches<ZSMR_FP16>(a, key[at], pos[at], part, stream);

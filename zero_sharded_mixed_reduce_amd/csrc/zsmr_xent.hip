@@ -331,6 +331,9 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
     const int rows = left > TM * 16 ? TM * 16 : (int)left;
     const bool whole = p.vocab - p.v0 - ((int64_t)mt * BM + wm * TM * 16) >= TM * 16;       // of the wave
     if constexpr (EPI == E_STATS) {
+        // the waves' parts, where the main loop's tiles were
+        float2* part = reinterpret_cast<float2*>(smem);
+        __syncthreads();
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
             const int64_t t = n0 + j * 16;
@@ -369,8 +372,15 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
                 for (int r = 0; r < 4; ++r) sum += exp2_of(acc[i][j][r], shift);
 #pragma unroll
             for (int d = 16; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-            if (lane < 16 && t < p.tokens)
-                p.stats[((p.v0 / BM + mt) * WM + wm) * p.tokens + t] = make_float2(sum == 0.f ? -INFINITY : shift, sum);
+            if (lane < 16) part[wm * BN + (wn * TN + j) * 16 + lane] = make_float2(sum == 0.f ? -INFINITY : shift, sum);
+        }
+        __syncthreads();
+        const int64_t t = (int64_t)nt * BN + threadIdx.x;
+        if (threadIdx.x < BN && t < p.tokens) {
+            float2 all = part[threadIdx.x];
+#pragma unroll
+            for (int i = 1; i < WM; ++i) all = join_parts(all, part[i * BN + threadIdx.x]);
+            p.stats[(p.v0 / BM + mt) * p.tokens + t] = all;
         }
     } else if constexpr (EPI == E_GRAD) {
         const float mul = p.mul ? p.mul[0] : p.g_mul;
@@ -448,7 +458,7 @@ __device__ __forceinline__ void put_summary(double sum, double count, float* sum
 }
 
 // Join the parts of each token's softmax: `lanes` tokens of a workgroup (a power
-// of two, at most 64), its groups of lanes share the parts.  A lone workgroup
+// of two), its groups of lanes share the parts.  A lone workgroup
 // has all tokens and leaves the summary too.
 constexpr int kStatsThreads = 1024;
 __global__ __launch_bounds__(kStatsThreads) void stats_kernel(const float2* stats, const float* target,
@@ -460,7 +470,7 @@ __global__ __launch_bounds__(kStatsThreads) void stats_kernel(const float2* stat
     const int64_t t = (int64_t)blockIdx.x * lanes + lane;
     float2 s = make_float2(-INFINITY, 0.f);
     if (t < tokens) {
-        constexpr int kAhead = 8;
+        constexpr int kAhead = 16;
         for (int i = group; i < parts; i += groups * kAhead) {
             float2 p[kAhead];
 #pragma unroll
@@ -476,8 +486,7 @@ __global__ __launch_bounds__(kStatsThreads) void stats_kernel(const float2* stat
         if (group < half) part[threadIdx.x] = s = join_parts(s, part[threadIdx.x + half * lanes]);
         __syncthreads();
     }
-    if (threadIdx.x >= 64) return;
-    const bool on = threadIdx.x < lanes && t < tokens;
+    const bool on = group == 0 && t < tokens;
     const bool counts = on && token_at(labels, id_bytes, t, vocab) >= 0;
     float out = 0.f;
     if (on) {
@@ -487,10 +496,8 @@ __global__ __launch_bounds__(kStatsThreads) void stats_kernel(const float2* stat
         loss[t] = out;
     }
     if (gridDim.x > 1) return;
-    double sum = out;
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) sum += __shfl_down(sum, d);
-    const int count = __popcll(__ballot(counts));
+    const double sum = block_sum<kStatsThreads>(out);
+    const int count = __syncthreads_count(counts);
     if (threadIdx.x == 0) put_summary(sum, count, summary);
 }
 
@@ -584,7 +591,6 @@ int token_tile(int64_t tokens) {
     // 192 where it pads less
     return tiles_of(tokens, 192) * 192 < tiles_of(tokens, 256) * 256 ? 192 : 256;
 }
-int vocab_waves(int64_t tokens) { return tokens <= 64 ? 8 : tokens <= 128 ? 4 : 2; }
 
 // The vocabulary's pieces: G of one takes about 512 MB at most, and the tiles of
 // dw over one fill the 256 CUs a whole number of times if it has that many.
@@ -618,7 +624,7 @@ Space space_of(char* ws, int64_t tokens, int64_t vocab, int64_t width, bool back
         return p;
     };
     const int64_t piece = piece_of(tokens, vocab, width), packed = ceil_to(width, 8);
-    s.stats = reinterpret_cast<float2*>(take(tiles_of(vocab, BM) * vocab_waves(tokens) * tokens * 8));
+    s.stats = reinterpret_cast<float2*>(take(tiles_of(vocab, BM) * tokens * 8));
     s.target = reinterpret_cast<float*>(take(tokens * 4));
     s.x = reinterpret_cast<uint16_t*>(take(tokens * packed * 2));
     s.w = reinterpret_cast<uint16_t*>(take(piece * packed * 2));
@@ -707,8 +713,9 @@ hipError_t forward(const XentArgs& a, void* ws, hipStream_t stream) {
             p.target = s.target;
             launch_product<DT, E_STATS>(p, bn, stream);
         }
-        const int32_t parts = (int32_t)tiles_of(a.vocab, BM) * vocab_waves(a.tokens);
-        int lanes = 64;
+        const int32_t parts = (int32_t)tiles_of(a.vocab, BM);
+        // up to 256 tokens in one workgroup, which saves the launch of the mean
+        int lanes = a.tokens <= 256 ? 256 : 64;
         while (lanes / 2 >= a.tokens) lanes /= 2;
         const unsigned grid = (unsigned)tiles_of(a.tokens, lanes);
         stats_kernel<<<grid, kStatsThreads, 0, stream>>>(s.stats, s.target, a.labels, a.id_bytes, a.tokens,
