@@ -32,6 +32,31 @@ __device__ __forceinline__ uint16_t narrow16(float x) {
     return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
 }
 
+// 16 bytes of any format as fp32 (kVec elements).  KEEP: through the caches,
+// else past them.
+template <int DT>
+constexpr int kVec = DT == ZSMR_FP32 ? 4 : 8;
+template <int DT>
+struct Vec {
+    float f[kVec<DT>];
+};
+template <int DT, bool KEEP>
+__device__ __forceinline__ Vec<DT> load16(const void* p, int64_t e) {
+    Vec<DT> v;
+    if constexpr (DT == ZSMR_FP32) {
+        const f32x4_any* q = reinterpret_cast<const f32x4_any*>(static_cast<const float*>(p) + e);
+        const f32x4 x = KEEP ? *q : __builtin_nontemporal_load(q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v.f[i] = x[i];
+    } else {
+        const u16x8_any* q = reinterpret_cast<const u16x8_any*>(static_cast<const uint16_t*>(p) + e);
+        const u16x8 x = KEEP ? *q : __builtin_nontemporal_load(q);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v.f[i] = widen16<DT>(x[i]);
+    }
+    return v;
+}
+
 // Eight elements of any format as fp32, and back.
 template <int DT>
 __device__ __forceinline__ f32x8 load8(const void* p, int64_t e) {
@@ -67,6 +92,20 @@ __device__ __forceinline__ void store8(void* p, int64_t e, f32x8 f) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[i] = narrow16<DT>(f[i]);
         *reinterpret_cast<u16x8_any*>(static_cast<uint16_t*>(p) + e) = h;
+    }
+}
+// store8 past the caches
+template <int DT>
+__device__ __forceinline__ void stream8(void* p, int64_t e, f32x8 f) {
+    if constexpr (DT == ZSMR_FP32) {
+        f32x4_any* q = reinterpret_cast<f32x4_any*>(static_cast<float*>(p) + e);
+        __builtin_nontemporal_store(f32x4{f[0], f[1], f[2], f[3]}, q);
+        __builtin_nontemporal_store(f32x4{f[4], f[5], f[6], f[7]}, q + 1);
+    } else {
+        u16x8 h;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = narrow16<DT>(f[i]);
+        __builtin_nontemporal_store(h, reinterpret_cast<u16x8_any*>(static_cast<uint16_t*>(p) + e));
     }
 }
 template <int DT>

@@ -35,17 +35,20 @@ __device__ __forceinline__ int item_of(const A& a, int b) {
     return lo;
 }
 
-template <int DT>
+// A lane reads 16 bytes at a time, so that an instruction covers one contiguous
+// KB: past the caches 6.5-6.7 TB/s on MI355X for 498 MB, through them 5.7-6.0.
+template <int DT, bool KEEP>
 __device__ __forceinline__ double chunk_sumsq(const void* p, int64_t e0, int64_t e1) {
+    constexpr int V = kVec<DT>;
     double s0 = 0, s1 = 0;
-    const int64_t body = e0 + (e1 - e0) / 8 * 8;
+    const int64_t body = e0 + (e1 - e0) / V * V;
 #pragma unroll 4
-    for (int64_t e = e0 + threadIdx.x * 8; e < body; e += kThreads * 8) {
-        const f32x8 f = load8<DT>(p, e);
+    for (int64_t e = e0 + threadIdx.x * V; e < body; e += kThreads * V) {
+        const Vec<DT> v = load16<DT, KEEP>(p, e);
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            s0 = __builtin_fma((double)f[i], (double)f[i], s0);
-            s1 = __builtin_fma((double)f[i + 1], (double)f[i + 1], s1);
+        for (int i = 0; i < V; i += 2) {
+            s0 = __builtin_fma((double)v.f[i], (double)v.f[i], s0);
+            s1 = __builtin_fma((double)v.f[i + 1], (double)v.f[i + 1], s1);
         }
     }
     const int64_t e = body + threadIdx.x;
@@ -55,18 +58,31 @@ __device__ __forceinline__ double chunk_sumsq(const void* p, int64_t e0, int64_t
     }
     return s0 + s1;
 }
+template <int DT>
+__device__ __forceinline__ double chunk_sumsq(const void* p, int64_t e0, int64_t e1, bool keep) {
+    return keep ? chunk_sumsq<DT, true>(p, e0, e1) : chunk_sumsq<DT, false>(p, e0, e1);
+}
+
+// The norm reads the list from its start and clipping reads it from its end.
+// The last kKeep chunks (118 MB of 16 bits, 236 MB of fp32) go through the caches
+// both times, so that clipping finds them in the 256 MB Infinity Cache; the
+// others past them, where HBM reads run faster.  Measured on MI355X, 498 MB of
+// fp32, norm + flatten: all through the caches 238 us, none 218, 3,000 chunks
+// 216, 3,600 212.
+constexpr int kKeep = 3600;
 
 // A workgroup takes every gridDim.x-th chunk and leaves one sum.
 __global__ __launch_bounds__(kThreads) void sumsq_kernel(NormArgs a, double* partial) {
     double s = 0;
     for (int b = blockIdx.x; b < a.chunks; b += gridDim.x) {
         const int k = item_of(a, b);
+        const bool keep = b >= a.chunks - kKeep;
         const void* p = a.it[k].p;
         const int64_t e0 = (int64_t)(b - a.it[k].chunk0) * kChunk, n = a.it[k].n;
         const int64_t e1 = e0 + kChunk < n ? e0 + kChunk : n;
-        if (a.it[k].dtype == ZSMR_FP32) s += chunk_sumsq<ZSMR_FP32>(p, e0, e1);
-        else if (a.it[k].dtype == ZSMR_BF16) s += chunk_sumsq<ZSMR_BF16>(p, e0, e1);
-        else s += chunk_sumsq<ZSMR_FP16>(p, e0, e1);
+        if (a.it[k].dtype == ZSMR_FP32) s += chunk_sumsq<ZSMR_FP32>(p, e0, e1, keep);
+        else if (a.it[k].dtype == ZSMR_BF16) s += chunk_sumsq<ZSMR_BF16>(p, e0, e1, keep);
+        else s += chunk_sumsq<ZSMR_FP16>(p, e0, e1, keep);
     }
     s = block_sum<kThreads>(s);
     if (threadIdx.x == 0) partial[blockIdx.x] = s;
@@ -89,18 +105,34 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const double* partia
     }
 }
 
-template <int S, int D>
+template <int S, bool KEEP>
+__device__ __forceinline__ f32x8 clip_load8(const void* p, int64_t e) {
+    f32x8 f;
+#pragma unroll
+    for (int i = 0; i < 8; i += kVec<S>) {
+        const Vec<S> v = load16<S, KEEP>(p, e + i);
+#pragma unroll
+        for (int j = 0; j < kVec<S>; ++j) f[i + j] = v.f[j];
+    }
+    return f;
+}
+template <int S, int D, bool KEEP>
 __device__ __forceinline__ void chunk_clip(const ClipItem& t, int64_t e0, int64_t e1, float c) {
     const int64_t body = e0 + (e1 - e0) / 8 * 8;
 #pragma unroll 4
     for (int64_t e = e0 + threadIdx.x * 8; e < body; e += kThreads * 8) {
-        f32x8 f = load8<S>(t.src, e);
+        f32x8 f = clip_load8<S, KEEP>(t.src, e);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] *= c;
-        store8<D>(t.dst, e, f);
+        stream8<D>(t.dst, e, f);
     }
     const int64_t e = body + threadIdx.x;
     if (e < e1) store1<D>(t.dst, e, load1<S>(t.src, e) * c);
+}
+template <int S, int D>
+__device__ __forceinline__ void chunk_clip(const ClipItem& t, int64_t e0, int64_t e1, float c, bool keep) {
+    if (keep) chunk_clip<S, D, true>(t, e0, e1, c);
+    else chunk_clip<S, D, false>(t, e0, e1, c);
 }
 template <int D>
 __device__ __forceinline__ void chunk_zero(const ClipItem& t, int64_t e0, int64_t e1) {
@@ -110,25 +142,24 @@ __device__ __forceinline__ void chunk_zero(const ClipItem& t, int64_t e0, int64_
 __global__ __launch_bounds__(kThreads) void clip_kernel(ClipArgs a) {
     const float c = a.coef ? *a.coef : 1.0f;
     if (a.in_place && c == 1.0f) return;
-    // from the end: the norm's pass read the list from its start, so what the
-    // Infinity Cache still holds is its end
-    const int b = a.chunks - 1 - (int)blockIdx.x;
+    const int b = blockIdx.x;
+    const bool keep = a.before + b < kKeep;
     const ClipItem t = a.it[item_of(a, b)];
-    const int64_t e0 = (int64_t)(b - t.chunk0) * kChunk;
+    const int64_t e0 = ((t.n - 1) / kChunk - (b - t.chunk0)) * kChunk;      // from the tensor's end
     const int64_t e1 = e0 + kChunk < t.n ? e0 + kChunk : t.n;
     const int s = t.src_dtype, d = t.dst_dtype;
     if (!t.src) {
         chunk_zero<ZSMR_BF16>(t, e0, e1);               // +0 is the same bits in both formats
     } else if (d == ZSMR_FP32) {
-        chunk_clip<ZSMR_FP32, ZSMR_FP32>(t, e0, e1, c);  // in place only
+        chunk_clip<ZSMR_FP32, ZSMR_FP32>(t, e0, e1, c, keep);  // in place only
     } else if (d == ZSMR_BF16) {
-        if (s == ZSMR_FP32) chunk_clip<ZSMR_FP32, ZSMR_BF16>(t, e0, e1, c);
-        else if (s == ZSMR_BF16) chunk_clip<ZSMR_BF16, ZSMR_BF16>(t, e0, e1, c);
-        else chunk_clip<ZSMR_FP16, ZSMR_BF16>(t, e0, e1, c);
+        if (s == ZSMR_FP32) chunk_clip<ZSMR_FP32, ZSMR_BF16>(t, e0, e1, c, keep);
+        else if (s == ZSMR_BF16) chunk_clip<ZSMR_BF16, ZSMR_BF16>(t, e0, e1, c, keep);
+        else chunk_clip<ZSMR_FP16, ZSMR_BF16>(t, e0, e1, c, keep);
     } else {
-        if (s == ZSMR_FP32) chunk_clip<ZSMR_FP32, ZSMR_FP16>(t, e0, e1, c);
-        else if (s == ZSMR_BF16) chunk_clip<ZSMR_BF16, ZSMR_FP16>(t, e0, e1, c);
-        else chunk_clip<ZSMR_FP16, ZSMR_FP16>(t, e0, e1, c);
+        if (s == ZSMR_FP32) chunk_clip<ZSMR_FP32, ZSMR_FP16>(t, e0, e1, c, keep);
+        else if (s == ZSMR_BF16) chunk_clip<ZSMR_BF16, ZSMR_FP16>(t, e0, e1, c, keep);
+        else chunk_clip<ZSMR_FP16, ZSMR_FP16>(t, e0, e1, c, keep);
     }
 }
 

@@ -87,25 +87,33 @@ struct Batches {
 int32_t clip(const void* const* ptrs, void* const* in_place, const int64_t* numels,
              const int32_t* dtypes, int32_t n, const float* coef, uint16_t* flat,
              int64_t flat_numel, int32_t flat_dtype, hipStream_t stream) {
-    auto launch = [&](const ClipArgs& a) { return launch_clip(a, stream); };
+    int64_t before = 0;
+    auto launch = [&](ClipArgs& a) {
+        a.before = before;
+        before += a.chunks;
+        return launch_clip(a, stream);
+    };
     Batches<kClipBatch, ClipArgs, ClipItem, decltype(launch)> b(launch);
     b.a.coef = coef;
     b.a.in_place = in_place != nullptr;
-    int64_t at = 0;
-    for (int32_t i = 0; i < n; ++i) {
+    // from the list's end to its start, which the kernel's reads count on
+    int64_t at = flat_numel;
+    if (!in_place) {
+        for (int32_t i = 0; i < n; ++i) at -= numels[i];
+        ClipItem pad{};
+        pad.dst = flat + (flat_numel - at);
+        pad.src_dtype = pad.dst_dtype = (int16_t)flat_dtype;
+        b.add(pad, at);
+        at = flat_numel - at;
+    }
+    for (int32_t i = n - 1; i >= 0; --i) {
+        at -= numels[i];
         ClipItem it{};
         it.src = ptrs[i];
         it.dst = in_place ? in_place[i] : flat + at;
         it.src_dtype = (int16_t)dtypes[i];
         it.dst_dtype = (int16_t)(in_place ? dtypes[i] : flat_dtype);
         b.add(it, numels[i]);
-        at += numels[i];
-    }
-    if (!in_place) {
-        ClipItem pad{};
-        pad.dst = flat + at;
-        pad.src_dtype = pad.dst_dtype = (int16_t)flat_dtype;
-        b.add(pad, flat_numel - at);
     }
     b.go();
     return done(b.err);
@@ -261,7 +269,7 @@ int32_t zsmr_grad_norm(const void* const* ptrs, const int64_t* numels, const int
     if ((st = check_space(ws, ws_bytes, chunks * 8))) return st;
     double* partial = static_cast<double*>(ws);
     int64_t at = 0;
-    auto launch = [&](const NormArgs& a) {
+    auto launch = [&](NormArgs& a) {
         const hipError_t e = launch_sumsq(a, partial + at, stream);
         at += sumsq_grid(a.chunks);
         return e;

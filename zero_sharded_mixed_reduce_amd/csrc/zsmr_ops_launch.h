@@ -34,6 +34,7 @@ struct NormArgs {
 struct ClipArgs {
     ClipItem it[kClipBatch];
     int32_t count, chunks;
+    int64_t before;                 // chunks of the launches before this one
     const float* coef;
     int32_t in_place;
 };
