@@ -78,8 +78,8 @@ __global__ __launch_bounds__(kThreads) void sumsq_kernel(NormArgs a, double* par
         const int k = item_of(a, b);
         const bool keep = b >= a.chunks - kKeep;
         const void* p = a.it[k].p;
-        const int64_t e0 = (int64_t)(b - a.it[k].chunk0) * kChunk, n = a.it[k].n;
-        const int64_t e1 = e0 + kChunk < n ? e0 + kChunk : n;
+        const int64_t e0 = (int64_t)(b - a.it[k].chunk0) * a.chunk, n = a.it[k].n;
+        const int64_t e1 = e0 + a.chunk < n ? e0 + a.chunk : n;
         if (a.it[k].dtype == ZSMR_FP32) s += chunk_sumsq<ZSMR_FP32>(p, e0, e1, keep);
         else if (a.it[k].dtype == ZSMR_BF16) s += chunk_sumsq<ZSMR_BF16>(p, e0, e1, keep);
         else s += chunk_sumsq<ZSMR_FP16>(p, e0, e1, keep);
@@ -88,14 +88,13 @@ __global__ __launch_bounds__(kThreads) void sumsq_kernel(NormArgs a, double* par
     if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
-constexpr int kJoinThreads = 1024;
-__global__ __launch_bounds__(kJoinThreads) void join_kernel(const double* partial, int64_t n,
-                                                            double* sumsq, double max_norm,
-                                                            double eps, float* norm_coef) {
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void join_kernel(const double* partial, int64_t n, double* sumsq,
+                                                       double max_norm, double eps, float* norm_coef) {
     double s = 0;
 #pragma unroll 8
-    for (int64_t i = threadIdx.x; i < n; i += kJoinThreads) s += partial[i];
-    s = block_sum<kJoinThreads>(s);
+    for (int64_t i = threadIdx.x; i < n; i += THREADS) s += partial[i];
+    s = block_sum<THREADS>(s);
     if (threadIdx.x != 0) return;
     if (sumsq) *sumsq = s;
     if (norm_coef) {
@@ -145,8 +144,8 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(ClipArgs a) {
     const int b = blockIdx.x;
     const bool keep = a.before + b < kKeep;
     const ClipItem t = a.it[item_of(a, b)];
-    const int64_t e0 = ((t.n - 1) / kChunk - (b - t.chunk0)) * kChunk;      // from the tensor's end
-    const int64_t e1 = e0 + kChunk < t.n ? e0 + kChunk : t.n;
+    const int64_t e0 = ((t.n - 1) / a.chunk - (b - t.chunk0)) * a.chunk;    // from the tensor's end
+    const int64_t e1 = e0 + a.chunk < t.n ? e0 + a.chunk : t.n;
     const int s = t.src_dtype, d = t.dst_dtype;
     if (!t.src) {
         chunk_zero<ZSMR_BF16>(t, e0, e1);               // +0 is the same bits in both formats
@@ -401,17 +400,19 @@ hipError_t launch_clip(const ClipArgs& a, hipStream_t stream) {
 
 hipError_t launch_join(const double* partial, int64_t n, double* sumsq, double max_norm,
                        double eps, float* norm_coef, hipStream_t stream) {
-    join_kernel<<<1, kJoinThreads, 0, stream>>>(partial, n, sumsq, max_norm, eps, norm_coef);
+    // one wave where it has few sums to add: nothing to wait for between waves
+    if (n <= 512) join_kernel<64><<<1, 64, 0, stream>>>(partial, n, sumsq, max_norm, eps, norm_coef);
+    else join_kernel<1024><<<1, 1024, 0, stream>>>(partial, n, sumsq, max_norm, eps, norm_coef);
     return hipGetLastError();
 }
 
 namespace {
 template <int DT>
-void reduce_launches(const StepArgs& a, double* partial, double* sumsq, hipStream_t stream) {
+hipError_t reduce_launches(const StepArgs& a, double* partial, double* sumsq, hipStream_t stream) {
     // one workgroup: 8 elements a lane, or twice that
     if (a.n <= 2 * kSmall * 8) {
         reduce_sumsq_small_kernel<DT><<<1, kSmall, 0, stream>>>(a, sumsq);
-        return;
+        return hipGetLastError();
     }
     int64_t parts = (a.n + kTile - 1) / kTile;
     int device = 0, cus = 0;
@@ -424,15 +425,14 @@ void reduce_launches(const StepArgs& a, double* partial, double* sumsq, hipStrea
     } else {
         reduce_sumsq_kernel<DT><<<(unsigned)parts, kThreads, 0, stream>>>(a, partial);
     }
-    join_kernel<<<1, kJoinThreads, 0, stream>>>(partial, parts, sumsq, 0, 0, nullptr);
+    return launch_join(partial, parts, sumsq, 0, 0, nullptr, stream);
 }
 }  // namespace
 
 hipError_t launch_reduce_sumsq(int dtype, const StepArgs& a, double* partial, double* sumsq,
                                hipStream_t stream) {
-    if (dtype == ZSMR_BF16) reduce_launches<ZSMR_BF16>(a, partial, sumsq, stream);
-    else reduce_launches<ZSMR_FP16>(a, partial, sumsq, stream);
-    return hipGetLastError();
+    return dtype == ZSMR_BF16 ? reduce_launches<ZSMR_BF16>(a, partial, sumsq, stream)
+                              : reduce_launches<ZSMR_FP16>(a, partial, sumsq, stream);
 }
 
 hipError_t launch_clipped(int dtype, const StepArgs& a, const float* coef, hipStream_t stream) {

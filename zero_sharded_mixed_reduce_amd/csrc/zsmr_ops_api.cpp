@@ -1,6 +1,7 @@
 // Host side of the operators declared in include/zsmr_ops.h: every argument is
 // checked here, then the launches of zsmr_ops_launch.h go to the caller's
 // stream.  No device memory is allocated and nothing is kept between calls.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -44,9 +45,8 @@ int32_t check_clip(double max_norm, double eps, const float* norm_coef) {
     return al(norm_coef, 4) ? ZSMR_OK : ZSMR_ERR_ALIGN;
 }
 
-int64_t chunks_of(int64_t n) { return ceil_div(n, kChunk); }
-
-// A list's tensors; *total gets their elements, *chunks their chunks.
+// A list's tensors; *total gets their elements, *chunks the most chunks they can
+// have.
 int32_t check_list(const void* const* ptrs, const int64_t* numels, const int32_t* dtypes,
                    int32_t n, int64_t* total, int64_t* chunks) {
     *total = *chunks = 0;
@@ -56,7 +56,7 @@ int32_t check_list(const void* const* ptrs, const int64_t* numels, const int32_t
         if (dtypes[i] != ZSMR_FP32 && !dtype_ok(dtypes[i])) return ZSMR_ERR_DTYPE;
         if (!al(ptrs[i], dtypes[i] == ZSMR_FP32 ? 4 : 2)) return ZSMR_ERR_ALIGN;
         *total += numels[i];
-        *chunks += chunks_of(numels[i]);
+        *chunks += ceil_div(numels[i], kChunk);
         if (*total > ZSMR_MAX_NUMEL || *chunks > INT32_MAX) return ZSMR_ERR_ARG;
     }
     return ZSMR_OK;
@@ -69,13 +69,13 @@ struct Batches {
     A a{};
     F flush;
     hipError_t err = hipSuccess;
-    explicit Batches(F f) : flush(f) {}
+    Batches(F f, int64_t total) : flush(f) { a.chunk = chunk_of_list(total); }
     void add(Item it, int64_t n) {
         if (n == 0 || err != hipSuccess) return;
         it.chunk0 = a.chunks;
         it.n = n;
         a.it[a.count++] = it;
-        a.chunks += (int32_t)chunks_of(n);
+        a.chunks += (int32_t)ceil_div(n, a.chunk);
         if (a.count == BATCH) go();
     }
     void go() {
@@ -86,25 +86,24 @@ struct Batches {
 
 int32_t clip(const void* const* ptrs, void* const* in_place, const int64_t* numels,
              const int32_t* dtypes, int32_t n, const float* coef, uint16_t* flat,
-             int64_t flat_numel, int32_t flat_dtype, hipStream_t stream) {
+             int64_t flat_numel, int32_t flat_dtype, int64_t total, hipStream_t stream) {
     int64_t before = 0;
     auto launch = [&](ClipArgs& a) {
         a.before = before;
         before += a.chunks;
         return launch_clip(a, stream);
     };
-    Batches<kClipBatch, ClipArgs, ClipItem, decltype(launch)> b(launch);
+    Batches<kClipBatch, ClipArgs, ClipItem, decltype(launch)> b(launch, total);
     b.a.coef = coef;
     b.a.in_place = in_place != nullptr;
     // from the list's end to its start, which the kernel's reads count on
-    int64_t at = flat_numel;
+    int64_t at = 0;
     if (!in_place) {
-        for (int32_t i = 0; i < n; ++i) at -= numels[i];
         ClipItem pad{};
-        pad.dst = flat + (flat_numel - at);
+        pad.dst = flat + total;
         pad.src_dtype = pad.dst_dtype = (int16_t)flat_dtype;
-        b.add(pad, at);
-        at = flat_numel - at;
+        b.add(pad, flat_numel - total);
+        at = total;
     }
     for (int32_t i = n - 1; i >= 0; --i) {
         at -= numels[i];
@@ -255,8 +254,9 @@ int32_t zsmr_xent_backward(const void* x, int64_t x_stride, const void* w, int64
 int64_t zsmr_norm_workspace(int64_t total, int32_t n_tensors) {
     if (total < 0 || total > ZSMR_MAX_NUMEL || n_tensors < 0) return -1;
     // one fp64 a chunk of a list (each tensor ends one) or a tile of a shard
-    const int64_t lists = total / kChunk + n_tensors, shard = ceil_div(total, kTile);
-    return 8 * (lists > shard ? lists : shard);
+    const int64_t short_list = total < kShortList ? total : kShortList;
+    const int64_t lists = std::max(total / kChunk, short_list / kShortChunk) + n_tensors;
+    return 8 * std::max(lists, ceil_div(total, kTile));
 }
 
 int32_t zsmr_grad_norm(const void* const* ptrs, const int64_t* numels, const int32_t* dtypes,
@@ -266,6 +266,10 @@ int32_t zsmr_grad_norm(const void* const* ptrs, const int64_t* numels, const int
     int32_t st = check_list(ptrs, numels, dtypes, n, &total, &chunks);
     if (st) return st;
     if ((st = check_clip(max_norm, eps, norm_coef))) return st;
+    if (total <= kShortList) {
+        chunks = 0;
+        for (int32_t i = 0; i < n; ++i) chunks += ceil_div(numels[i], kShortChunk);
+    }
     if ((st = check_space(ws, ws_bytes, chunks * 8))) return st;
     double* partial = static_cast<double*>(ws);
     int64_t at = 0;
@@ -274,7 +278,7 @@ int32_t zsmr_grad_norm(const void* const* ptrs, const int64_t* numels, const int
         at += sumsq_grid(a.chunks);
         return e;
     };
-    Batches<kNormBatch, NormArgs, NormItem, decltype(launch)> b(launch);
+    Batches<kNormBatch, NormArgs, NormItem, decltype(launch)> b(launch, total);
     for (int32_t i = 0; i < n; ++i) {
         NormItem it{};
         it.p = ptrs[i];
@@ -302,7 +306,7 @@ int32_t zsmr_clip_grads(void* const* ptrs, const int64_t* numels, const int32_t*
     if (st) return st;
     if (!coef) return ZSMR_ERR_ARG;
     if (!al(coef, 4)) return ZSMR_ERR_ALIGN;
-    return clip(const_cast<const void* const*>(ptrs), ptrs, numels, dtypes, n, coef, nullptr, 0, 0, stream);
+    return clip(const_cast<const void* const*>(ptrs), ptrs, numels, dtypes, n, coef, nullptr, 0, 0, total, stream);
 }
 
 int32_t zsmr_clip_flatten(const void* const* ptrs, const int64_t* numels, const int32_t* dtypes,
@@ -313,11 +317,11 @@ int32_t zsmr_clip_flatten(const void* const* ptrs, const int64_t* numels, const 
     if (st) return st;
     if (!dtype_ok(flat_dtype)) return ZSMR_ERR_DTYPE;
     if (flat_numel < total || flat_numel > ZSMR_MAX_NUMEL || (flat_numel > 0 && !flat) ||
-        chunks + chunks_of(flat_numel - total) > INT32_MAX)
+        ceil_div(flat_numel, kShortChunk) > INT32_MAX)
         return ZSMR_ERR_ARG;
     if (!al(flat, 2) || !al(coef, 4)) return ZSMR_ERR_ALIGN;
     return clip(ptrs, nullptr, numels, dtypes, n, coef, static_cast<uint16_t*>(flat), flat_numel,
-                flat_dtype, stream);
+                flat_dtype, total, stream);
 }
 
 int32_t zero_reduce_shard_sumsq(zsmr_ctx* c, int32_t rank, int32_t unit, const void* grads,

@@ -9,7 +9,12 @@
 namespace zsmr {
 
 // ---- norm and clipping (zsmr_norm.hip)
-constexpr int kChunk = 16384;       // elements of a list tensor one workgroup handles
+// Elements of a list tensor one workgroup handles at a time: few in a short
+// list, whose call is as long as one workgroup takes.  Measured on MI355X, 54
+// tensors of 0.25M fp32, norm + flatten: CHUNKNUMBERS
+constexpr int kChunk = 16384, kShortChunk = 2048;
+constexpr int64_t kShortList = int64_t(1) << 22;
+inline int chunk_of_list(int64_t total) { return total <= kShortList ? kShortChunk : kChunk; }
 constexpr int kTile = 2048;         // elements of a shard one workgroup handles
 struct NormItem {
     const void* p;
@@ -29,11 +34,11 @@ struct ClipItem {
 constexpr int kNormBatch = 160, kClipBatch = 120;
 struct NormArgs {
     NormItem it[kNormBatch];
-    int32_t count, chunks;
+    int32_t count, chunks, chunk;
 };
 struct ClipArgs {
     ClipItem it[kClipBatch];
-    int32_t count, chunks;
+    int32_t count, chunks, chunk;
     int64_t before;                 // chunks of the launches before this one
     const float* coef;
     int32_t in_place;

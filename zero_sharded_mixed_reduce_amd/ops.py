@@ -63,8 +63,8 @@ def _lib():
 
 
 def _raw(name: str):
-    """An entry point whose integers all come from tensors, so that none can
-    be outside its C type: the check, 2 us a call, is left out."""
+    """An entry point whose integers come from tensors or are checked by its
+    caller: the general check, 2 us a call, is left out."""
     fn = _RAW.get(name)
     if fn is None:
         fn = _RAW[name] = getattr(_lib(), name).fn
@@ -270,15 +270,39 @@ def zsmr_clip_flatten(tensors, coef, flat, stream=None) -> None:
         _z._check(code, "zsmr_clip_flatten")
 
 
+def _piece(x, n: int, size: int, what: str) -> Optional[int]:
+    """Address of n elements of `size` bytes (raw addresses are the caller's to
+    check)."""
+    if x is None or isinstance(x, int):
+        return x
+    if not x.is_contiguous() or x.numel() * x.element_size() < n * size:
+        _z._fits(x, n, size, what)
+    return _ptr(x)
+
+
+_I32, _I64 = 1 << 31, 1 << 63
+
+
+def _checked_ints(name: str, i32, i64=()) -> None:
+    for x in i32:
+        if not -_I32 <= x < _I32:
+            raise ValueError(f"{name}: {x} is outside int32")
+    for x in i64:
+        if not -_I64 <= x < _I64:
+            raise ValueError(f"{name}: {x} is outside int64")
+
+
 def zero_reduce_shard_sumsq(ctx, rank: int, unit: int, grads, row_stride: int, base_elem: int,
                             mean: bool, g_out, sumsq, ws, stream=None) -> None:
+    _checked_ints("zero_reduce_shard_sumsq", (rank, unit), (row_stride, base_elem))
     n = _z._piece_len(ctx, rank, unit)
     _z._rows_fit(ctx, grads, row_stride, base_elem, n, "grads")
-    _z._fits(g_out, n, 4, "g_out")
-    _z._check(_lib().zero_reduce_shard_sumsq(ctx.handle, rank, unit, _ptr(grads), int(row_stride),
-                                             int(base_elem), 1 if mean else 0, _ptr(g_out),
-                                             _vector(sumsq, 1, torch.float64, "sumsq"), *_space(ws),
-                                             _z._stream(stream)), "zero_reduce_shard_sumsq")
+    code = _raw("zero_reduce_shard_sumsq")(ctx.handle, rank, unit, _ptr(grads), row_stride, base_elem,
+                                           1 if mean else 0, _piece(g_out, n, 4, "g_out"),
+                                           _vector(sumsq, 1, torch.float64, "sumsq"), *_space(ws),
+                                           _z._stream(stream))
+    if code:
+        _z._check(code, "zero_reduce_shard_sumsq")
 
 
 @functools.lru_cache(maxsize=16)
@@ -288,13 +312,12 @@ def _adam_ref(lr: float, beta1: float, beta2: float, eps: float):
 
 def zero_clipped_step(ctx, rank: int, unit: int, g, coef, master, m, v, p16_dst, t: int, lr: float,
                       betas=(0.9, 0.999), eps: float = 1e-8, stream=None) -> None:
+    _checked_ints("zero_clipped_step", (rank, unit, t))
     n = _z._piece_len(ctx, rank, unit)
-    _z._fits(g, n, 4, "g")
-    _z._fits(master, n, 4, "master")
-    _z._fits(m, n, 4, "m")
-    _z._fits(v, n, 4, "v")
-    _z._fits(p16_dst, n, 2, "p16_dst")
-    _z._check(_lib().zero_clipped_step(ctx.handle, rank, unit, _ptr(g),
-                                       _vector(coef, 1, torch.float32, "coef"), _ptr(master), _ptr(m),
-                                       _ptr(v), _ptr(p16_dst), int(t), _adam_ref(lr, *betas, eps),
-                                       _z._stream(stream)), "zero_clipped_step")
+    code = _raw("zero_clipped_step")(ctx.handle, rank, unit, _piece(g, n, 4, "g"),
+                                     _vector(coef, 1, torch.float32, "coef"),
+                                     _piece(master, n, 4, "master"), _piece(m, n, 4, "m"),
+                                     _piece(v, n, 4, "v"), _piece(p16_dst, n, 2, "p16_dst"), t,
+                                     _adam_ref(lr, *betas, eps), _z._stream(stream))
+    if code:
+        _z._check(code, "zero_clipped_step")
