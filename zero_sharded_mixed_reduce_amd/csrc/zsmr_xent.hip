@@ -298,11 +298,11 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
     if (steps > 0) {
         ta.load(smem, true);
         tb.load(smem + TA::kBytes, true);
-        ZSMR_WAIT(0);
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
         ta.load(smem + kStage, steps > 1);
         tb.load(smem + kStage + TA::kBytes, steps > 1);
+        ZSMR_WAIT(kLoads);              // the first step's
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
         read(a0, b0, smem, 0);
     }
     for (int s = 0; s < steps; ++s) {
