@@ -474,6 +474,48 @@ def test_clipped_step_has_the_bits_of_the_plain_steps(numel, world, dt, pad, shi
     assert a["ag_elems"] == b["ag_elems"] + (S if world > 1 else 0)
 
 
+@pytest.mark.parametrize("world,extra,shift,dt", [(16, 0, 0, "bf16"), (17, 511, 1, "fp16"), (24, 5, 3, "bf16")])
+def test_windowed_reduce(world, extra, shift, dt):
+    """One rank's large shard with many rows, whose results are stored in write
+    windows: the bits of zero_reduce_shard and the sum of their squares."""
+    n, t = 1024 * 18 * 512 + extra, T16[dt]
+    g = gen(10)
+    ctx = z.zero_init_shards(n * world, world, z.ZSMR_ZERO2, dt)
+    raw = torch.randn(world * (n + shift) + 8, generator=g, device="cuda", dtype=t).mul_(0.01)[shift:]
+    red = torch.full((n + 16,), 7.0, device="cuda")
+    want, sums = torch.empty(n, device="cuda"), torch.empty(1, device="cuda", dtype=torch.float64)
+    size = z.zsmr_norm_workspace(n, 1)
+    ws, guard = space(size)
+    z.zero_reduce_shard(ctx, 1, 0, raw, n + shift, 0, True, want)
+    for _ in range(2):
+        z.zero_reduce_shard_sumsq(ctx, 1, 0, raw, n + shift, 0, True, red, sums, ws)
+        assert torch.equal(red[:n].view(torch.int32), want.view(torch.int32))
+        exact = float(want.double().square().sum())
+        assert abs(float(sums) - exact) <= 1e-11 * exact
+    assert bool((red[n:] == 7).all())
+    intact(guard, size)
+
+
+@pytest.mark.parametrize("sizes", [[40_000_003, 5, 30_000_000], [1] + [9_000_000] * 8])
+def test_norm_clip_flatten_of_long_lists(sizes):
+    """More chunks than workgroups, and than what is kept in the caches."""
+    xs = tensor_list(sizes, (torch.bfloat16,))
+    total = sum(sizes)
+    size = z.zsmr_norm_workspace(total, len(xs))
+    ws, guard = space(size)
+    out = torch.empty(2, device="cuda")
+    z.zsmr_grad_norm(xs, 1.0, out, ws)
+    intact(guard, size)
+    norm = math.sqrt(sum(float(x.double().square().sum()) for x in xs))
+    assert abs(out[0].item() - norm) <= 2 * U * norm
+    flat = torch.empty(total + 20_001, device="cuda", dtype=torch.float16)
+    z.zsmr_clip_flatten(xs, out[1:], flat)
+    want = (torch.cat(xs).float() * out[1]).half()
+    assert torch.equal(flat[:total], want) and not bool(flat[total:].any())
+    z.zsmr_clip_grads(xs, out[1:])
+    assert torch.equal(torch.cat(xs), (torch.cat(tensor_list(sizes, (torch.bfloat16,))).float() * out[1]).bfloat16())
+
+
 def test_join_of_many_sums():
     sums = torch.rand(5000, device="cuda", dtype=torch.float64)
     out = torch.empty(2, device="cuda")
@@ -537,3 +579,42 @@ def test_stream_and_graph(n, vocab, width):
             assert torch.equal(captured[k], want[k]), k
         chain(None, w, table, ids, labels, eager)
         torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------- example --
+def test_example_trains_and_matches_a_plain_step():
+    """The example's first step against the same step in 64 bits, and its loss
+    falls over the next ones."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "bigram.py")
+    spec = importlib.util.spec_from_file_location("bigram", path)
+    bigram = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(bigram)
+    torch.manual_seed(1)
+    vocab, width, n, world = 301, 40, 130, 3
+    model = bigram.Bigram(vocab, width, n, world, 0.05, 1e-2)
+    g = gen(11)
+    successor = torch.randperm(vocab, generator=g, device="cuda")
+    x, y = bigram.batch(successor, world, n, g)
+    params = model.params[:2 * vocab * width].double().requires_grad_()
+    master = model.master.double()
+    e, w = params.view(2, vocab, width)
+    rows = []
+    for r in range(world):
+        loss = torch.nn.functional.cross_entropy(e[x[r]] @ w.t(), y[r], ignore_index=-1)
+        rows.append(torch.autograd.grad(loss, params, retain_graph=r + 1 < world)[0])
+    grad = torch.stack(rows).mean(0)
+    norm = float(grad.norm())
+    loss, norm_coef = model.step(x, y)
+    # three 16-bit roundings a gradient element (G, dx, the row): their sum in the norm
+    assert abs(norm_coef[0].item() - norm) <= 3 * half(torch.bfloat16) * norm
+    coef = 0.05 / (norm + 1e-6)
+    assert abs(norm_coef[1].item() - coef) <= 3 * half(torch.bfloat16) * coef
+    # the first Adam step moves by lr * g / (|g| + eps'): compare where g is not near zero
+    big = grad.abs() * coef > 1e-5
+    moved = (model.master[:grad.numel()].double() - master[:grad.numel()])[big]
+    assert float((moved + 1e-2 * torch.sign(grad[big])).abs().max()) < 1e-4
+    assert torch.equal(model.params, model.master.to(torch.bfloat16))
+    losses, _ = bigram.train(vocab=500, width=64, tokens=1000, world=2, steps=40, say=lambda *_: None)
+    assert losses[0] > 0.9 * math.log(500) and losses[-1] < 0.5 * losses[0]

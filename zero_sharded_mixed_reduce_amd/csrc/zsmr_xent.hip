@@ -330,10 +330,43 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
     const int64_t left = p.vocab - p.v0 - m0;
     const int rows = left > TM * 16 ? TM * 16 : (int)left;
     const bool whole = p.vocab - p.v0 - ((int64_t)mt * BM + wm * TM * 16) >= TM * 16;       // of the wave
+    // 16-bit results leave through LDS, as [n][m] where the main loop's tiles
+    // were (chunk c of row n in slot c ^ (n % 32)): a lane holds 8 bytes of 16
+    // different rows of memory, and stored like that each write is a quarter of
+    // a line.  From LDS a wave stores two rows of 512 bytes at a time.
+    // (FIGURES)
+    auto stage = [&](int i, int j, u16x4 h) {
+        const int n = (wn * TN + j) * 16 + lane % 16, c = (wm * TM + i) * 2 + lane / 32;
+        *reinterpret_cast<u16x4*>(smem + n * (BM * 2) + (c ^ (n & 31)) * 16 + (lane / 16 & 1) * 8) = h;
+    };
+    // rows: of the tile; cols: from its first on
+    auto store_tile = [&](uint16_t* out, int64_t ld, int64_t rows, int64_t cols) {
+        __syncthreads();
+#pragma unroll 4
+        for (int q = threadIdx.x; q < BN * (BM / 8); q += kThreads) {
+            const int n = q / (BM / 8), c = q % (BM / 8);
+            if (n >= rows || c * 8 >= cols) continue;
+            const u16x8 h = *reinterpret_cast<const u16x8*>(smem + n * (BM * 2) + (c ^ (n & 31)) * 16);
+            uint16_t* o = out + n * ld + c * 8;
+            if (c * 8 + 8 <= cols) {
+                *reinterpret_cast<u16x8_any*>(o) = h;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (c * 8 + k < cols) o[k] = h[k];
+            }
+        }
+    };
+    auto narrow4 = [&](f32x4 f) {
+        u16x4 h;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) h[r] = narrow16<DT>(f[r]);
+        return h;
+    };
+    __syncthreads();        // every wave's last loads are in
     if constexpr (EPI == E_STATS) {
         // the waves' parts, where the main loop's tiles were
         float2* part = reinterpret_cast<float2*>(smem);
-        __syncthreads();
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
             const int64_t t = n0 + j * 16;
@@ -393,7 +426,6 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
             const int mine = label >= 0 && far >= 0 && far < rows && (far & 12) == 0 ? (int)far : -1;
             const bool none = label < 0;
             const float shift = p.lse[t] * kLog2e, weight = (p.grad ? p.grad[t] : 1.f) * mul;
-            uint16_t* g = p.g + t * p.ldg + m0;
             const bool has = __any(mine >= 0);
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
@@ -405,20 +437,19 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
                     for (int r = 0; r < 4; ++r)
                         if (i * 16 + r == mine) f[r] -= 1.f;
                 }
-                u16x4 h;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) h[r] = narrow16<DT>(f[r] * weight);
+                u16x4 h = narrow4(f * weight);
                 if (none) h = 0;
                 if (!whole) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         if (i * 16 + r >= rows) h[r] = 0;
                 }
-                *reinterpret_cast<u16x4*>(g + i * 16) = h;      // ldg is a multiple of the tile
+                stage(i, j, h);
             }
         }
-    } else if constexpr (EPI == E_DX) {
-        const float mul = out_mul(p);
+        // ldg is a multiple of the tile: past the vocabulary there are zeros
+        store_tile(p.g + (int64_t)nt * BN * p.ldg + (int64_t)mt * BM, p.ldg, p.tokens - (int64_t)nt * BN, BM);
+    } else if (EPI == E_DX && p.sum_out) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
             const int64_t t = n0 + j * 16;
@@ -430,22 +461,34 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
                 if (h >= p.width) continue;
                 f32x4 f = acc[i][j];
                 if (p.sum_in) f += *reinterpret_cast<const f32x4*>(s + h);
-                if (p.sum_out) *reinterpret_cast<f32x4*>(s + h) = f;
-                else put4<DT>(p.out + t * p.ldo, h, p.width, f * mul, false);
+                *reinterpret_cast<f32x4*>(s + h) = f;
             }
         }
     } else {
+        // dx's last piece, or dw: rows of the result are columns of the tile
         const float mul = out_mul(p);
+        const int64_t rows = EPI == E_DX ? p.tokens : p.vocab - p.v0;
+        uint16_t* out = EPI == E_DX ? p.out : p.out + p.v0 * p.ldo;
+        const bool add = EPI == E_DW && p.accumulate;
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-            const int64_t v = p.v0 + n0 + j * 16;
-            if (v >= p.vocab) continue;
+            const int64_t n = n0 + j * 16;
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
                 const int64_t h = m0 + i * 16;
-                if (h < p.width) put4<DT>(p.out + v * p.ldo, h, p.width, acc[i][j] * mul, p.accumulate);
+                f32x4 f = acc[i][j];
+                if (EPI == E_DX && p.sum_in && n < rows && h < p.width)
+                    f += *reinterpret_cast<const f32x4*>(p.sum + n * p.lds + h);
+                // what is added to has to be added before the one rounding
+                if (add) {
+                    if (n < rows && h < p.width) put4<DT>(out + n * p.ldo, h, p.width, f * mul, true);
+                } else {
+                    stage(i, j, narrow4(f * mul));
+                }
             }
         }
+        const int64_t first = (int64_t)nt * BN, col = (int64_t)mt * BM;
+        if (!add) store_tile(out + first * p.ldo + col, p.ldo, rows - first, p.width - col);
     }
 #endif
 }
@@ -595,8 +638,10 @@ int token_tile(int64_t tokens) {
 // The vocabulary's pieces: G of one takes about 512 MB at most, and the tiles of
 // dw over one fill the 256 CUs a whole number of times if it has that many.
 constexpr int64_t kCus = 256;
+constexpr int64_t kMaxPiece = int64_t(1) << 21;     // G's rows: byte offsets within a tile fit 31 bits
 int64_t piece_of(int64_t tokens, int64_t vocab, int64_t width) {
     int64_t tiles = std::max<int64_t>(1, (int64_t(1) << 28) / std::max<int64_t>(tokens, 1) / BM);
+    tiles = std::min<int64_t>(tiles, kMaxPiece / BM);
     if (tiles >= tiles_of(vocab, BM)) return ceil_to(vocab, BM);
     const int64_t across = tiles_of(width, BM), rounds = tiles * across / kCus;
     if (rounds > 0) tiles = rounds * kCus / across;
