@@ -86,11 +86,11 @@ struct Tile {
     __device__ __forceinline__ void init(const Mat& m, int64_t at, int64_t k0) {
         const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
         if constexpr (OUTER) {
-            static_assert(!OUTER || R == 256, "k-outer tiles are 256 wide");
+            static_assert(!OUTER || R == 128 || R == 256, "a wave's load is whole rows of k");
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                const int k = (wave + kWaves * i) * 2 + lane / 32;
-                const int chunk = (lane % 32) ^ swizzle(k);
+                const int k = (wave + kWaves * i) * (512 / R) + lane / (R / 8);
+                const int chunk = (lane % (R / 8)) ^ swizzle(k);
                 // columns past the end are no part of any result, but their
                 // addresses must stay inside the operand
                 off[i] = at + chunk * 8 < m.cols ? (uint32_t)(k * m.ld * 2 + chunk * 16) : 0x80000000u;
@@ -114,6 +114,8 @@ struct Tile {
     }
     // Start the loads of one step into `to` (kBytes of LDS) and move on; `on`
     // false: the same instructions, which read nothing and write zeros.
+    // AUX: 2 for operands that are read once, past the caches.
+    template <int AUX>
     __device__ __forceinline__ void load(char* to, bool on) {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
         const int bound = !on || left < 0 ? 0 : left > 0x7fffffff ? 0x7fffffff : (int)left;
@@ -125,7 +127,7 @@ struct Tile {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(to + (wave + kWaves * i) * 1024), 16,
-                                                     past ? 0x80000000u : off[i], 0, 0, 0);
+                                                     past ? 0x80000000u : off[i], 0, 0, AUX);
         base += step;
         left -= step;
         k_left -= BK;
@@ -238,6 +240,9 @@ template <int DT, int EPI, int BN, int WM>
 __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
 #if defined(__HIP_DEVICE_COMPILE__)     // the scheduling hints have no host form
     constexpr bool A_OUTER = EPI == E_DX || EPI == E_DW, B_OUTER = EPI == E_DW;
+    // A tile that holds all tokens reads the weights once: past the caches 1.05 GB
+    // took 160 us on MI355X (16 tokens), through them 177.
+    constexpr int kStream = EPI != E_DW && BN <= 128 ? 2 : 0;
     constexpr int WN = kWaves / WM, TM = BM / WM / 16, TN = BN / WN / 16;
     typedef Tile<BM, A_OUTER> TA;
     typedef Tile<BN, B_OUTER> TB;
@@ -296,10 +301,10 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
             for (int j = 0; j < TN; ++j) acc[i][j] = mfma<DT>(a[i], b[j], acc[i][j]);
     };
     if (steps > 0) {
-        ta.load(smem, true);
-        tb.load(smem + TA::kBytes, true);
-        ta.load(smem + kStage, steps > 1);
-        tb.load(smem + kStage + TA::kBytes, steps > 1);
+        ta.template load<kStream>(smem, true);
+        tb.template load<0>(smem + TA::kBytes, true);
+        ta.template load<kStream>(smem + kStage, steps > 1);
+        tb.template load<0>(smem + kStage + TA::kBytes, steps > 1);
         ZSMR_WAIT(kLoads);              // the first step's
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
@@ -314,8 +319,8 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
         ZSMR_WAIT(0);
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        ta.load(cur, s + 2 < steps);
-        tb.load(cur + TA::kBytes, s + 2 < steps);
+        ta.template load<kStream>(cur, s + 2 < steps);
+        tb.template load<0>(cur + TA::kBytes, s + 2 < steps);
         read(a0, b0, next, 0);
         multiply(a1, b1);
         interleave<kReads, kLoads, kMfma>();
@@ -500,8 +505,8 @@ __device__ __forceinline__ void put_summary(double sum, double count, float* sum
     summary[2] = (float)count;
 }
 
-// Join the parts of each token's softmax: `lanes` tokens of a workgroup (a power
-// of two), its groups of lanes share the parts.  A lone workgroup
+// Join the parts of each token's softmax: `lanes` tokens of a workgroup, its groups
+// of lanes share the parts.  A lone workgroup
 // has all tokens and leaves the summary too.
 constexpr int kStatsThreads = 1024;
 __global__ __launch_bounds__(kStatsThreads) void stats_kernel(const float2* stats, const float* target,
@@ -512,7 +517,7 @@ __global__ __launch_bounds__(kStatsThreads) void stats_kernel(const float2* stat
     const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes, groups = kStatsThreads / lanes;
     const int64_t t = (int64_t)blockIdx.x * lanes + lane;
     float2 s = make_float2(-INFINITY, 0.f);
-    if (t < tokens) {
+    if (t < tokens && group < groups) {
         constexpr int kAhead = 16;
         for (int i = group; i < parts; i += groups * kAhead) {
             float2 p[kAhead];
@@ -525,9 +530,11 @@ __global__ __launch_bounds__(kStatsThreads) void stats_kernel(const float2* stat
     }
     part[threadIdx.x] = s;
     __syncthreads();
-    for (int half = groups / 2; half > 0; half /= 2) {
-        if (group < half) part[threadIdx.x] = s = join_parts(s, part[threadIdx.x + half * lanes]);
+    for (int left = groups; left > 1;) {
+        const int half = (left + 1) / 2;
+        if (group + half < left) part[threadIdx.x] = s = join_parts(s, part[threadIdx.x + half * lanes]);
         __syncthreads();
+        left = half;
     }
     const bool on = group == 0 && t < tokens;
     const bool counts = on && token_at(labels, id_bytes, t, vocab) >= 0;
@@ -654,6 +661,15 @@ int splits_of(int64_t tokens, int64_t width, int64_t piece) {
     return (int)std::max<int64_t>(1, std::min(want, most));
 }
 
+// Vocabulary rows of a tile of dw: 256, or 128, which take a little over half as
+// long, where that ends sooner.  A piece of 27 tiles of 256 across 3 (8,192
+// tokens, width 768) fills a third of the CUs once: 184 us on MI355X, in tiles of
+// 128 136.
+int dw_tile(int64_t across, int64_t rows) {
+    const int64_t wide = tiles_of(across * tiles_of(rows, 256), kCus), narrow = tiles_of(across * tiles_of(rows, 128), kCus);
+    return narrow * 11 < wide * 20 ? 128 : 256;
+}
+
 struct Space {
     float2* stats;
     float *target, *mul, *sum;
@@ -686,7 +702,8 @@ template <int DT, int EPI>
 void launch_product(const Product& p, int bn, hipStream_t stream) {
     const unsigned grid = (unsigned)(p.m_tiles * p.n_tiles * p.splits);
     if constexpr (EPI == E_DW) {
-        product_kernel<DT, EPI, 256, 2><<<grid, kThreads, 0, stream>>>(p);
+        if (bn == 128) product_kernel<DT, EPI, 128, 4><<<grid, kThreads, 0, stream>>>(p);
+        else product_kernel<DT, EPI, 256, 2><<<grid, kThreads, 0, stream>>>(p);
     } else {
         if (bn == 64) product_kernel<DT, EPI, 64, 8><<<grid, kThreads, 0, stream>>>(p);
         else if (bn == 128) product_kernel<DT, EPI, 128, 4><<<grid, kThreads, 0, stream>>>(p);
@@ -760,8 +777,7 @@ hipError_t forward(const XentArgs& a, void* ws, hipStream_t stream) {
         }
         const int32_t parts = (int32_t)tiles_of(a.vocab, BM);
         // up to 256 tokens in one workgroup, which saves the launch of the mean
-        int lanes = a.tokens <= 256 ? 256 : 64;
-        while (lanes / 2 >= a.tokens) lanes /= 2;
+        const int lanes = a.tokens <= 256 ? (int)ceil_to(a.tokens, 16) : 64;
         const unsigned grid = (unsigned)tiles_of(a.tokens, lanes);
         stats_kernel<<<grid, kStatsThreads, 0, stream>>>(s.stats, s.target, a.labels, a.id_bytes, a.tokens,
                                                          a.vocab, parts, lanes, a.loss, a.lse, a.summary);
@@ -820,12 +836,13 @@ hipError_t backward(const XentArgs& a, void* ws, hipStream_t stream) {
             d.b = Mat{s.g, piece, a.tokens, padded};
             d.k = a.tokens;
             d.m_tiles = (int32_t)tiles_of(a.width, BM);
-            d.n_tiles = (int32_t)tiles_of(rows, 256);
+            const int wide = dw_tile(d.m_tiles, rows);
+            d.n_tiles = (int32_t)tiles_of(rows, wide);
             d.k_split = (int32_t)ceil_to(a.tokens, BK);
             d.out = a.dw;
             d.ldo = a.dw_stride;
             d.accumulate = a.accumulate;
-            launch_product<DT, E_DW>(d, 256, stream);
+            launch_product<DT, E_DW>(d, wide, stream);
         }
     }
     return hipGetLastError();
