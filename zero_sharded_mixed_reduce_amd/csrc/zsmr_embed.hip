@@ -43,7 +43,7 @@ __global__ __launch_bounds__(kThreads) void lookup_kernel(EmbedArgs a, uint32_t 
 #pragma unroll
             for (int k = 0; k < 8; ++k) f[k] *= a.scale;
         }
-        store8<DT>(out, j, f);
+        stream8<DT>(out, j, f);
     } else {
         for (int64_t k = j; k < a.width; ++k) store1<DT>(out, k, id < 0 ? 0.f : load1<DT>(row, k) * a.scale);
     }
@@ -255,7 +255,14 @@ __device__ __forceinline__ void put_part(float* p, int64_t j, int64_t width, f32
 }
 template <int DT>
 __device__ __forceinline__ f32x8 get_row(const void* p, int64_t j, int64_t width) {
-    if (j + 8 <= width) return load8<DT>(p, j);
+    if (j + 8 <= width) {
+        if constexpr (DT == ZSMR_FP32) return load8<DT>(p, j);
+        f32x8 f;
+        const Vec<DT> v = load16<DT, false>(p, j);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = v.f[k];
+        return f;
+    }
     f32x8 f = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k)
