@@ -154,30 +154,55 @@ def test_clipped_step_refusals_count_nothing():
     assert all(z.zero_counters(ctx, r)["traffic_elems"] == 0 for r in range(4))
 
 
-def test_binding_checks_tensors_before_the_library(monkeypatch):
-    """Shapes, formats and strides are refused by name, and a host tensor never
-    reaches the library."""
+def test_binding_checks_tensors_before_the_library():
+    """Shapes, formats and strides are refused by name before any address is
+    taken, and a tensor in host memory never reaches the library."""
     t, ids = torch.zeros(10, 16, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int64)
-    out = torch.zeros(3, 16, dtype=torch.bfloat16)
-    with pytest.raises(ValueError, match="device memory"):
-        z.zsmr_embed_lookup(t, ids, out)
-    # host tensors stand for device ones from here on; no call gets as far as the library
-    monkeypatch.setattr(ops, "_ptr", lambda x: None if x is None else x.data_ptr())
-    monkeypatch.setattr(ops, "_raw", lambda name: lambda *a: pytest.fail(f"{name} was called"))
-    for bad in ((t.float(), ids, out), (t, ids, out[:2]), (t, ids, out.half()), (t, ids, out[:, :8]), (t.t(), ids, out),
-                (t[0], ids, out), (t.as_strided((10, 16), (8, 1)), ids, out)):
-        with pytest.raises(ValueError):
+    out, f3 = torch.zeros(3, 16, dtype=torch.bfloat16), torch.zeros(3)
+    ws = torch.zeros(64, dtype=torch.uint8)
+    for bad, why in (((t.float(), ids, out), "16-bit"), ((t, ids, out[:2]), "2 x 16"), ((t, ids, out.half()), "format"),
+                     ((t, ids, out[:, :8]), "3 x 8"), ((t.t(), ids, out), "contiguous"), ((t[0], ids, out), "matrix"),
+                     ((t.as_strided((10, 16), (8, 1)), ids, out), "overlap"), ((t, ids.float(), out), "token ids"),
+                     ((t, ids[None], out), "token ids"), ((t, torch.zeros(6, dtype=torch.int64)[::2], out), "token ids"),
+                     ((t, ids, out), "host memory")):
+        with pytest.raises(ValueError, match=why):
             z.zsmr_embed_lookup(*bad, stream=0)
-    for bad in (ids.float(), ids[None], torch.zeros(6, dtype=torch.int64)[::2]):
-        with pytest.raises(ValueError):
-            ops._ids(bad)
-    with pytest.raises(ValueError, match="lse"):
-        z.zsmr_xent_forward(out, t, ids, torch.zeros(3), torch.zeros(2), torch.zeros(3), None, stream=0)
-    with pytest.raises(ValueError, match="dw"):
-        z.zsmr_xent_backward(out, t, ids, torch.zeros(3), None, t[:5], None, stream=0)
-    with pytest.raises(ValueError, match="tensor list"):
-        z.zsmr_grad_norm([t.t()], 1.0, torch.zeros(2), None, stream=0)
-    with pytest.raises(ValueError, match="tensor list"):
-        z.zsmr_grad_norm((np.zeros(2, np.int64), np.zeros(1, np.int64), np.zeros(2, np.int32)), 1.0, torch.zeros(2), None, stream=0)
-    with pytest.raises(ValueError, match="flat"):
-        z.zsmr_clip_flatten([], None, torch.zeros(4), stream=0)
+    for bad, why in (((out, ids, t[:, :8], ws), "3 x 16"), ((out, ids, t, ws[::2]), "workspace"), ((out, ids, t, ws), "host memory")):
+        with pytest.raises(ValueError, match=why):
+            z.zsmr_embed_grad(*bad, stream=0)
+    for bad, why in (((out, t, ids, f3, f3[:2], f3, ws), "lse"), ((out, t, ids, f3.double(), f3, f3, ws), "loss"),
+                     ((out, t, ids, f3, f3, f3[:2], ws), "summary"), ((out, t, ids, f3, f3, f3, ws), "host memory")):
+        with pytest.raises(ValueError, match=why):
+            z.zsmr_xent_forward(*bad, stream=0)
+    for bad, kw, why in (((out, t, ids, f3, None, t[:5], ws), {}, "dw"), ((out, t, ids, f3, out[:2], None, ws), {}, "dx"),
+                         ((out, t, ids, f3, out, t, ws), {"grad": f3[:1]}, "grad"), ((out, t, ids, f3, out, t, ws), {"scale": ids}, "scale"),
+                         ((out, t, ids, f3, None, None, ws), {}, "host memory")):
+        with pytest.raises(ValueError, match=why):
+            z.zsmr_xent_backward(*bad, stream=0, **kw)
+    i64, i32 = np.zeros(2, np.int64), np.zeros(2, np.int32)
+    for bad in ([t.t()], (i64, i64[:1], i32), (i64, i32, i32), (i64, i64, i64), (np.zeros(4, np.int64)[::2], i64, i32), (i64[None], i64, i32)):
+        with pytest.raises(ValueError, match="tensor list"):
+            z.zsmr_grad_norm(bad, 1.0, f3, ws, stream=0)
+        with pytest.raises(ValueError, match="tensor list"):
+            z.zsmr_clip_grads(bad, f3, stream=0)
+    for flat, why in ((f3, "flat"), (out.t(), "flat"), (out, "host memory")):
+        with pytest.raises(ValueError, match=why):
+            z.zsmr_clip_flatten((i64[:0], i64[:0], i32[:0]), None, flat, stream=0)
+    with pytest.raises(ValueError, match="sums"):
+        z.zsmr_clip_coef(f3.double(), 4, 1.0, f3, stream=0)
+    ctx = z.zero_init_shards(1000, 4, z.ZSMR_ZERO2, "bf16")
+    rows, shard, sums = torch.zeros(4000, dtype=torch.bfloat16), torch.zeros(250), torch.zeros(1, dtype=torch.float64)
+    for change, why in ((dict(base_elem=751), "grads"), (dict(g_out=shard[:249]), "g_out"), (dict(sumsq=shard), "sumsq"), (dict(rank=1 << 32), "int32"),
+                        (dict(row_stride=1 << 63), "int64"), ({}, "host memory")):
+        with pytest.raises(ValueError, match=why):
+            z.zero_reduce_shard_sumsq(**(dict(ctx=ctx, rank=0, unit=0, grads=rows, row_stride=1000, base_elem=0, mean=True, g_out=shard,
+                                              sumsq=sums, ws=ws, stream=0) | change))
+    for change, why in ((dict(g=shard[:249]), "g"), (dict(m=shard.bfloat16()), "m"), (dict(p16_dst=rows[:249]), "p16_dst"), (dict(coef=sums), "coef"),
+                        (dict(t=1 << 31), "int32"), ({}, "host memory")):
+        with pytest.raises(ValueError, match=why):
+            z.zero_clipped_step(**(dict(ctx=ctx, rank=0, unit=0, g=shard, coef=shard, master=shard, m=shard, v=shard, p16_dst=rows, t=1, lr=1e-3,
+                                        stream=0) | change))
+    assert z.zero_counters(ctx, 0)["traffic_elems"] == 0
+    for call in (lambda: ops._ops.embed_lookup(t), lambda: ops._ops.embed_lookup(1, 2, 3, 4, 5), lambda: z.zsmr_embed_lookup(t, None, out, stream=0)):
+        with pytest.raises((TypeError, AttributeError, ValueError)):
+            call()

@@ -204,14 +204,11 @@ def _fits(x, elems: int, elem_bytes: int, what: str) -> None:
 def _piece_len(ctx, rank: int, unit: int) -> int:
     """Elements of the (rank, unit) piece, or 0 where the layout refuses the
     pair (the call itself then reports the error)."""
-    n = ctx._lens.get((rank, unit))
-    if n is None:
-        off, ln, loc = _i64(), _i64(), _i64()
-        if _lib().zero_layout(ctx.handle, rank, unit, ctypes.byref(off), ctypes.byref(ln),
-                              ctypes.byref(loc)) != ZSMR_OK:
-            return 0
-        n = ctx._keep_len(rank, unit, ln.value)
-    return n
+    off, ln, loc = _i64(), _i64(), _i64()
+    if _lib().zero_layout(ctx.handle, rank, unit, ctypes.byref(off), ctypes.byref(ln),
+                          ctypes.byref(loc)) != ZSMR_OK:
+        return 0
+    return ln.value
 
 
 def _rows_fit(ctx, grads, row_stride: int, base: int, end: int, what: str) -> None:
@@ -245,8 +242,6 @@ class Ctx:
     def __init__(self, handle: int):
         self.handle = handle
         self._world = None
-        self._stage = None
-        self._lens = {}         # (rank, unit) -> elements of the piece
 
     @property
     def world(self) -> int:
@@ -254,15 +249,6 @@ class Ctx:
         if self._world is None:
             self._world = zero_layout_info(self)["world"]
         return self._world
-
-    def _keep_len(self, rank: int, unit: int, n: int) -> int:
-        """Keep the length of a piece, which is fixed when the context is made
-        (but for stage 4, where units can change owners)."""
-        if self._stage is None:
-            self._stage = zero_layout_info(self)["stage"]
-        if self._stage != ZSMR_ZERO3_OWNER and len(self._lens) < 4096:
-            self._lens[rank, unit] = n
-        return n
 
     def close(self):
         if self.handle:

@@ -2,6 +2,8 @@
 
 * ``zero_sharded_mixed_reduce_amd/libzsmr.so`` -- the ZeRO shard step (C ABI in
   ``include/zsmr.h``) and the operators around it (``include/zsmr_ops.h``).
+* ``zero_sharded_mixed_reduce_amd/_ops.so`` -- the native half of the Python
+  binding of those operators (host code, g++).
 * ``synth/libzsmr_synth.so`` -- the GPU fill kernels of the seeded input
   generator (C ABI in ``include/zsmr_synth.h``).
 * ``ceiling/libzsmr_ceiling.so`` -- pure-read and pure-write reference
@@ -19,6 +21,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -28,6 +31,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libzsmr.so")
 LIB_SOURCES = ("zsmr_kernels.hip", "zsmr_api.cpp", "zsmr_norm.hip", "zsmr_embed.hip",
                "zsmr_xent.hip", "zsmr_ops_api.cpp")
+BINDING = os.path.join(PKG, "_ops.so")
 SYNTH_LIB = os.path.join(ROOT, "synth", "libzsmr_synth.so")
 CEILING_LIB = os.path.join(ROOT, "ceiling", "libzsmr_ceiling.so")
 
@@ -64,6 +68,18 @@ def build_lib(extra=()):
     return LIB
 
 
+def build_binding():
+    """The native half of the Python binding: host code against libzsmr.so,
+    which it finds beside itself."""
+    rocm = os.path.dirname(os.path.dirname(hipcc()))
+    tmp = BINDING + ".tmp"
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+          "-I", INCLUDE, "-I", os.path.join(rocm, "include"), "-I", sysconfig.get_paths()["include"],
+          os.path.join(CSRC, "zsmr_python.cpp"), "-L", PKG, "-lzsmr", "-Wl,-rpath,$ORIGIN", "-o", tmp])
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build_synth(extra=()):
     _build(SYNTH_LIB, [os.path.join(ROOT, "synth", "synth_fill.hip")], extra)
     return SYNTH_LIB
@@ -76,6 +92,7 @@ def build_ceiling(extra=()):
 
 def build_all():
     build_lib()
+    build_binding()
     build_synth()
     build_ceiling()
 
