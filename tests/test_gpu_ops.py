@@ -474,11 +474,11 @@ def test_clipped_step_has_the_bits_of_the_plain_steps(numel, world, dt, pad, shi
     assert a["ag_elems"] == b["ag_elems"] + (S if world > 1 else 0)
 
 
-@pytest.mark.parametrize("world,extra,shift,dt", [(16, 0, 0, "bf16"), (17, 511, 1, "fp16"), (24, 5, 3, "bf16")])
+@pytest.mark.parametrize("world,extra,shift,dt", [(16, 0, 0, "bf16"), (32, 0, 0, "bf16"), (33, 511, 1, "fp16"), (47, 5, 3, "bf16")])
 def test_windowed_reduce(world, extra, shift, dt):
     """One rank's large shard with many rows, whose results are stored in write
     windows: the bits of zero_reduce_shard and the sum of their squares."""
-    n, t = 1024 * 18 * 512 + extra, T16[dt]
+    n, t = 1024 * 18 * 512 + extra, T16[dt]         # windows from 2^28 elements in 32 rows on
     g = gen(10)
     ctx = z.zero_init_shards(n * world, world, z.ZSMR_ZERO2, dt)
     raw = torch.randn(world * (n + shift) + 8, generator=g, device="cuda", dtype=t).mul_(0.01)[shift:]
@@ -494,6 +494,23 @@ def test_windowed_reduce(world, extra, shift, dt):
         assert abs(float(sums) - exact) <= 1e-11 * exact
     assert bool((red[n:] == 7).all())
     intact(guard, size)
+
+
+def test_reduce_of_very_many_rows_of_a_short_piece():
+    """16,400 ranks of 20,000: as much to read as a windowed reduce has, but
+    fewer tiles than it has waves."""
+    n, world = 20_000, 16_400
+    ctx = z.zero_init_shards(n * world, world, z.ZSMR_ZERO2, "bf16")
+    raw = torch.randn(world * n, generator=gen(12), device="cuda", dtype=torch.bfloat16)
+    red, want, sums = torch.empty(n, device="cuda"), torch.empty(n, device="cuda"), torch.empty(1, device="cuda", dtype=torch.float64)
+    size = z.zsmr_norm_workspace(n, 1)
+    ws, guard = space(size)
+    z.zero_reduce_shard(ctx, 3, 0, raw, n, 0, True, want)
+    z.zero_reduce_shard_sumsq(ctx, 3, 0, raw, n, 0, True, red, sums, ws)
+    intact(guard, size)
+    assert torch.equal(red.view(torch.int32), want.view(torch.int32))
+    exact = float(want.double().square().sum())
+    assert abs(float(sums) - exact) <= 1e-12 * exact
 
 
 @pytest.mark.parametrize("sizes", [[40_000_003, 5, 30_000_000], [1] + [9_000_000] * 8])

@@ -249,7 +249,6 @@ __global__ __launch_bounds__(kSmall) void reduce_sumsq_small_kernel(StepArgs a, 
 // ring 2.61-2.85).
 constexpr int kRing = 18;
 constexpr uint32_t kCycle = 10000, kWindow = 400, kLead = 133;      // ticks of 10 ns
-constexpr int kWindowRows = 16;
 __device__ __forceinline__ void wait_clock(uint64_t t) {
     for (int i = 0; i < (1 << 16); ++i) {           // bounded: a wave always goes on
         if (__builtin_amdgcn_s_memrealtime() >= t) break;
@@ -407,6 +406,16 @@ hipError_t launch_join(const double* partial, int64_t n, double* sumsq, double m
 }
 
 namespace {
+// Windows pay where writes are a small share of a long stream.  Measured on
+// MI355X, as it comes against windows, us: 8 rows of 30M 97 / 123; 16 rows of
+// 30M 182 / 193, of 100M 664 / 627; 24 rows of 30M 269 / 275; 32 rows of 4.8M
+// 58.2 / 58.7, of 9.6M 115 / 109, of 30M 357 / 334; 64 rows of 2.4M 54 / 61, of
+// 4.8M 111 / 107, of 30M 684 / 623.
+bool windows_pay(int64_t rows, int64_t n) {
+    const int64_t read = rows * n;
+    return rows >= 32 ? read >= int64_t(1) << 28 : rows >= 16 && read >= int64_t(1) << 30;
+}
+
 template <int DT>
 hipError_t reduce_launches(const StepArgs& a, double* partial, double* sumsq, hipStream_t stream) {
     // one workgroup: 8 elements a lane, or twice that
@@ -416,10 +425,9 @@ hipError_t reduce_launches(const StepArgs& a, double* partial, double* sumsq, hi
     }
     int64_t parts = (a.n + kTile - 1) / kTile;
     int device = 0, cus = 0;
-    // windows pay once every wave fills its ring
-    if (a.nrows >= kWindowRows && hipGetDevice(&device) == hipSuccess &&
+    if (windows_pay(a.nrows, a.n) && hipGetDevice(&device) == hipSuccess &&
         hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device) == hipSuccess &&
-        a.n / 512 >= (int64_t)cus * (kThreads / 64) * kRing) {
+        a.n / 512 >= (int64_t)cus * (kThreads / 64)) {      // a tile for every wave
         parts = cus;
         reduce_sumsq_windows_kernel<DT><<<cus, kThreads, 0, stream>>>(a, partial);
     } else {
