@@ -236,18 +236,19 @@ __device__ __forceinline__ void put4(uint16_t* p, int64_t at, int64_t width, f32
     }
 }
 
-template <int DT, int EPI, int BN, int WM>
+// ONCE: no other workgroup reads the same part of A (one tile holds all of n).
+template <int DT, int EPI, int BN, int WM, int STAGES, bool ONCE>
 __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
 #if defined(__HIP_DEVICE_COMPILE__)     // the scheduling hints have no host form
     constexpr bool A_OUTER = EPI == E_DX || EPI == E_DW, B_OUTER = EPI == E_DW;
-    // A tile that holds all tokens reads the weights once: past the caches 1.05 GB
-    // took 160 us on MI355X (16 tokens), through them 177.
-    constexpr int kStream = EPI != E_DW && BN <= 128 ? 2 : 0;
+    // Weights that are read once go past the caches: 1.05 GB took 160 us on MI355X
+    // (16 tokens), through them 177.
+    constexpr int kStream = ONCE ? 2 : 0;
     constexpr int WN = kWaves / WM, TM = BM / WM / 16, TN = BN / WN / 16;
     typedef Tile<BM, A_OUTER> TA;
     typedef Tile<BN, B_OUTER> TB;
     constexpr int kLoads = TA::kLoads + TB::kLoads, kStage = TA::kBytes + TB::kBytes;
-    __shared__ __attribute__((aligned(1024))) char smem[2 * kStage];
+    __shared__ __attribute__((aligned(1024))) char smem[STAGES * kStage];
 
     // Consecutive workgroups go to the eight XCDs in turn; each XCD takes a
     // contiguous run of tiles, in groups of 8 in m, so that the tiles it works
@@ -279,12 +280,12 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = 0.f;
 
-    // Two stages of LDS and two sets of operand registers: the second half's
+    // STAGES of LDS and two sets of operand registers: the second half's
     // operands of a step (k 32..63) are read while its first half is
     // multiplied, the next step's first half while the second is.  The barrier
     // between the halves is the only one of a step: behind it every wave has the
-    // stage's operands in registers, so its LDS is refilled (with the step after
-    // the next), and the next step's loads, which had a whole step to arrive,
+    // stage's operands in registers, so its LDS is refilled (STAGES steps
+    // ahead), and the next step's loads, which had STAGES - 1 steps to arrive,
     // are there.
     constexpr int kReads = TM * (A_OUTER ? 2 : 1) + TN * (B_OUTER ? 2 : 1), kMfma = TM * TN;
     u32x4 a0[TM], b0[TN], a1[TM], b1[TN];
@@ -301,29 +302,31 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
             for (int j = 0; j < TN; ++j) acc[i][j] = mfma<DT>(a[i], b[j], acc[i][j]);
     };
     if (steps > 0) {
-        ta.template load<kStream>(smem, true);
-        tb.template load<0>(smem + TA::kBytes, true);
-        ta.template load<kStream>(smem + kStage, steps > 1);
-        tb.template load<0>(smem + kStage + TA::kBytes, steps > 1);
-        ZSMR_WAIT(kLoads);              // the first step's
+#pragma unroll
+        for (int s = 0; s < STAGES; ++s) {
+            ta.template load<kStream>(smem + s * kStage, s < steps);
+            tb.template load<0>(smem + s * kStage + TA::kBytes, s < steps);
+        }
+        ZSMR_WAIT((STAGES - 1) * kLoads);       // the first step's
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         read(a0, b0, smem, 0);
     }
+    char* cur = smem;
     for (int s = 0; s < steps; ++s) {
-        char* cur = smem + (s & 1) * kStage;
-        char* next = smem + (~s & 1) * kStage;
+        char* next = cur == smem + (STAGES - 1) * kStage ? smem : cur + kStage;
         read(a1, b1, cur, 1);
         multiply(a0, b0);
         interleave<kReads, 0, kMfma>();
-        ZSMR_WAIT(0);
+        ZSMR_WAIT((STAGES - 2) * kLoads);
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        ta.template load<kStream>(cur, s + 2 < steps);
-        tb.template load<0>(cur + TA::kBytes, s + 2 < steps);
+        ta.template load<kStream>(cur, s + STAGES < steps);
+        tb.template load<0>(cur + TA::kBytes, s + STAGES < steps);
         read(a0, b0, next, 0);
         multiply(a1, b1);
         interleave<kReads, kLoads, kMfma>();
+        cur = next;
     }
     ZSMR_WAIT(0);           // no load may still be on its way to this LDS when the workgroup ends
 
@@ -635,16 +638,31 @@ __global__ __launch_bounds__(256) void splits_kernel(Product p) {
 int64_t ceil_to(int64_t n, int64_t k) { return (n + k - 1) / k * k; }
 int64_t tiles_of(int64_t n, int64_t k) { return (n + k - 1) / k; }
 
-// Tokens of a tile: as few as hold all of them.
-int token_tile(int64_t tokens) {
-    if (tokens <= 128) return tokens <= 64 ? 64 : 128;
-    // 192 where it pads less
-    return tiles_of(tokens, 192) * 192 < tiles_of(tokens, 256) * 256 ? 192 : 256;
+constexpr int64_t kCus = 256;
+
+// Tokens of a tile, given the tiles (and splits) on the other side: the width
+// whose rounds over the CUs end soonest.  A step of 64 k takes about 0.55, 0.9,
+// 1.25 and 1.6 us for 64, 128, 192 and 256 tokens on MI355X.  215 tokens over
+// 2,113 x 3,832 with gradients take 134 us in tiles of 64, in one of 256 230; 8,192
+// over 50,257 x 768 2.5 ms in tiles of 256.
+int token_tile(int64_t tokens, int64_t others) {
+    const int widths[4] = {64, 128, 192, 256}, cost[4] = {11, 18, 25, 32};
+    int best = 0;
+    int64_t least = INT64_MAX;
+    for (int i = 0; i < 4; ++i) {
+        const int64_t n = tiles_of(std::max<int64_t>(tokens, 1), widths[i]);
+        const int64_t ends = tiles_of(n * others, kCus) * cost[i];
+        if (ends < least) {
+            least = ends;
+            best = widths[i];
+        }
+        if (n == 1) break;                  // wider tiles only pad
+    }
+    return best;
 }
 
 // The vocabulary's pieces: G of one takes about 512 MB at most, and the tiles of
 // dw over one fill the 256 CUs a whole number of times if it has that many.
-constexpr int64_t kCus = 256;
 constexpr int64_t kMaxPiece = int64_t(1) << 21;     // G's rows: byte offsets within a tile fit 31 bits
 int64_t piece_of(int64_t tokens, int64_t vocab, int64_t width) {
     int64_t tiles = std::max<int64_t>(1, (int64_t(1) << 28) / std::max<int64_t>(tokens, 1) / BM);
@@ -654,11 +672,22 @@ int64_t piece_of(int64_t tokens, int64_t vocab, int64_t width) {
     if (rounds > 0) tiles = rounds * kCus / across;
     return tiles * BM;
 }
-// k splits of the dx product: enough to give every CU a tile.
-int splits_of(int64_t tokens, int64_t width, int64_t piece) {
-    const int64_t tiles = tiles_of(width, BM) * tiles_of(std::max<int64_t>(tokens, 1), token_tile(tokens));
-    const int64_t want = 2 * kCus / tiles, most = piece / 1024;
-    return (int)std::max<int64_t>(1, std::min(want, most));
+// The dx product: k splits that give every CU one tile, or two where that leaves
+// clearly fewer CUs without (8,192 tokens of width 768: 96 tiles, so 5 splits and
+// not 2), but none shorter than 512 of k, because their sums go through memory;
+// and the tokens of a tile.
+struct DxShape {
+    int splits, tile;
+};
+DxShape dx_shape(int64_t tokens, int64_t width, int64_t piece) {
+    const int64_t across = tiles_of(width, BM);
+    DxShape d{1, token_tile(tokens, across)};
+    const int64_t tiles = across * tiles_of(std::max<int64_t>(tokens, 1), d.tile);
+    const int64_t one = kCus / tiles, two = 2 * kCus / tiles;
+    const int64_t want = two * 9 > one * 20 ? two : one;        // two / 2 > 1.11 * one
+    d.splits = (int)std::max<int64_t>(1, std::min(want, piece / 512));
+    d.tile = token_tile(tokens, across * d.splits);
+    return d;
 }
 
 // Vocabulary rows of a tile of dw: 256, or 128, which take a little over half as
@@ -692,7 +721,7 @@ Space space_of(char* ws, int64_t tokens, int64_t vocab, int64_t width, bool back
     if (backward) {
         s.mul = reinterpret_cast<float*>(take(8));
         s.g = reinterpret_cast<uint16_t*>(take(tokens * piece * 2));
-        s.sum = reinterpret_cast<float*>(take(tokens * ceil_to(width, 4) * 4 * splits_of(tokens, width, piece)));
+        s.sum = reinterpret_cast<float*>(take(tokens * ceil_to(width, 4) * 4 * dx_shape(tokens, width, piece).splits));
     }
     s.bytes = at;
     return s;
@@ -702,13 +731,21 @@ template <int DT, int EPI>
 void launch_product(const Product& p, int bn, hipStream_t stream) {
     const unsigned grid = (unsigned)(p.m_tiles * p.n_tiles * p.splits);
     if constexpr (EPI == E_DW) {
-        if (bn == 128) product_kernel<DT, EPI, 128, 4><<<grid, kThreads, 0, stream>>>(p);
-        else product_kernel<DT, EPI, 256, 2><<<grid, kThreads, 0, stream>>>(p);
+        if (bn == 128) product_kernel<DT, EPI, 128, 4, 3, false><<<grid, kThreads, 0, stream>>>(p);
+        else product_kernel<DT, EPI, 256, 2, 2, false><<<grid, kThreads, 0, stream>>>(p);
+    } else if (bn == 64) {
+        // Two workgroups share a CU's LDS with two stages each; where there is
+        // at most one for a CU it takes four, and waits a third as long: 44 tokens
+        // over 1,892 x 4,008 106 -> 38 us on MI355X.
+        if (grid > kCus && p.n_tiles == 1) product_kernel<DT, EPI, 64, 8, 2, true><<<grid, kThreads, 0, stream>>>(p);
+        else product_kernel<DT, EPI, 64, 8, 4, false><<<grid, kThreads, 0, stream>>>(p);
+    } else if (bn == 128) {
+        if (p.n_tiles == 1) product_kernel<DT, EPI, 128, 4, 3, true><<<grid, kThreads, 0, stream>>>(p);
+        else product_kernel<DT, EPI, 128, 4, 3, false><<<grid, kThreads, 0, stream>>>(p);
+    } else if (bn == 192) {
+        product_kernel<DT, EPI, 192, 2, 2, false><<<grid, kThreads, 0, stream>>>(p);
     } else {
-        if (bn == 64) product_kernel<DT, EPI, 64, 8><<<grid, kThreads, 0, stream>>>(p);
-        else if (bn == 128) product_kernel<DT, EPI, 128, 4><<<grid, kThreads, 0, stream>>>(p);
-        else if (bn == 192) product_kernel<DT, EPI, 192, 2><<<grid, kThreads, 0, stream>>>(p);
-        else product_kernel<DT, EPI, 256, 2><<<grid, kThreads, 0, stream>>>(p);
+        product_kernel<DT, EPI, 256, 2, 2, false><<<grid, kThreads, 0, stream>>>(p);
     }
 }
 
@@ -763,11 +800,11 @@ Product logits_of(const XentArgs& a, const Operands& o, int64_t v0, int bn) {
 template <int DT>
 hipError_t forward(const XentArgs& a, void* ws, hipStream_t stream) {
     const Space s = space_of(static_cast<char*>(ws), a.tokens, a.vocab, a.width, false);
-    const int bn = token_tile(a.tokens);
     if (a.tokens) {
         Operands o;
         pack_x(a, s, &o, stream);
         const int64_t piece = loads16(a.w, a.w_stride, a.width) ? a.vocab : piece_of(a.tokens, a.vocab, a.width);
+        const int bn = token_tile(a.tokens, tiles_of(std::min(piece, a.vocab), BM));
         for (int64_t v0 = 0; v0 < a.vocab; v0 += piece) {
             pack_w(a, s, v0, std::min(piece, a.vocab - v0), &o, stream);
             Product p = logits_of(a, o, v0, bn);
@@ -790,9 +827,10 @@ hipError_t forward(const XentArgs& a, void* ws, hipStream_t stream) {
 template <int DT>
 hipError_t backward(const XentArgs& a, void* ws, hipStream_t stream) {
     const Space s = space_of(static_cast<char*>(ws), a.tokens, a.vocab, a.width, true);
-    const int bn = token_tile(a.tokens);
     const int64_t piece = piece_of(a.tokens, a.vocab, a.width);
-    const int splits = splits_of(a.tokens, a.width, piece);
+    const int bn = token_tile(a.tokens, tiles_of(std::min(piece, a.vocab), BM));
+    const DxShape shape = dx_shape(a.tokens, a.width, piece);
+    const int splits = shape.splits;
     const bool fp16 = DT == ZSMR_FP16, weighted = fp16 && a.grad;
     if (weighted) mul_kernel<<<1, kMulThreads, 0, stream>>>(a.grad, a.tokens, a.scale, s.mul);
     Operands o;
@@ -818,6 +856,7 @@ hipError_t backward(const XentArgs& a, void* ws, hipStream_t stream) {
             d.b = Mat{s.g, piece, a.tokens, padded};
             d.k = padded;
             d.m_tiles = (int32_t)tiles_of(a.width, BM);
+            d.n_tiles = (int32_t)tiles_of(a.tokens, shape.tile);
             d.splits = splits;
             d.k_split = (int32_t)ceil_to(tiles_of(padded, splits), BK);
             d.sum = s.sum;
@@ -826,7 +865,7 @@ hipError_t backward(const XentArgs& a, void* ws, hipStream_t stream) {
             d.sum_out = splits > 1 || v0 + piece < a.vocab;
             d.out = a.dx;
             d.ldo = a.dx_stride;
-            launch_product<DT, E_DX>(d, bn, stream);
+            launch_product<DT, E_DX>(d, shape.tile, stream);
             if (splits > 1 && v0 + piece >= a.vocab)
                 splits_kernel<DT><<<(unsigned)tiles_of(a.tokens * (d.lds / 4), 256), 256, 0, stream>>>(d);
         }
