@@ -640,21 +640,23 @@ int64_t tiles_of(int64_t n, int64_t k) { return (n + k - 1) / k; }
 
 constexpr int64_t kCus = 256;
 
-// Tokens of a tile, given the tiles (and splits) on the other side: the width
-// whose rounds over the CUs end soonest.  A step of 64 k takes about 0.55, 0.9,
-// 1.25 and 1.6 us for 64, 128, 192 and 256 tokens on MI355X.  215 tokens over
-// 2,113 x 3,832 with gradients take 134 us in tiles of 64, in one of 256 230; 8,192
-// over 50,257 x 768 2.5 ms in tiles of 256.
+// Tokens of a tile, and what a step of 64 k takes with so many on MI355X, in
+// twentieths of a microsecond.
+constexpr int kWidths = 4, kWidth[kWidths] = {64, 128, 192, 256}, kCost[kWidths] = {11, 18, 25, 32};
+
+// Tokens of a tile, given the tiles on the other side: the width whose rounds
+// over the CUs end soonest.  215 tokens over 2,113 x 3,832 with gradients take 134
+// us in tiles of 64, in one of 256 230; 8,192 over 50,257 x 768 2.5 ms in tiles of
+// 256.
 int token_tile(int64_t tokens, int64_t others) {
-    const int widths[4] = {64, 128, 192, 256}, cost[4] = {11, 18, 25, 32};
     int best = 0;
     int64_t least = INT64_MAX;
-    for (int i = 0; i < 4; ++i) {
-        const int64_t n = tiles_of(std::max<int64_t>(tokens, 1), widths[i]);
-        const int64_t ends = tiles_of(n * others, kCus) * cost[i];
+    for (int i = 0; i < kWidths; ++i) {
+        const int64_t n = tiles_of(std::max<int64_t>(tokens, 1), kWidth[i]);
+        const int64_t ends = tiles_of(n * others, kCus) * kCost[i];
         if (ends < least) {
             least = ends;
-            best = widths[i];
+            best = kWidth[i];
         }
         if (n == 1) break;                  // wider tiles only pad
     }
@@ -672,22 +674,31 @@ int64_t piece_of(int64_t tokens, int64_t vocab, int64_t width) {
     if (rounds > 0) tiles = rounds * kCus / across;
     return tiles * BM;
 }
-// The dx product: k splits that give every CU one tile, or two where that leaves
-// clearly fewer CUs without (8,192 tokens of width 768: 96 tiles, so 5 splits and
-// not 2), but none shorter than 512 of k, because their sums go through memory;
-// and the tokens of a tile.
+// The dx product: its k splits (none shorter than 512 of k) and the tokens of a
+// tile.  Splits fill the CUs once or twice, but each writes and reads T x H sums at
+// about 5 TB/s.  8,192 tokens of width 768: 5 splits in tiles of 256; 129 tokens:
+// 28 in tiles of 64, 29 us with the sums on MI355X, where 49 in tiles of 192 took
+// 36.
 struct DxShape {
     int splits, tile;
 };
 DxShape dx_shape(int64_t tokens, int64_t width, int64_t piece) {
-    const int64_t across = tiles_of(width, BM);
-    DxShape d{1, token_tile(tokens, across)};
-    const int64_t tiles = across * tiles_of(std::max<int64_t>(tokens, 1), d.tile);
-    const int64_t one = kCus / tiles, two = 2 * kCus / tiles;
-    const int64_t want = two * 9 > one * 20 ? two : one;        // two / 2 > 1.11 * one
-    d.splits = (int)std::max<int64_t>(1, std::min(want, piece / 512));
-    d.tile = token_tile(tokens, across * d.splits);
-    return d;
+    DxShape best{};
+    double least = 0;
+    for (int i = 0; i < kWidths; ++i) {
+        const int64_t n = tiles_of(std::max<int64_t>(tokens, 1), kWidth[i]), tiles = n * tiles_of(width, BM);
+        for (int rounds = 1; rounds <= 2; ++rounds) {
+            const int64_t splits = std::max<int64_t>(1, std::min(rounds * kCus / tiles, piece / 512));
+            double us = (double)tiles_of(tiles * splits, kCus) * kCost[i] / 20 * tiles_of(piece, BK * splits);
+            if (splits > 1) us += (double)splits * tokens * width * 8 / 5e6;
+            if (!best.tile || us < least) {
+                least = us;
+                best = DxShape{(int)splits, kWidth[i]};
+            }
+        }
+        if (n == 1) break;
+    }
+    return best;
 }
 
 // Vocabulary rows of a tile of dw: 256, or 128, which take a little over half as
