@@ -138,7 +138,8 @@ def embed_grad_case(n, vocab, width, kind, dt, accumulate, stride=0, shift=0, id
 @pytest.mark.parametrize("n,vocab,width,kind", [
     (1, 1, 1, "same"), (1, 10, 64, "some"), (63, 7, 65, "some"), (64, 40, 768, "distinct"), (65, 100, 9, "same"), (130, 3, 520, "some"),
     (1000, 50257, 768, "some"), (2049, 511, 24, "some"), (2048, 512, 2056, "some"), (4097, 4096, 64, "distinct"), (5000, 300000, 16, "some"),
-    (70000, 1000, 8, "some"), (3000, 50, 128, "same"), (100, 20, 64, "none")])
+    (70000, 1000, 8, "some"), (16384, 70000, 16, "some"),
+    (16385, 300000, 8, "some"), (16000, 900, 24, "same"), (3000, 50, 128, "same"), (100, 20, 64, "none")])
 @pytest.mark.parametrize("dt,accumulate", [("bf16", False), ("fp16", True)])
 def test_embed_grad(n, vocab, width, kind, dt, accumulate):
     embed_grad_case(n, vocab, width, kind, dt, accumulate)
