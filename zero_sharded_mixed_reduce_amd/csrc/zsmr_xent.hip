@@ -9,6 +9,11 @@
 // pass computes them again, a piece of the vocabulary at a time, with an
 // epilogue that leaves G in 16 bits as the operand of the other two products.
 // So a training step does 8 T V H operations where the mathematics needs 6.
+// Measured on MI355X, 8,192 tokens, vocabulary 128,256, width 4,096, bf16: logits
+// 1.32 PFLOP/s, with G's epilogue 1.25, dx 1.38-1.41, dw 1.28-1.33, where the
+// library's products of these shapes reach 1.41 (logits), 1.35 (dx) and 1.10 (dw).
+// The matrix units are busy for 63-72% of the cycles at a clock that their power
+// holds at 1.8-2.0 GHz.
 //
 // One main loop serves all products: D[m, n] = sum_k A[m, k] B[n, k] over a
 // 256 x BN tile, 64 k a step, by 8 waves.  An operand whose k is contiguous in
@@ -704,7 +709,7 @@ DxShape dx_shape(int64_t tokens, int64_t width, int64_t piece) {
 // Vocabulary rows of a tile of dw: 256, or 128, which take a little over half as
 // long, where that ends sooner.  A piece of 27 tiles of 256 across 3 (8,192
 // tokens, width 768) fills a third of the CUs once: 184 us on MI355X, in tiles of
-// 128 136.
+// 128 119-124.
 int dw_tile(int64_t across, int64_t rows) {
     const int64_t wide = tiles_of(across * tiles_of(rows, 256), kCus), narrow = tiles_of(across * tiles_of(rows, 128), kCus);
     return narrow * 11 < wide * 20 ? 128 : 256;
