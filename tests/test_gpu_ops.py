@@ -266,7 +266,7 @@ def test_xent_weighted_accumulated_and_sharp(dt):
     xent_case(200, 700, 128, dt, sigma=12.0, grad=True)
 
 
-@pytest.mark.parametrize("n,vocab,width,stride", [(8192, 33500, 64, 0), (5000, 60000, 65, 0), (70, 300, 2056, 0)])
+@pytest.mark.parametrize("n,vocab,width,stride", [(8192, 33500, 64, 0), (5000, 60000, 65, 0), (33, 70000, 130, 131), (70, 300, 2056, 0)])
 def test_xent_in_pieces(n, vocab, width, stride):
     """More than 2^28 probabilities (several pieces of the vocabulary), also
     where each piece of the weights is packed; and a split k."""

@@ -679,6 +679,11 @@ int64_t piece_of(int64_t tokens, int64_t vocab, int64_t width) {
     if (rounds > 0) tiles = rounds * kCus / across;
     return tiles * BM;
 }
+// Pieces of weights that have to be packed first: their copy stays under 268 MB at
+// width 4,096, also where G would allow more rows.
+int64_t packed_piece(int64_t tokens, int64_t vocab, int64_t width) {
+    return std::min<int64_t>(piece_of(tokens, vocab, width), 32768);
+}
 // The dx product: its k splits (none shorter than 512 of k) and the tokens of a
 // tile.  Splits fill the CUs once or twice, but each writes and reads T x H sums at
 // about 5 TB/s.  8,192 tokens of width 768: 5 splits in tiles of 256; 129 tokens:
@@ -730,14 +735,16 @@ Space space_of(char* ws, int64_t tokens, int64_t vocab, int64_t width, bool back
         return p;
     };
     const int64_t piece = piece_of(tokens, vocab, width), packed = ceil_to(width, 8);
+    const int64_t rows = packed_piece(tokens, vocab, width);
     s.stats = reinterpret_cast<float2*>(take(tiles_of(vocab, BM) * tokens * 8));
     s.target = reinterpret_cast<float*>(take(tokens * 4));
     s.x = reinterpret_cast<uint16_t*>(take(tokens * packed * 2));
-    s.w = reinterpret_cast<uint16_t*>(take(piece * packed * 2));
+    s.w = reinterpret_cast<uint16_t*>(take(rows * packed * 2));
     if (backward) {
         s.mul = reinterpret_cast<float*>(take(8));
         s.g = reinterpret_cast<uint16_t*>(take(tokens * piece * 2));
-        s.sum = reinterpret_cast<float*>(take(tokens * ceil_to(width, 4) * 4 * dx_shape(tokens, width, piece).splits));
+        const int splits = std::max(dx_shape(tokens, width, piece).splits, dx_shape(tokens, width, rows).splits);
+        s.sum = reinterpret_cast<float*>(take(tokens * ceil_to(width, 4) * 4 * splits));
     }
     s.bytes = at;
     return s;
@@ -819,7 +826,7 @@ hipError_t forward(const XentArgs& a, void* ws, hipStream_t stream) {
     if (a.tokens) {
         Operands o;
         pack_x(a, s, &o, stream);
-        const int64_t piece = loads16(a.w, a.w_stride, a.width) ? a.vocab : piece_of(a.tokens, a.vocab, a.width);
+        const int64_t piece = loads16(a.w, a.w_stride, a.width) ? a.vocab : packed_piece(a.tokens, a.vocab, a.width);
         const int bn = token_tile(a.tokens, tiles_of(std::min(piece, a.vocab), BM));
         for (int64_t v0 = 0; v0 < a.vocab; v0 += piece) {
             pack_w(a, s, v0, std::min(piece, a.vocab - v0), &o, stream);
@@ -843,7 +850,8 @@ hipError_t forward(const XentArgs& a, void* ws, hipStream_t stream) {
 template <int DT>
 hipError_t backward(const XentArgs& a, void* ws, hipStream_t stream) {
     const Space s = space_of(static_cast<char*>(ws), a.tokens, a.vocab, a.width, true);
-    const int64_t piece = piece_of(a.tokens, a.vocab, a.width);
+    const int64_t piece = loads16(a.w, a.w_stride, a.width) ? piece_of(a.tokens, a.vocab, a.width)
+                                                            : packed_piece(a.tokens, a.vocab, a.width);
     const int bn = token_tile(a.tokens, tiles_of(std::min(piece, a.vocab), BM));
     const DxShape shape = dx_shape(a.tokens, a.width, piece);
     const int splits = shape.splits;
