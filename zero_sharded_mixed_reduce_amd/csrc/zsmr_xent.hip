@@ -28,6 +28,7 @@
 
 #include "zsmr_dev.h"
 #include "zsmr_ops_launch.h"
+#include "zsmr_xent_plan.h"
 
 #pragma clang fp contract(off)
 
@@ -40,7 +41,6 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
 constexpr int kWaves = 8, kThreads = kWaves * 64;
-constexpr int BM = 256, BK = 64;
 
 template <int DT>
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
@@ -177,8 +177,6 @@ __device__ __forceinline__ void interleave() {
 #define ZSMR_WAIT(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | 0x70 | ((n) >> 4 << 14))
 
 // ------------------------------------------------------------------ product --
-enum : int { E_STATS, E_GRAD, E_DX, E_DW };
-
 struct Product {
     Mat a, b;
     int64_t k;                      // of the product
@@ -640,132 +638,38 @@ __global__ __launch_bounds__(256) void splits_kernel(Product p) {
 }
 
 // --------------------------------------------------------------------- host --
-int64_t ceil_to(int64_t n, int64_t k) { return (n + k - 1) / k * k; }
-int64_t tiles_of(int64_t n, int64_t k) { return (n + k - 1) / k; }
-
-constexpr int64_t kCus = 256;
-
-// Tokens of a tile, and what a step of 64 k takes with so many on MI355X, in
-// twentieths of a microsecond.
-constexpr int kWidths = 4, kWidth[kWidths] = {64, 128, 192, 256}, kCost[kWidths] = {11, 18, 25, 32};
-
-// Tokens of a tile, given the tiles on the other side: the width whose rounds
-// over the CUs end soonest.  215 tokens over 2,113 x 3,832 with gradients take 134
-// us in tiles of 64, in one of 256 230; 8,192 over 50,257 x 768 2.5 ms in tiles of
-// 256.
-int token_tile(int64_t tokens, int64_t others) {
-    int best = 0;
-    int64_t least = INT64_MAX;
-    for (int i = 0; i < kWidths; ++i) {
-        const int64_t n = tiles_of(std::max<int64_t>(tokens, 1), kWidth[i]);
-        const int64_t ends = tiles_of(n * others, kCus) * kCost[i];
-        if (ends < least) {
-            least = ends;
-            best = kWidth[i];
-        }
-        if (n == 1) break;                  // wider tiles only pad
-    }
-    return best;
-}
-
-// The vocabulary's pieces: G of one takes about 512 MB at most, and the tiles of
-// dw over one fill the 256 CUs a whole number of times if it has that many.
-constexpr int64_t kMaxPiece = int64_t(1) << 21;     // G's rows: byte offsets within a tile fit 31 bits
-int64_t piece_of(int64_t tokens, int64_t vocab, int64_t width) {
-    int64_t tiles = std::max<int64_t>(1, (int64_t(1) << 28) / std::max<int64_t>(tokens, 1) / BM);
-    tiles = std::min<int64_t>(tiles, kMaxPiece / BM);
-    if (tiles >= tiles_of(vocab, BM)) return ceil_to(vocab, BM);
-    const int64_t across = tiles_of(width, BM), rounds = tiles * across / kCus;
-    if (rounds > 0) tiles = rounds * kCus / across;
-    return tiles * BM;
-}
-// Pieces of weights that have to be packed first: their copy stays under 268 MB at
-// width 4,096, also where G would allow more rows.
-int64_t packed_piece(int64_t tokens, int64_t vocab, int64_t width) {
-    return std::min<int64_t>(piece_of(tokens, vocab, width), 32768);
-}
-// The dx product: its k splits (none shorter than 512 of k) and the tokens of a
-// tile.  Splits fill the CUs once or twice, but each writes and reads T x H sums at
-// about 5 TB/s.  8,192 tokens of width 768: 5 splits in tiles of 256; 129 tokens:
-// 28 in tiles of 64, 29 us with the sums on MI355X, where 49 in tiles of 192 took
-// 36.
-struct DxShape {
-    int splits, tile;
-};
-DxShape dx_shape(int64_t tokens, int64_t width, int64_t piece) {
-    DxShape best{};
-    double least = 0;
-    for (int i = 0; i < kWidths; ++i) {
-        const int64_t n = tiles_of(std::max<int64_t>(tokens, 1), kWidth[i]), tiles = n * tiles_of(width, BM);
-        for (int rounds = 1; rounds <= 2; ++rounds) {
-            const int64_t splits = std::max<int64_t>(1, std::min(rounds * kCus / tiles, piece / 512));
-            double us = (double)tiles_of(tiles * splits, kCus) * kCost[i] / 20 * tiles_of(piece, BK * splits);
-            if (splits > 1) us += (double)splits * tokens * width * 8 / 5e6;
-            if (!best.tile || us < least) {
-                least = us;
-                best = DxShape{(int)splits, kWidth[i]};
-            }
-        }
-        if (n == 1) break;
-    }
-    return best;
-}
-
-// Vocabulary rows of a tile of dw: 256, or 128, which take a little over half as
-// long, where that ends sooner.  A piece of 27 tiles of 256 across 3 (8,192
-// tokens, width 768) fills a third of the CUs once: 184 us on MI355X, in tiles of
-// 128 119-124.
-int dw_tile(int64_t across, int64_t rows) {
-    const int64_t wide = tiles_of(across * tiles_of(rows, 256), kCus), narrow = tiles_of(across * tiles_of(rows, 128), kCus);
-    return narrow * 11 < wide * 20 ? 128 : 256;
-}
-
 struct Space {
     float2* stats;
     float *target, *mul, *sum;
     uint16_t *x, *w, *g;
-    int64_t bytes;
 };
-Space space_of(char* ws, int64_t tokens, int64_t vocab, int64_t width, bool backward) {
+Space space_of(void* ws, int64_t tokens, int64_t vocab, int64_t width, bool backward) {
+    const XentSpace at = xent_space(tokens, vocab, width, backward);
+    char* const p = static_cast<char*>(ws);
     Space s{};
-    int64_t at = 0;
-    auto take = [&](int64_t bytes) {
-        char* p = ws + at;
-        at += ceil_to(bytes, 256);
-        return p;
-    };
-    const int64_t piece = piece_of(tokens, vocab, width), packed = ceil_to(width, 8);
-    const int64_t rows = packed_piece(tokens, vocab, width);
-    s.stats = reinterpret_cast<float2*>(take(tiles_of(vocab, BM) * tokens * 8));
-    s.target = reinterpret_cast<float*>(take(tokens * 4));
-    s.x = reinterpret_cast<uint16_t*>(take(tokens * packed * 2));
-    s.w = reinterpret_cast<uint16_t*>(take(rows * packed * 2));
-    if (backward) {
-        s.mul = reinterpret_cast<float*>(take(8));
-        s.g = reinterpret_cast<uint16_t*>(take(tokens * piece * 2));
-        const int splits = std::max(dx_shape(tokens, width, piece).splits, dx_shape(tokens, width, rows).splits);
-        s.sum = reinterpret_cast<float*>(take(tokens * ceil_to(width, 4) * 4 * splits));
-    }
-    s.bytes = at;
+    s.stats = reinterpret_cast<float2*>(p + at.stats);
+    s.target = reinterpret_cast<float*>(p + at.target);
+    s.x = reinterpret_cast<uint16_t*>(p + at.x);
+    s.w = reinterpret_cast<uint16_t*>(p + at.w);
+    s.mul = reinterpret_cast<float*>(p + at.mul);
+    s.g = reinterpret_cast<uint16_t*>(p + at.g);
+    s.sum = reinterpret_cast<float*>(p + at.sum);
     return s;
 }
 
 template <int DT, int EPI>
-void launch_product(const Product& p, int bn, hipStream_t stream) {
-    const unsigned grid = (unsigned)(p.m_tiles * p.n_tiles * p.splits);
+void launch_product(const Product& p, const ProductShape& shape, hipStream_t stream) {
+    const unsigned grid = (unsigned)shape.grid();
     if constexpr (EPI == E_DW) {
-        if (bn == 128) product_kernel<DT, EPI, 128, 4, 3, false><<<grid, kThreads, 0, stream>>>(p);
+        if (shape.tile == 128) product_kernel<DT, EPI, 128, 4, 3, false><<<grid, kThreads, 0, stream>>>(p);
         else product_kernel<DT, EPI, 256, 2, 2, false><<<grid, kThreads, 0, stream>>>(p);
-    } else if (bn == 64) {
-        // Two workgroups share a CU's LDS with two stages each; where there is
-        // at most one for a CU it takes four, and waits a third as long: 44 tokens
-        // over 1,892 x 4,008 106 -> 38 us on MI355X.
-        if (grid > kCus && p.n_tiles == 1) product_kernel<DT, EPI, 64, 8, 2, true><<<grid, kThreads, 0, stream>>>(p);
+    } else if (shape.tile == 64) {
+        if (shape.once) product_kernel<DT, EPI, 64, 8, 2, true><<<grid, kThreads, 0, stream>>>(p);
         else product_kernel<DT, EPI, 64, 8, 4, false><<<grid, kThreads, 0, stream>>>(p);
-    } else if (bn == 128) {
-        if (p.n_tiles == 1) product_kernel<DT, EPI, 128, 4, 3, true><<<grid, kThreads, 0, stream>>>(p);
+    } else if (shape.tile == 128) {
+        if (shape.once) product_kernel<DT, EPI, 128, 4, 3, true><<<grid, kThreads, 0, stream>>>(p);
         else product_kernel<DT, EPI, 128, 4, 3, false><<<grid, kThreads, 0, stream>>>(p);
-    } else if (bn == 192) {
+    } else if (shape.tile == 192) {
         product_kernel<DT, EPI, 192, 2, 2, false><<<grid, kThreads, 0, stream>>>(p);
     } else {
         product_kernel<DT, EPI, 256, 2, 2, false><<<grid, kThreads, 0, stream>>>(p);
@@ -801,17 +705,15 @@ void pack_w(const XentArgs& a, const Space& s, int64_t v0, int64_t rows, Operand
     o->w = Mat{s.w, ld, rows, ld};
 }
 
-Product logits_of(const XentArgs& a, const Operands& o, int64_t v0, int bn) {
+// A product's sizes; its operands come next.
+Product product_of(const XentArgs& a, const ProductShape& shape) {
     Product p{};
-    p.a = o.w;
-    p.b = o.x;
-    p.k = std::min(o.w.cols, o.x.cols);
-    p.a.cols = p.b.cols = p.k;
-    p.m_tiles = (int32_t)tiles_of(o.w.rows, BM);
-    p.n_tiles = (int32_t)tiles_of(a.tokens, bn);
-    p.splits = 1;
-    p.k_split = (int32_t)ceil_to(p.k, BK);
-    p.v0 = v0;
+    p.k = shape.k;
+    p.m_tiles = (int32_t)shape.m_tiles;
+    p.n_tiles = (int32_t)shape.n_tiles;
+    p.splits = shape.splits;
+    p.k_split = (int32_t)shape.k_split;
+    p.v0 = shape.v0;
     p.vocab = a.vocab;
     p.tokens = a.tokens;
     p.width = a.width;
@@ -819,22 +721,27 @@ Product logits_of(const XentArgs& a, const Operands& o, int64_t v0, int bn) {
     p.id_bytes = a.id_bytes;
     return p;
 }
+// The operands of the logits.
+void set_logits(Product* p, const Operands& o) {
+    p->a = o.w;
+    p->b = o.x;
+    p->a.cols = p->b.cols = p->k;
+}
 
 template <int DT>
 hipError_t forward(const XentArgs& a, void* ws, hipStream_t stream) {
-    const Space s = space_of(static_cast<char*>(ws), a.tokens, a.vocab, a.width, false);
+    const Space s = space_of(ws, a.tokens, a.vocab, a.width, false);
     if (a.tokens) {
         Operands o;
         pack_x(a, s, &o, stream);
-        const int64_t piece = loads16(a.w, a.w_stride, a.width) ? a.vocab : packed_piece(a.tokens, a.vocab, a.width);
-        const int bn = token_tile(a.tokens, tiles_of(std::min(piece, a.vocab), BM));
-        for (int64_t v0 = 0; v0 < a.vocab; v0 += piece) {
-            pack_w(a, s, v0, std::min(piece, a.vocab - v0), &o, stream);
-            Product p = logits_of(a, o, v0, bn);
+        forward_products(a.tokens, a.vocab, a.width, !loads16(a.w, a.w_stride, a.width), [&](const ProductShape& shape) {
+            pack_w(a, s, shape.v0, shape.rows, &o, stream);
+            Product p = product_of(a, shape);
+            set_logits(&p, o);
             p.stats = s.stats;
             p.target = s.target;
-            launch_product<DT, E_STATS>(p, bn, stream);
-        }
+            launch_product<DT, E_STATS>(p, shape, stream);
+        });
         const int32_t parts = (int32_t)tiles_of(a.vocab, BM);
         // up to 256 tokens in one workgroup, which saves the launch of the mean
         const int lanes = a.tokens <= 256 ? (int)ceil_to(a.tokens, 16) : 64;
@@ -849,72 +756,56 @@ hipError_t forward(const XentArgs& a, void* ws, hipStream_t stream) {
 
 template <int DT>
 hipError_t backward(const XentArgs& a, void* ws, hipStream_t stream) {
-    const Space s = space_of(static_cast<char*>(ws), a.tokens, a.vocab, a.width, true);
-    const int64_t piece = loads16(a.w, a.w_stride, a.width) ? piece_of(a.tokens, a.vocab, a.width)
-                                                            : packed_piece(a.tokens, a.vocab, a.width);
-    const int bn = token_tile(a.tokens, tiles_of(std::min(piece, a.vocab), BM));
-    const DxShape shape = dx_shape(a.tokens, a.width, piece);
-    const int splits = shape.splits;
+    const Space s = space_of(ws, a.tokens, a.vocab, a.width, true);
+    const bool packed = !loads16(a.w, a.w_stride, a.width);
+    const int64_t piece = packed ? packed_piece(a.tokens, a.vocab, a.width) : piece_of(a.tokens, a.vocab, a.width);
     const bool fp16 = DT == ZSMR_FP16, weighted = fp16 && a.grad;
     if (weighted) mul_kernel<<<1, kMulThreads, 0, stream>>>(a.grad, a.tokens, a.scale, s.mul);
     Operands o;
     pack_x(a, s, &o, stream);
-    for (int64_t v0 = 0; v0 < a.vocab; v0 += piece) {
-        const int64_t rows = std::min(piece, a.vocab - v0);
-        if (a.tokens) pack_w(a, s, v0, rows, &o, stream);
-        else o.w = Mat{a.w, a.w_stride, rows, a.width};     // no token: dw is zero, nothing is read
-        Product p = logits_of(a, o, v0, bn);
-        p.lse = a.lse;
-        p.grad = a.grad;
+    backward_products(a.tokens, a.vocab, a.width, packed, a.dx, a.dw, [&](const ProductShape& shape) {
+        Product p = product_of(a, shape);
         p.mul = weighted ? s.mul : nullptr;
         p.g_mul = fp16 ? kFp16Mul : 1.f;
         p.out_mul = fp16 ? 1.f / kFp16Mul : 1.f;
         p.scale = a.scale;
-        p.g = s.g;
-        p.ldg = piece;
-        if (a.tokens) launch_product<DT, E_GRAD>(p, bn, stream);
-        const int64_t padded = ceil_to(rows, 8);        // G is zero past the vocabulary
-        if (a.dx && a.tokens) {
-            Product d = p;
-            d.a = o.w;
-            d.b = Mat{s.g, piece, a.tokens, padded};
-            d.k = padded;
-            d.m_tiles = (int32_t)tiles_of(a.width, BM);
-            d.n_tiles = (int32_t)tiles_of(a.tokens, shape.tile);
-            d.splits = splits;
-            d.k_split = (int32_t)ceil_to(tiles_of(padded, splits), BK);
-            d.sum = s.sum;
-            d.lds = ceil_to(a.width, 4);
-            d.sum_in = v0 > 0;
-            d.sum_out = splits > 1 || v0 + piece < a.vocab;
-            d.out = a.dx;
-            d.ldo = a.dx_stride;
-            launch_product<DT, E_DX>(d, shape.tile, stream);
-            if (splits > 1 && v0 + piece >= a.vocab)
-                splits_kernel<DT><<<(unsigned)tiles_of(a.tokens * (d.lds / 4), 256), 256, 0, stream>>>(d);
+        if (shape.epi == E_GRAD) {
+            pack_w(a, s, shape.v0, shape.rows, &o, stream);
+            set_logits(&p, o);
+            p.lse = a.lse;
+            p.grad = a.grad;
+            p.g = s.g;
+            p.ldg = piece;
+            launch_product<DT, E_GRAD>(p, shape, stream);
+            return;
         }
-        if (a.dw) {
-            Product d = p;
-            d.a = o.x;
-            d.b = Mat{s.g, piece, a.tokens, padded};
-            d.k = a.tokens;
-            d.m_tiles = (int32_t)tiles_of(a.width, BM);
-            const int wide = dw_tile(d.m_tiles, rows);
-            d.n_tiles = (int32_t)tiles_of(rows, wide);
-            d.k_split = (int32_t)ceil_to(a.tokens, BK);
-            d.out = a.dw;
-            d.ldo = a.dw_stride;
-            d.accumulate = a.accumulate;
-            launch_product<DT, E_DW>(d, wide, stream);
+        p.b = Mat{s.g, piece, a.tokens, ceil_to(shape.rows, 8)};       // G is zero past the vocabulary
+        if (shape.epi == E_DX) {
+            p.a = o.w;
+            p.sum = s.sum;
+            p.lds = ceil_to(a.width, 4);
+            p.sum_in = shape.sum_in;
+            p.sum_out = shape.sum_out;
+            p.out = a.dx;
+            p.ldo = a.dx_stride;
+            launch_product<DT, E_DX>(p, shape, stream);
+            if (shape.splits > 1 && shape.v0 + piece >= a.vocab)
+                splits_kernel<DT><<<(unsigned)tiles_of(a.tokens * (p.lds / 4), 256), 256, 0, stream>>>(p);
+        } else {
+            p.a = o.x;
+            p.out = a.dw;
+            p.ldo = a.dw_stride;
+            p.accumulate = a.accumulate;
+            launch_product<DT, E_DW>(p, shape, stream);
         }
-    }
+    });
     return hipGetLastError();
 }
 
 }  // namespace
 
 int64_t xent_bytes(int64_t tokens, int64_t vocab, int64_t width, bool backward) {
-    return space_of(nullptr, tokens, vocab, width, backward).bytes;
+    return xent_space(tokens, vocab, width, backward).bytes;
 }
 
 hipError_t launch_xent_forward(const XentArgs& a, void* ws, hipStream_t stream) {
