@@ -576,16 +576,18 @@ __global__ __launch_bounds__(kMeanThreads) void mean_kernel(const float* loss, c
 // the results are divided by again.  bf16 has fp32's range and needs none.  fp16
 // has all its bits down to 2^-14 only, and most probabilities of a large
 // vocabulary are below that: there |G| <= max |grad| is moved to [2^14, 2^15),
-// just below fp16's largest value.
+// just below fp16's largest value.  The maximum is over the tokens that count:
+// padding has no gradient, whatever its weight.
 constexpr float kFp16Mul = 16384.f;
 constexpr int kMulThreads = 1024;
-__global__ __launch_bounds__(kMulThreads) void mul_kernel(const float* grad, int64_t tokens, const float* scale,
+__global__ __launch_bounds__(kMulThreads) void mul_kernel(const float* grad, const void* labels, int32_t id_bytes,
+                                                          int64_t tokens, int64_t vocab, const float* scale,
                                                           float* mul) {
     __shared__ float part[kMulThreads / 64];
     float top = 0.f;
     for (int64_t t = threadIdx.x; t < tokens; t += kMulThreads) {
         const float g = fabsf(grad[t]);
-        if (g < INFINITY) top = fmaxf(top, g);
+        if (g < INFINITY && token_at(labels, id_bytes, t, vocab) >= 0) top = fmaxf(top, g);
     }
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
@@ -760,7 +762,7 @@ hipError_t backward(const XentArgs& a, void* ws, hipStream_t stream) {
     const bool packed = !loads16(a.w, a.w_stride, a.width);
     const int64_t piece = packed ? packed_piece(a.tokens, a.vocab, a.width) : piece_of(a.tokens, a.vocab, a.width);
     const bool fp16 = DT == ZSMR_FP16, weighted = fp16 && a.grad;
-    if (weighted) mul_kernel<<<1, kMulThreads, 0, stream>>>(a.grad, a.tokens, a.scale, s.mul);
+    if (weighted) mul_kernel<<<1, kMulThreads, 0, stream>>>(a.grad, a.labels, a.id_bytes, a.tokens, a.vocab, a.scale, s.mul);
     Operands o;
     pack_x(a, s, &o, stream);
     backward_products(a.tokens, a.vocab, a.width, packed, a.dx, a.dw, [&](const ProductShape& shape) {
