@@ -43,3 +43,28 @@ def test_weights_of_tokens_that_do_not_count(dt, value):
     for a, b in zip(want, got):
         assert torch.equal(bits(a), bits(b))
     assert bool((got[3][off] == 0).all()) and bool((got[4] != 0).any())
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -65504.0])
+@pytest.mark.parametrize("n,vocab,width,stride,dt", [(70, 300, 64, 0, "bf16"), (300, 1000, 136, 0, "fp16"), (90, 600, 65, 67, "bf16"), (1, 40, 8, 0, "fp16")])
+def test_hidden_states_of_tokens_that_do_not_count(n, vocab, width, stride, dt, value):
+    """Nor does it matter what a token without a label holds in x: the bits of
+    zeros there, in every gradient, and a loss of zero."""
+    say("[x of padding]", n, vocab, width, stride, dt, value)
+    g, t = gen(22), T16[dt]
+    x, w = normal(g, (n, width), 1.0, t, stride), normal(g, (vocab, width), 0.2, t, stride)
+    labels = tokens(g, n, vocab, "some")
+    labels[0] = -1
+    off = (labels < 0) | (labels >= vocab)
+    old = normal(g, (vocab, width), 0.1, t)
+    for accumulate in (None, old):
+        x[off] = 0
+        want = xent_both(x, w, labels, accumulate=accumulate)
+        x[off] = value
+        before = x.clone()
+        got = xent_both(x, w, labels, accumulate=accumulate)
+        assert torch.equal(bits(x), bits(before)), "x was written"
+        for a, b, name in zip(want, got, ("loss", "lse", "summary", "dx", "dw")):
+            keep = ~off if name == "lse" else slice(None)
+            assert torch.equal(bits(a[keep]), bits(b[keep])), name
+        assert bool((got[0][off] == 0).all()) and bool((got[3][off] == 0).all())

@@ -602,14 +602,17 @@ __global__ __launch_bounds__(kMulThreads) void mul_kernel(const float* grad, con
 }
 
 // Rows of any length, stride and alignment to rows of a multiple of 8 elements,
-// zero-filled: what the products' 16-byte loads need.
+// zero-filled: what the products' 16-byte loads need.  With labels, rows of
+// tokens that do not count become zeros.
 __global__ __launch_bounds__(256) void pack_kernel(const uint16_t* src, int64_t stride, int64_t rows,
-                                                   int64_t width, uint16_t* dst, int64_t ld) {
+                                                   int64_t width, uint16_t* dst, int64_t ld, const void* labels,
+                                                   int32_t id_bytes, int64_t vocab) {
     const int64_t vecs = ld / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t row = i / vecs, j = (i - row * vecs) * 8;
     if (row >= rows) return;
     u16x8 h = 0;
-    if (j + 8 <= width) {
+    if (labels && token_at(labels, id_bytes, row, vocab) < 0) {
+    } else if (j + 8 <= width) {
         h = *reinterpret_cast<const u16x8_any*>(src + row * stride + j);
     } else {
 #pragma unroll
@@ -681,29 +684,30 @@ void launch_product(const Product& p, const ProductShape& shape, hipStream_t str
 bool loads16(const uint16_t* p, int64_t stride, int64_t width) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0 && width % 8 == 0;
 }
-void pack(const uint16_t* src, int64_t stride, int64_t rows, int64_t width, uint16_t* dst, int64_t ld,
-          hipStream_t stream) {
-    if (!rows) return;
-    pack_kernel<<<(unsigned)tiles_of(rows * (ld / 8), 256), 256, 0, stream>>>(src, stride, rows, width, dst, ld);
-}
 
 // The operands of the products over the vocabulary from v0 on.  Operands that
 // 16-byte loads cannot read are packed first: x once, w piece by piece.
 struct Operands {
     Mat x, w;
 };
-void pack_x(const XentArgs& a, const Space& s, Operands* o, hipStream_t stream) {
+// counted: dw is asked for.  It adds G's rows times x's, and zero times what is not
+// finite is NaN, so tokens that do not count must not bring their x: it is packed
+// with zeros there, whatever its alignment.  On MI355X that takes 2 us of the 130
+// of 129 tokens over 50,257 x 768, 8 of 2,490 with 8,192 tokens.
+void pack_x(const XentArgs& a, const Space& s, bool counted, Operands* o, hipStream_t stream) {
     o->x = Mat{a.x, a.x_stride, a.tokens, a.width};
-    if (loads16(a.x, a.x_stride, a.width)) return;
+    if (!a.tokens || (!counted && loads16(a.x, a.x_stride, a.width))) return;
     const int64_t ld = ceil_to(a.width, 8);
-    pack(a.x, a.x_stride, a.tokens, a.width, s.x, ld, stream);
+    pack_kernel<<<(unsigned)tiles_of(a.tokens * (ld / 8), 256), 256, 0, stream>>>(
+        a.x, a.x_stride, a.tokens, a.width, s.x, ld, counted ? a.labels : nullptr, a.id_bytes, a.vocab);
     o->x = Mat{s.x, ld, a.tokens, ld};
 }
 void pack_w(const XentArgs& a, const Space& s, int64_t v0, int64_t rows, Operands* o, hipStream_t stream) {
-    o->w = Mat{a.w + v0 * a.w_stride, a.w_stride, rows, a.width};
+    const uint16_t* w = a.w + v0 * a.w_stride;
+    o->w = Mat{w, a.w_stride, rows, a.width};
     if (loads16(a.w, a.w_stride, a.width)) return;
     const int64_t ld = ceil_to(a.width, 8);
-    pack(a.w + v0 * a.w_stride, a.w_stride, rows, a.width, s.w, ld, stream);
+    pack_kernel<<<(unsigned)tiles_of(rows * (ld / 8), 256), 256, 0, stream>>>(w, a.w_stride, rows, a.width, s.w, ld, nullptr, 0, 0);
     o->w = Mat{s.w, ld, rows, ld};
 }
 
@@ -735,7 +739,7 @@ hipError_t forward(const XentArgs& a, void* ws, hipStream_t stream) {
     const Space s = space_of(ws, a.tokens, a.vocab, a.width, false);
     if (a.tokens) {
         Operands o;
-        pack_x(a, s, &o, stream);
+        pack_x(a, s, false, &o, stream);
         forward_products(a.tokens, a.vocab, a.width, !loads16(a.w, a.w_stride, a.width), [&](const ProductShape& shape) {
             pack_w(a, s, shape.v0, shape.rows, &o, stream);
             Product p = product_of(a, shape);
@@ -764,7 +768,7 @@ hipError_t backward(const XentArgs& a, void* ws, hipStream_t stream) {
     const bool fp16 = DT == ZSMR_FP16, weighted = fp16 && a.grad;
     if (weighted) mul_kernel<<<1, kMulThreads, 0, stream>>>(a.grad, a.labels, a.id_bytes, a.tokens, a.vocab, a.scale, s.mul);
     Operands o;
-    pack_x(a, s, &o, stream);
+    pack_x(a, s, a.dw, &o, stream);
     backward_products(a.tokens, a.vocab, a.width, packed, a.dx, a.dw, [&](const ProductShape& shape) {
         Product p = product_of(a, shape);
         p.mul = weighted ? s.mul : nullptr;
