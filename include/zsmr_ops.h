@@ -75,6 +75,7 @@ int32_t zsmr_embed_grad(const void* dout, int64_t dout_stride, int32_t dtype, co
  * labels as ids above (outside [0, vocab): the token does not count, its loss
  * and gradient are zero, and its x and weight may hold anything).  With s[t, v] = x[t, :] . w[v, :],
  *   lse[t] = log sum_v exp s[t, v],   loss[t] = lse[t] - s[t, label_t].
+ * A logit below -2.3e38 counts as -infinity; one above 2.3e38 makes lse infinite.
  * The logits exist a tile (forward) or a piece of the vocabulary (backward,
  * as 16-bit probabilities) at a time. */
 

@@ -5,7 +5,7 @@ import torch
 
 import zero_sharded_mixed_reduce_amd as z
 from tests.gpu_helpers import say
-from tests.test_gpu_ops import T16, gen, normal, space, tokens
+from tests.test_gpu_ops import T16, U, gen, half, normal, space, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +68,31 @@ def test_hidden_states_of_tokens_that_do_not_count(n, vocab, width, stride, dt, 
             keep = ~off if name == "lse" else slice(None)
             assert torch.equal(bits(a[keep]), bits(b[keep])), name
         assert bool((got[0][off] == 0).all()) and bool((got[3][off] == 0).all())
+
+
+def test_logits_near_the_ends_of_fp32():
+    """Rows of the head that give the lowest logits fp32 has are as good as
+    absent, also where a whole tile of the vocabulary is of them; logits of
+    3e38 make the statistics infinite and are not passed over."""
+    g, t = gen(23), torch.bfloat16
+    n, vocab, width = 40, 900, 64
+    x, w = normal(g, (n, width), 1.0, t), normal(g, (vocab, width), 0.2, t)
+    x[:, 0] = 1
+    labels = torch.randint(256, (n,), generator=g, device="cuda")
+    low = w.clone()
+    low[256:768] = 0
+    low[256:768, 0] = torch.finfo(t).min
+    loss, lse, summary, dx, dw = xent_both(x, low, labels)
+    rest = torch.cat([w[:256], w[768:]])
+    want = xent_both(x, rest, labels)
+    # fp32 sums of the same exponentials in another order
+    tol = 2.0 ** -20 + 600 * U
+    assert float((lse - want[1]).abs().max()) <= tol and float((loss - want[0]).abs().max()) <= tol
+    assert bool((dw[256:768] == 0).all())
+    # G, held in 16 bits, and the result's rounding
+    assert float((dx.double() - want[3].double()).norm()) <= 2 * half(t) * float(want[3].double().norm())
+    high = w.clone()
+    high[300] = 0
+    high[300, 0] = 3e38
+    loss, lse, *_ = xent_both(x, high, labels)
+    assert bool(torch.isinf(lse).all()) and bool((lse > 0).all()) and bool(torch.isinf(loss).all())

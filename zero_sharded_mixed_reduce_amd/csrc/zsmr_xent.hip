@@ -212,6 +212,13 @@ template <typename = void>
 __device__ __forceinline__ float exp2_of(float s, float shift) {
     return __builtin_amdgcn_exp2f(__builtin_fmaf(s, kLog2e, -shift));
 }
+// The shift of a maximum, which is held to +-2.3e38 so that it stays finite: rows
+// below that alone (or none at all, -inf) add up to zero and one above it makes the
+// sum infinite, where shifts of -+inf would give NaN or pass over it.
+template <typename = void>
+__device__ __forceinline__ float shift_of(float top) {
+    return __builtin_amdgcn_fmed3f(top, -2.3e38f, 2.3e38f) * kLog2e;
+}
 // Two parts of a softmax: (shift, sum of the powers relative to it).
 __device__ __forceinline__ float2 join_parts(float2 a, float2 b) {
     const float top = fmaxf(a.x, b.x);
@@ -404,11 +411,10 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
             for (int i = 0; i < TM; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) top = fmaxf(top, acc[i][j][r]);
-            // the four lane groups hold other rows of the same column; the
-            // power's argument must not become -inf + inf where no row is left
+            // the four lane groups hold other rows of the same column
 #pragma unroll
             for (int d = 16; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-            const float shift = top == -INFINITY ? 0.f : top * kLog2e;
+            const float shift = shift_of(top);
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < TM; ++i)
