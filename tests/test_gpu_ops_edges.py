@@ -96,3 +96,24 @@ def test_logits_near_the_ends_of_fp32():
     high[300, 0] = 3e38
     loss, lse, *_ = xent_both(x, high, labels)
     assert bool(torch.isinf(lse).all()) and bool((lse > 0).all()) and bool(torch.isinf(loss).all())
+
+
+def test_a_list_that_can_be_gone_through_once():
+    """The gradients of a model's parameters, as a generator gives them: the bits
+    of the same tensors in a list."""
+    g = gen(25)
+    xs = [torch.randn(k, generator=g, device="cuda") for k in (7, 5000, 1)]
+    a, b = torch.empty(2, device="cuda"), torch.empty(2, device="cuda")
+    ws, _ = space(z.zsmr_norm_workspace(5008, 3))
+    z.zsmr_grad_norm(xs, 1.0, a, ws)
+    z.zsmr_grad_norm((x for x in xs), 1.0, b, ws)
+    assert torch.equal(a, b) and a[0].item() > 0
+    rows = [torch.empty(5008, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    z.zsmr_clip_flatten(xs, a[1:], rows[0])
+    z.zsmr_clip_flatten((x for x in xs), a[1:], rows[1])
+    assert torch.equal(bits(rows[0]), bits(rows[1]))
+    ys = [x.clone() for x in xs]
+    z.zsmr_clip_grads(xs, a[1:])
+    z.zsmr_clip_grads((y for y in ys), a[1:])
+    for x, y in zip(xs, ys):
+        assert torch.equal(bits(x), bits(y))

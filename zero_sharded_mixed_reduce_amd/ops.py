@@ -6,7 +6,7 @@ whose last dimension is contiguous (any stride between rows); their sizes,
 strides and formats come from the tensors, which are checked against each
 other before the library is called.  All arithmetic runs in its HIP kernels.
 
-A list of gradient tensors is either a sequence of contiguous torch tensors, or
+A list of gradient tensors is either any iterable of contiguous torch tensors, or
 ``(addresses, numels, dtypes)``: three numpy arrays (int64, int64, int32 format
 codes) that a program may keep as long as its tensors stay where they are.
 """
@@ -111,6 +111,7 @@ def _list(tensors) -> tuple:
     """A tensor list's three arrays."""
     if type(tensors) is tuple and len(tensors) == 3 and isinstance(tensors[0], np.ndarray):
         return tensors
+    tensors = list(tensors)         # gone through more than once below
     for i, x in enumerate(tensors):
         if not x.is_contiguous() or x.dtype not in TENSOR_CODES:
             raise ValueError(f"tensor list: tensor {i} is not contiguous fp16, bf16 or fp32")
