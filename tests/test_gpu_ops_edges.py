@@ -117,3 +117,36 @@ def test_a_list_that_can_be_gone_through_once():
     z.zsmr_clip_grads((y for y in ys), a[1:])
     for x, y in zip(xs, ys):
         assert torch.equal(bits(x), bits(y))
+
+
+def test_embedding_gradient_of_more_rows_than_a_launch_zeroes():
+    """2^28 + 5 rows of width 8: a workgroup for every 16 of them would be 2^32
+    work items and more."""
+    vocab, t = (1 << 28) + 5, torch.bfloat16
+    table = torch.ones(vocab, 8, device="cuda", dtype=t)
+    ids = torch.tensor([vocab - 1, 0, 1 << 28, -1], device="cuda")
+    rows = torch.randn(4, 8, generator=gen(26), device="cuda").to(t)
+    ws, _ = space(z.zsmr_embed_grad_workspace(vocab, 8, 4))
+    z.zsmr_embed_grad(rows, ids, table, ws)
+    assert torch.equal(table[ids[:3]], rows[:3])
+    assert sum(int((part != 0).any(1).sum()) for part in table.split(1 << 26)) == 3
+    del table
+    torch.cuda.empty_cache()
+
+
+def test_lookup_of_more_elements_than_a_launch_has_work_items():
+    """2^24 tokens of width 2,056: 2^32 groups of eight elements and more, 69 GB of
+    output."""
+    n, width, t = 1 << 24, 2056, torch.bfloat16
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB of free device memory")
+    g = gen(27)
+    table = normal(g, (1000, width), 1.0, t)
+    ids = torch.randint(-1, 1000, (n,), generator=g, device="cuda", dtype=torch.int32)
+    out = torch.full((n, width), 7.0, device="cuda", dtype=t)
+    z.zsmr_embed_lookup(table, ids, out)
+    whole = torch.cat([table, torch.zeros(1, width, device="cuda", dtype=t)])       # -1 reads the last row
+    for k in range(0, n, 1 << 20):
+        assert torch.equal(out[k:k + (1 << 20)], whole[ids[k:k + (1 << 20)].long()]), k
+    del out
+    torch.cuda.empty_cache()

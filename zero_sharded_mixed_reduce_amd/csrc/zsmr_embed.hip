@@ -349,11 +349,13 @@ __device__ __forceinline__ void add_runs(const EmbedArgs& a, const uint32_t* key
     }
 }
 
-// The first workgroups add up runs, the others write zeros meanwhile.
+// The first workgroups add up runs, the others write zeros meanwhile.  first: of
+// this launch's workgroups.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void grad_kernel(EmbedArgs a, const uint32_t* key, const uint32_t* pos,
-                                                        float* part, int chunk, int64_t chunks, int col_blocks) {
-    const int64_t b = blockIdx.x, runs = chunks * col_blocks;
+                                                        float* part, int chunk, int64_t chunks, int col_blocks,
+                                                        int64_t first) {
+    const int64_t b = first + blockIdx.x, runs = chunks * col_blocks;
     if (b < runs) add_runs<DT>(a, key, pos, part, b / col_blocks, chunk, b % col_blocks * kBlockCols + threadIdx.x * 8);
     else zero_rows(a, key, (b - runs) * kZeroRows);
 }
@@ -419,16 +421,25 @@ void grad_launches(const EmbedArgs& a, const uint32_t* key, const uint32_t* pos,
     const int chunk = chunk_of(a.tokens), cols = (int)col_blocks_of(a.width);
     const int64_t chunks = (a.tokens + chunk - 1) / chunk;
     const int64_t zeros = a.accumulate ? 0 : (a.vocab + kZeroRows - 1) / kZeroRows;
-    grad_kernel<DT><<<(unsigned)(chunks * cols + zeros), kThreads, 0, stream>>>(a, key, pos, part, chunk, chunks, cols);
+    launch_groups(chunks * cols + zeros, [&](int64_t first, int64_t count) {
+        grad_kernel<DT><<<(unsigned)count, kThreads, 0, stream>>>(a, key, pos, part, chunk, chunks, cols, first);
+    });
     if (chunks > 1) join_runs_kernel<DT><<<dim3((unsigned)chunks, cols), kThreads, 0, stream>>>(a, key, part, chunk);
 }
 
 }  // namespace
 
 hipError_t launch_embed_lookup(const EmbedArgs& a, hipStream_t stream) {
-    const int64_t vecs = (a.width + 7) / 8, grid = (a.tokens * vecs + kThreads - 1) / kThreads;
-    if (a.dtype == ZSMR_BF16) lookup_kernel<ZSMR_BF16><<<(unsigned)grid, kThreads, 0, stream>>>(a, (uint32_t)vecs);
-    else lookup_kernel<ZSMR_FP16><<<(unsigned)grid, kThreads, 0, stream>>>(a, (uint32_t)vecs);
+    const int64_t vecs = (a.width + 7) / 8;
+    launch_rows(a.tokens, vecs, [&](int64_t first, int64_t count) {
+        EmbedArgs part = a;
+        part.tokens = count;
+        part.ids = static_cast<const char*>(a.ids) + first * a.id_bytes;
+        part.dst = a.dst + first * a.dst_stride;
+        const unsigned grid = (unsigned)((count * vecs + kThreads - 1) / kThreads);
+        if (a.dtype == ZSMR_BF16) lookup_kernel<ZSMR_BF16><<<grid, kThreads, 0, stream>>>(part, (uint32_t)vecs);
+        else lookup_kernel<ZSMR_FP16><<<grid, kThreads, 0, stream>>>(part, (uint32_t)vecs);
+    });
     return hipGetLastError();
 }
 

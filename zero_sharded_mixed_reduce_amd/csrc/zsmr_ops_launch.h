@@ -8,6 +8,20 @@
 
 namespace zsmr {
 
+// A launch has fewer than 2^32 work items in a dimension; in workgroups of 256:
+constexpr int64_t kMaxGroups = ((int64_t(1) << 32) - 1) / 256;
+// What is longer is launched in parts: rows of `items` work items each, from the
+// first one on, and workgroups.  each(first, count).
+template <typename F>
+void launch_rows(int64_t rows, int64_t items, F each) {
+    const int64_t most = kMaxGroups * 256 / items;
+    for (int64_t first = 0; first < rows; first += most) each(first, rows - first < most ? rows - first : most);
+}
+template <typename F>
+void launch_groups(int64_t groups, F each) {
+    launch_rows(groups, 256, each);
+}
+
 // ---- norm and clipping (zsmr_norm.hip)
 // Elements of a list tensor one workgroup handles at a time: few in a short
 // list, whose call is as long as one workgroup takes.  Norm and flatten of 54
