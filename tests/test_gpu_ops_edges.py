@@ -5,7 +5,7 @@ import torch
 
 import zero_sharded_mixed_reduce_amd as z
 from tests.gpu_helpers import say
-from tests.test_gpu_ops import T16, U, gen, half, normal, space, tokens
+from tests.test_gpu_ops import T16, U, gen, half, intact, normal, space, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -149,4 +149,33 @@ def test_lookup_of_more_elements_than_a_launch_has_work_items():
     for k in range(0, n, 1 << 20):
         assert torch.equal(out[k:k + (1 << 20)], whole[ids[k:k + (1 << 20)].long()]), k
     del out
+    torch.cuda.empty_cache()
+
+
+def test_scores_of_more_tiles_than_a_launch_holds():
+    """2^20 tokens over 2^20 + 300 rows: 2^24 tiles, which would be 2^33 work
+    items.  The statistics of some tokens against 64 bits."""
+    n, vocab, width, t = 1 << 20, (1 << 20) + 300, 64, torch.bfloat16
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB of free device memory")
+    g = gen(28)
+    x, w = normal(g, (n, width), 1.0, t), normal(g, (vocab, width), 0.25, t)
+    labels = torch.randint(vocab, (n,), generator=g, device="cuda")
+    some = torch.cat([torch.arange(40, device="cuda"), torch.randint(n, (40,), generator=g, device="cuda"), torch.arange(n - 40, n, device="cuda")])
+    labels[some[::3]] = torch.randint(vocab - 300, vocab, (40,), generator=g, device="cuda")
+    loss, lse, summary = (torch.full((k,), float("nan"), device="cuda") for k in (n, n, 3))
+    size = z.zsmr_xent_workspace(n, vocab, width, backward=False)
+    ws, raw = space(size)
+    z.zsmr_xent_forward(x, w, labels, loss, lse, summary, ws)
+    intact(raw, size)
+    s = x[some].double() @ w.double().t()
+    want = torch.logsumexp(s, 1)
+    # fp32 logits of 64 products, exponentials of fp32 arguments, sums over parts of 256 rows
+    es = float(U * width * (x[some].double().abs() @ w.double().abs().t()).max())
+    tol = es + 2.0 ** -20 + U * vocab / 64 + 4 * U * float(want.max())
+    assert float((lse[some].double() - want).abs().max()) <= tol
+    assert float((loss[some].double() - (want - s.gather(1, labels[some][:, None])[:, 0])).abs().max()) <= tol + es
+    assert bool(torch.isfinite(loss).all()) and summary[2].item() == n
+    assert abs(summary[0].item() - float(loss.double().mean())) <= 2 * U * summary[0].item()
+    del ws, raw
     torch.cuda.empty_cache()

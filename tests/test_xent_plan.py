@@ -5,6 +5,7 @@ under AddressSanitizer and UndefinedBehaviorSanitizer.
 
 * The pieces are whole tiles, at least one, and cover the vocabulary once; the
   tiles of each product cover its sides, its splits all of k.
+* No launch has 2^32 work items.
 * Every part of the workspace holds what the products put there.
 """
 import os
@@ -48,6 +49,7 @@ static void check(int64_t n, int64_t v, int64_t h) {
         if (n) {
             int64_t at = 0;
             forward_products(n, v, h, pack, [&](const ProductShape& p) {
+                CHECK(p.grid() * 512 < (int64_t(1) << 32));
                 CHECK(p.epi == E_STATS && p.v0 == at && p.v0 % BM == 0 && p.rows > 0);
                 CHECK(!pack || p.rows <= packed);
                 CHECK(p.m_tiles * BM >= p.rows && (p.m_tiles - 1) * BM < p.rows);
@@ -61,6 +63,8 @@ static void check(int64_t n, int64_t v, int64_t h) {
             if (p.epi == (n ? E_GRAD : E_DW)) { CHECK(p.v0 == at); at += p.rows; }
             ++seen[p.epi];
             CHECK(p.rows > 0 && p.rows <= rows && p.v0 + p.rows == at);
+            // x and w of 550 GB at most: no card holds more
+            CHECK(p.grid() * 512 < (int64_t(1) << 32) || n * h > (int64_t(1) << 38) || v * h > (int64_t(1) << 38));
             CHECK(p.k_split % BK == 0 && p.k_split * p.splits >= p.k && p.splits >= 1);
             const int64_t m = p.epi == E_GRAD ? p.rows : h, across = p.epi == E_DW ? p.rows : n;
             CHECK(p.m_tiles * BM >= m && (p.m_tiles - 1) * BM < m && p.n_tiles * p.tile >= across && (p.n_tiles - 1) * p.tile < across);

@@ -704,8 +704,11 @@ void pack_x(const XentArgs& a, const Space& s, bool counted, Operands* o, hipStr
     o->x = Mat{a.x, a.x_stride, a.tokens, a.width};
     if (!a.tokens || (!counted && loads16(a.x, a.x_stride, a.width))) return;
     const int64_t ld = ceil_to(a.width, 8);
-    pack_kernel<<<(unsigned)tiles_of(a.tokens * (ld / 8), 256), 256, 0, stream>>>(
-        a.x, a.x_stride, a.tokens, a.width, s.x, ld, counted ? a.labels : nullptr, a.id_bytes, a.vocab);
+    launch_rows(a.tokens, ld / 8, [&](int64_t first, int64_t count) {
+        const char* labels = counted ? static_cast<const char*>(a.labels) + first * a.id_bytes : nullptr;
+        pack_kernel<<<(unsigned)tiles_of(count * (ld / 8), 256), 256, 0, stream>>>(
+            a.x + first * a.x_stride, a.x_stride, count, a.width, s.x + first * ld, ld, labels, a.id_bytes, a.vocab);
+    });
     o->x = Mat{s.x, ld, a.tokens, ld};
 }
 void pack_w(const XentArgs& a, const Space& s, int64_t v0, int64_t rows, Operands* o, hipStream_t stream) {
@@ -713,7 +716,10 @@ void pack_w(const XentArgs& a, const Space& s, int64_t v0, int64_t rows, Operand
     o->w = Mat{w, a.w_stride, rows, a.width};
     if (loads16(a.w, a.w_stride, a.width)) return;
     const int64_t ld = ceil_to(a.width, 8);
-    pack_kernel<<<(unsigned)tiles_of(rows * (ld / 8), 256), 256, 0, stream>>>(w, a.w_stride, rows, a.width, s.w, ld, nullptr, 0, 0);
+    launch_rows(rows, ld / 8, [&](int64_t first, int64_t count) {
+        pack_kernel<<<(unsigned)tiles_of(count * (ld / 8), 256), 256, 0, stream>>>(
+            w + first * a.w_stride, a.w_stride, count, a.width, s.w + first * ld, ld, nullptr, 0, 0);
+    });
     o->w = Mat{s.w, ld, rows, ld};
 }
 

@@ -12,6 +12,8 @@ namespace zsmr {
 
 constexpr int BM = 256, BK = 64;        // rows and k of a product's tile in a step
 constexpr int64_t kCus = 256;
+// Tiles of one launch: 512 work items each, and a launch has fewer than 2^32.
+constexpr int64_t kMaxTiles = int64_t(1) << 22;
 
 // The products: logits reduced to statistics, logits turned into G, and the two
 // gradients.
@@ -134,11 +136,12 @@ inline ProductShape logits_shape(int epi, int64_t tokens, int64_t width, int64_t
     return p;
 }
 
-// The products of a forward call, in order.  packed: the weights are packed piece
-// by piece.
+// The products of a forward call, in order: one, but for weights that are packed
+// piece by piece, and for more tiles than a launch holds.
 template <typename F>
 void forward_products(int64_t tokens, int64_t vocab, int64_t width, bool packed, F each) {
-    const int64_t piece = packed ? packed_piece(tokens, vocab, width) : vocab;
+    const int64_t most = std::max<int64_t>(1, kMaxTiles / tiles_of(tokens, kWidth[0])) * BM;
+    const int64_t piece = std::min(most, packed ? packed_piece(tokens, vocab, width) : vocab);
     const int tile = token_tile(tokens, tiles_of(std::min(piece, vocab), BM));
     for (int64_t v0 = 0; v0 < vocab; v0 += piece) each(logits_shape(E_STATS, tokens, width, v0, std::min(piece, vocab - v0), tile));
 }
