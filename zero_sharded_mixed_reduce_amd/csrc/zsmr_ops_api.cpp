@@ -45,14 +45,18 @@ int32_t check_clip(double max_norm, double eps, const float* norm_coef) {
     return al(norm_coef, 4) ? ZSMR_OK : ZSMR_ERR_ALIGN;
 }
 
-// A list's tensors; *total gets their elements, *chunks the most chunks they can
-// have.
+// Elements of a list tensor, or of a gradient row's pad: what one launch can take in
+// chunks (550 GB of 16 bits).
+constexpr int64_t kMaxItem = kMaxGroups * kChunk;
+
+// A list's tensors; *total gets their elements, *chunks the chunks they have if the
+// list is a long one.
 int32_t check_list(const void* const* ptrs, const int64_t* numels, const int32_t* dtypes,
                    int32_t n, int64_t* total, int64_t* chunks) {
     *total = *chunks = 0;
     if (n < 0 || (n > 0 && (!ptrs || !numels || !dtypes))) return ZSMR_ERR_ARG;
     for (int32_t i = 0; i < n; ++i) {
-        if (numels[i] < 0 || numels[i] > ZSMR_MAX_NUMEL || (!ptrs[i] && numels[i] > 0)) return ZSMR_ERR_ARG;
+        if (numels[i] < 0 || numels[i] > kMaxItem || (!ptrs[i] && numels[i] > 0)) return ZSMR_ERR_ARG;
         if (dtypes[i] != ZSMR_FP32 && !dtype_ok(dtypes[i])) return ZSMR_ERR_DTYPE;
         if (!al(ptrs[i], dtypes[i] == ZSMR_FP32 ? 4 : 2)) return ZSMR_ERR_ALIGN;
         *total += numels[i];
@@ -62,16 +66,18 @@ int32_t check_list(const void* const* ptrs, const int64_t* numels, const int32_t
     return ZSMR_OK;
 }
 
-// Puts work items into the launches of at most BATCH items and 2^30 chunks that
-// carry them in their arguments; flush(args) launches one.
+// Puts work items into the launches of at most BATCH items and kMaxGroups chunks that
+// carry them in their arguments; flush(args) launches one.  length: of the whole
+// list, or of the row it is flattened into.
 template <int BATCH, typename A, typename Item, typename F>
 struct Batches {
     A a{};
     F flush;
     hipError_t err = hipSuccess;
-    Batches(F f, int64_t total) : flush(f) { a.chunk = chunk_of_list(total); }
+    Batches(F f, int64_t length) : flush(f) { a.chunk = chunk_of_list(length); }
     void add(Item it, int64_t n) {
         if (n == 0 || err != hipSuccess) return;
+        if (a.chunks + ceil_div(n, a.chunk) > kMaxGroups) go();
         it.chunk0 = a.chunks;
         it.n = n;
         a.it[a.count++] = it;
@@ -93,7 +99,7 @@ int32_t clip(const void* const* ptrs, void* const* in_place, const int64_t* nume
         before += a.chunks;
         return launch_clip(a, stream);
     };
-    Batches<kClipBatch, ClipArgs, ClipItem, decltype(launch)> b(launch, total);
+    Batches<kClipBatch, ClipArgs, ClipItem, decltype(launch)> b(launch, in_place ? total : flat_numel);
     b.a.coef = coef;
     b.a.in_place = in_place != nullptr;
     // from the list's end to its start, which the kernel's reads count on
@@ -316,9 +322,7 @@ int32_t zsmr_clip_flatten(const void* const* ptrs, const int64_t* numels, const 
     const int32_t st = check_list(ptrs, numels, dtypes, n, &total, &chunks);
     if (st) return st;
     if (!dtype_ok(flat_dtype)) return ZSMR_ERR_DTYPE;
-    if (flat_numel < total || flat_numel > ZSMR_MAX_NUMEL || (flat_numel > 0 && !flat) ||
-        ceil_div(flat_numel, kShortChunk) > INT32_MAX)
-        return ZSMR_ERR_ARG;
+    if (flat_numel < total || flat_numel - total > kMaxItem || (flat_numel > 0 && !flat)) return ZSMR_ERR_ARG;
     if (!al(flat, 2) || !al(coef, 4)) return ZSMR_ERR_ALIGN;
     return clip(ptrs, nullptr, numels, dtypes, n, coef, static_cast<uint16_t*>(flat), flat_numel,
                 flat_dtype, total, stream);
