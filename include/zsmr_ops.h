@@ -143,7 +143,8 @@ int32_t zsmr_clip_flatten(const void* const* ptrs, const int64_t* numels, const 
 /* ---- the clipped shard step ----------------------------------------------
  * The global norm depends on every rank's reduced gradient, so the step is two
  * passes with the join between them: zero_reduce_shard_sumsq on every piece,
- * zsmr_clip_coef on the sums, zero_clipped_step on every piece. */
+ * zsmr_clip_coef on the sums, zero_clipped_step on every piece.  A piece has
+ * fewer than 2^35 elements, otherwise ZSMR_ERR_ARG. */
 
 /* zero_reduce_shard (the same bits in g_out, the same counting), and in the
  * same pass sumsq[0] = the sum of the squares of g_out (fp64, device). */

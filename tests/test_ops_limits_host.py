@@ -53,8 +53,24 @@ static void lists() {
     g_clip.clear();
 }
 
+static void pieces() {
+    const zsmr_adam hp = {1e-3, 0.9, 0.999, 1e-8};
+    for (int over = 0; over < 2; ++over) {
+        const int64_t n = zsmr::kMaxGroups * zsmr::kTile + over;
+        zsmr_ctx* c = nullptr;
+        CHECK(zero_init_shards(&c, n, 1, ZSMR_ZERO2, ZSMR_BF16, ZSMR_BF16, 0, nullptr, 0) == ZSMR_OK);
+        g_step.clear();
+        const int32_t want = over ? ZSMR_ERR_ARG : ZSMR_OK;
+        CHECK(zero_reduce_shard_sumsq(c, 0, 0, P, n, 0, 1, (float*)P, (double*)P, P, zsmr_norm_workspace(n, 1), nullptr) == want);
+        CHECK(zero_clipped_step(c, 0, 0, (float*)P, nullptr, (float*)P, (float*)P, (float*)P, P, 1, &hp, nullptr) == want);
+        CHECK(g_step.size() == (over ? 0u : 2u));
+        zero_destroy(c);
+    }
+}
+
 int main() {
     lists();
+    pieces();
     std::printf("host checks passed\n");
     return 0;
 }

@@ -339,8 +339,8 @@ int32_t zero_reduce_shard_sumsq(zsmr_ctx* c, int32_t rank, int32_t unit, const v
     if (!g_out || !sumsq || (mean != 0 && mean != 1)) return ZSMR_ERR_ARG;
     if (!al(g_out, 4) || !al(sumsq, 8)) return ZSMR_ERR_ALIGN;
     const int64_t tiles = ceil_div(len, kTile);
+    if (tiles > kMaxGroups) return ZSMR_ERR_ARG;        // one launch; 137 GB of g_out
     if ((st = check_space(ws, ws_bytes, tiles * 8))) return st;
-    if (tiles > INT32_MAX) return ZSMR_ERR_ARG;
     StepArgs a{};
     a.grads = static_cast<const uint16_t*>(grads) + base;
     a.row_stride = row_stride;
@@ -371,7 +371,7 @@ int32_t zero_clipped_step(zsmr_ctx* c, int32_t rank, int32_t unit, const float* 
     int64_t len = 0;
     piece(c, rank, unit, nullptr, &len, nullptr);
     if (len == 0) return ZSMR_OK;
-    if (ceil_div(len, kTile) > INT32_MAX) return ZSMR_ERR_ARG;
+    if (ceil_div(len, kTile) > kMaxGroups) return ZSMR_ERR_ARG;
     a.g_in = g;
     a.master = master;
     a.m = m;
