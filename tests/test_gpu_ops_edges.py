@@ -179,3 +179,25 @@ def test_scores_of_more_tiles_than_a_launch_holds():
     assert abs(summary[0].item() - float(loss.double().mean())) <= 2 * U * summary[0].item()
     del ws, raw
     torch.cuda.empty_cache()
+
+
+def test_raw_addresses():
+    """Every buffer but a matrix may be a raw address, which the caller has
+    checked: the same bits as with tensors."""
+    g, t = gen(24), torch.bfloat16
+    n, vocab, width = 33, 200, 64
+    x, w, labels = normal(g, (n, width), 1.0, t), normal(g, (vocab, width), 0.2, t), tokens(g, n, vocab, "some")
+    weights = torch.rand(n, generator=g, device="cuda")
+    a, b = ([torch.empty(n, device="cuda"), torch.empty(n, device="cuda"), torch.empty(3, device="cuda"), torch.empty_like(x), torch.empty_like(w)]
+            for _ in range(2))
+    size = max(z.zsmr_xent_workspace(n, vocab, width), z.zsmr_embed_grad_workspace(vocab, width, n), z.zsmr_norm_workspace(vocab * width, 1))
+    ws, _ = space(size)
+    for (loss, lse, summary, dx, dw), f in ((a, lambda y: y), (b, lambda y: y.data_ptr())):
+        z.zsmr_xent_forward(x, w, labels, f(loss), f(lse), f(summary), f(ws))
+        z.zsmr_xent_backward(x, w, labels, f(lse), dx, dw, f(ws), grad=f(weights), scale=f(summary) + 4 if f(ws) is not ws else summary[1:2])
+        z.zsmr_embed_grad(dx, labels, dw, f(ws), accumulate=True)
+        out = torch.empty(2, device="cuda")
+        z.zsmr_grad_norm([dw], 1e-3, f(out), f(ws))
+        z.zsmr_clip_grads([dw], f(out) + 4 if f(ws) is not ws else out[1:])
+    for p, q in zip(a, b):
+        assert torch.equal(bits(p), bits(q))

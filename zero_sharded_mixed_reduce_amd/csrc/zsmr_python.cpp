@@ -166,7 +166,10 @@ struct Vector {
     const char* what;
     int64_t bytes = 0;
     Vector(PyObject* t, int64_t n, PyObject* dtype, const char* name) : x(t), what(name) {
-        if (none_or_raw(t)) return;
+        if (none_or_raw(t)) {
+            bytes = t == Py_None ? 0 : INT64_MAX;       // of a workspace
+            return;
+        }
         Shape shape(t);
         int64_t have = shape.numel();
         if (!dtype) {
@@ -293,6 +296,10 @@ int32_t clip_grads(Args a) {            // addresses, numels, dtypes, coef, stre
 int32_t clip_flatten(Args a) {          // addresses, numels, dtypes, coef, flat, stream
     List list(a);
     Vector coef(a[3], 1, t_fp32, "coef");
+    if (none_or_raw(a[4])) {
+        PyErr_SetString(PyExc_ValueError, "flat: a tensor is required, which says the row's format and length");
+        fail();
+    }
     Ref format(PyObject_GetAttr(a[4], n_dtype));
     const int dtype = code_of(format.p);
     if (dtype != ZSMR_FP16 && dtype != ZSMR_BF16) {

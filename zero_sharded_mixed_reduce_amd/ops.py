@@ -4,7 +4,9 @@ Every function has the name of a C entry point; the checks and the calls are in
 the extension module ``_ops`` (``csrc/zsmr_python.cpp``).  Matrices are torch tensors
 whose last dimension is contiguous (any stride between rows); their sizes,
 strides and formats come from the tensors, which are checked against each
-other before the library is called.  All arithmetic runs in its HIP kernels.
+other before the library is called.  Vectors of floats and workspaces may also be raw device
+addresses, whose lengths are the caller's to check.  All arithmetic runs in the
+library's HIP kernels.
 
 A list of gradient tensors is either any iterable of contiguous torch tensors, or
 ``(addresses, numels, dtypes)``: three numpy arrays (int64, int64, int32 format
