@@ -7,6 +7,7 @@ under AddressSanitizer and UndefinedBehaviorSanitizer.
   tiles of each product cover its sides, its splits all of k.
 * No launch has 2^32 work items.
 * Every part of the workspace holds what the products put there.
+* The shapes of the GPU tests select every form of the product kernel there is.
 """
 import os
 import shutil
@@ -124,3 +125,46 @@ def test_plan_over_the_accepted_sizes(tmp_path, sanitize):
     env = dict(os.environ, ASAN_OPTIONS="halt_on_error=1:verify_asan_link_order=0", UBSAN_OPTIONS="print_stacktrace=1:halt_on_error=1")
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300, env=env)
     assert r.returncode == 0 and "plan checks passed" in r.stdout, (r.stdout + r.stderr)[-4000:]
+
+
+VARIANTS = r"""
+#include <cstdio>
+#include <cstdlib>
+#include "zsmr_xent_plan.h"
+using namespace zsmr;
+int main(int argc, char** argv) {
+    for (int i = 1; i + 2 < argc; i += 3) {
+        const int64_t n = std::atoll(argv[i]), v = std::atoll(argv[i + 1]), h = std::atoll(argv[i + 2]);
+        auto print = [&](const ProductShape& p) {
+            std::printf("%d %d %d %d %s\n", p.epi, p.tile, p.stages, p.once, p.epi != E_DX ? "-" : p.sum_in ? p.sum_out ? "middle" : "last" : p.sum_out ? "first" : "only");
+        };
+        forward_products(n, v, h, h % 8 != 0, print);
+        backward_products(n, v, h, h % 8 != 0, true, true, print);
+    }
+    return 0;
+}
+"""
+# as zsmr_xent.hip has them: tile, stages, once
+TOKEN_TILES = [(64, 2, 1), (64, 4, 0), (128, 3, 1), (128, 3, 0), (192, 2, 0), (256, 2, 0)]
+
+
+def variants_of(exe, shapes):
+    out = subprocess.run([str(exe)] + [str(k) for shape in shapes for k in shape], capture_output=True, text=True, check=True, timeout=60).stdout
+    return {tuple(line.split()) for line in out.splitlines()}
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_the_gpu_tests_shapes_select_every_form(tmp_path):
+    from tests.test_gpu_ops_variants import XENT_SHAPES
+    exe = compile_driver(tmp_path, VARIANTS)
+    seen = variants_of(exe, XENT_SHAPES)
+    forms = {v[:4] for v in seen}
+    for epi in "012":
+        assert forms >= {(epi, str(t), str(s), str(o)) for t, s, o in TOKEN_TILES}, epi
+    assert {v for v in forms if v[0] == "3"} == {("3", "128", "3", "0"), ("3", "256", "2", "0")}
+    assert len(forms) == 3 * len(TOKEN_TILES) + 2, "a form that zsmr_xent.hip does not have"
+    # dx adds what earlier pieces left, and leaves sums for later ones, in each wide tile
+    for tile in ("128", "192", "256"):
+        assert {v[4] for v in seen if v[:2] == ("2", tile)} == {"only", "first", "middle", "last"}, tile
+    # and so does the largest workload of this repository: four pieces, one split
+    assert ("2", "256", "2", "0", "last") in variants_of(exe, [(8192, 128256, 4096)])
