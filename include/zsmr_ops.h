@@ -80,7 +80,11 @@ int32_t zsmr_embed_grad(const void* dout, int64_t dout_stride, int32_t dtype, co
  * as 16-bit probabilities) at a time. */
 
 /* Bytes of workspace of a forward call (backward == 0), or of both calls
- * (backward == 1); -1 for sizes they refuse. */
+ * (backward == 1); -1 for sizes they refuse.  It serves operands of any stride
+ * and alignment: a copy of x and of up to 32,768 rows of w (268 MB at width
+ * 4,096) is part of it, of which w's is left alone where 16-byte loads can read
+ * w.  The backward pass's probabilities are the most of it otherwise: 512 MB at
+ * most, and 512 bytes a token from 2^20 tokens on. */
 int64_t zsmr_xent_workspace(int64_t n_tokens, int64_t vocab, int64_t width, int32_t backward);
 
 /* loss and lse: n_tokens fp32 each (lse of every token, labelled or not).
@@ -97,7 +101,12 @@ int32_t zsmr_xent_forward(const void* x, int64_t x_stride, const void* w, int64_
  * lse as the forward call left it.  grad: n_tokens fp32, or NULL for ones;
  * scale: one fp32 on the device, or NULL for 1 (the mean's is summary + 1).
  * dx or dw may be NULL: that gradient is left out.  accumulate == 1 adds to
- * dw.  G is rounded to 16 bits for the matrix instructions that use it. */
+ * dw.  G is rounded to 16 bits for the matrix instructions that use it.  In
+ * fp16 it is held times a power of two that brings the largest |grad| of the
+ * tokens that count to 2^14..2^15, one for all tokens: what lies below 2^-28 of
+ * that weight is rounded to steps of 2^-39 of it.  So in fp16 the dx row of a
+ * token whose weight is 1e-5 or less of the largest has fewer bits than its
+ * neighbours'; bf16 has fp32's range and no such limit. */
 int32_t zsmr_xent_backward(const void* x, int64_t x_stride, const void* w, int64_t w_stride,
                            int32_t dtype, const void* labels, int32_t id_bytes, int64_t n_tokens,
                            int64_t vocab, int64_t width, const float* lse, const float* grad,
