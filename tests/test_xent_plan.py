@@ -47,7 +47,7 @@ static void check(int64_t n, int64_t v, int64_t h) {
     if (v / piece > 600) return;
     for (int pack = 0; pack < 2; ++pack) {
         const int64_t rows = pack ? packed : piece;
-        if (n) {
+        {
             int64_t at = 0;
             forward_products(n, v, h, pack, [&](const ProductShape& p) {
                 CHECK(p.grid() * 512 < (int64_t(1) << 32));

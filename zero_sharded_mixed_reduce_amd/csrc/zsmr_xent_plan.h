@@ -142,7 +142,7 @@ inline ProductShape logits_shape(int epi, int64_t tokens, int64_t width, int64_t
 // piece by piece, and for more tiles than a launch holds.
 template <typename F>
 void forward_products(int64_t tokens, int64_t vocab, int64_t width, bool packed, F each) {
-    const int64_t most = std::max<int64_t>(1, kMaxTiles / tiles_of(tokens, kWidth[0])) * BM;
+    const int64_t most = std::max<int64_t>(1, kMaxTiles / tiles_of(std::max<int64_t>(tokens, 1), kWidth[0])) * BM;
     const int64_t piece = std::min(most, packed ? packed_piece(tokens, vocab, width) : vocab);
     const int tile = token_tile(tokens, tiles_of(std::min(piece, vocab), BM));
     for (int64_t v0 = 0; v0 < vocab; v0 += piece) each(logits_shape(E_STATS, tokens, width, v0, std::min(piece, vocab - v0), tile));
