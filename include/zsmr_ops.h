@@ -12,7 +12,12 @@
  *   - the clipped shard step: reduce with the shard's sum of squares, the join
  *     of all ranks' sums, and Adam on the clipped gradient with the cast
  *     ("The four schemes", Base._adam and ZeRO1.step).  The pages do not clip;
- *     the arithmetic of reduce, Adam and cast is that of zsmr.h.
+ *     the arithmetic of reduce, Adam and cast is that of zsmr.h;
+ *   - the orthogonalised update of matrices by Newton-Schulz products, and the
+ *     shard step that applies it to matrices a rank owns whole (reduce, momentum,
+ *     orthogonalise, update, cast);
+ *   - scores of logits that a program has: log probabilities of given tokens with
+ *     entropy and top alternatives, and their gradient.
  *
  * The conventions of zsmr.h hold: status codes, caller-owned device memory,
  * asynchronous launches on the caller's stream, every argument checked before
@@ -36,7 +41,7 @@
 extern "C" {
 #endif
 
-/* a third format, for the tensors of a gradient list only */
+/* a third format: tensors of a gradient list, matrices, logits */
 #define ZSMR_FP32 3
 
 /* Limits of the 2-D operators: rows of at most 2^21 elements (also the
@@ -168,6 +173,105 @@ int32_t zero_reduce_shard_sumsq(zsmr_ctx* ctx, int32_t rank, int32_t unit, const
 int32_t zero_clipped_step(zsmr_ctx* ctx, int32_t rank, int32_t unit, const float* g,
                           const float* coef, float* master, float* m, float* v, void* p16_dst,
                           int32_t t, const zsmr_adam* hp, hipStream_t stream);
+
+/* ---- the orthogonalised update --------------------------------------------
+ * From X0 = x / (|x|_F + eps), for each of `steps` triples (a, b, c):
+ *   X' = a X + (b A + c A^2) X,  A = X X^T  (for a matrix taller than wide: of
+ *   its transpose),
+ * an odd polynomial that moves every singular value the way the triple says:
+ * with a = 3.4445, b = -4.7750, c = 2.0315 five times, to about 1.  Every
+ * product has fp32's accuracy (operands of 22 bits, fp32 sums), whatever the
+ * formats of x and out.  A matrix of zeros gives zeros; one with a NaN or an
+ * infinity gives NaN. */
+#define ZSMR_MAX_NS_STEPS 16
+typedef struct zsmr_newton {
+    double eps;                             /* finite, >= 0 */
+    int32_t steps;                          /* 1 .. ZSMR_MAX_NS_STEPS */
+    int32_t pad;
+    double coef[ZSMR_MAX_NS_STEPS][3];      /* finite; no step may move a singular value beyond 181,
+                                             * nor make b s^2 + c s^4 larger than 32,768 */
+} zsmr_newton;
+
+/* Sides of a matrix at most 2^18, elements at most 2^33, matrices of a call at
+ * most 2^20. */
+#define ZSMR_MAX_SIDE     ((int64_t)1 << 18)
+#define ZSMR_MAX_MATRIX   ((int64_t)1 << 33)
+#define ZSMR_MAX_MATRICES ((int64_t)1 << 20)
+
+/* Bytes of workspace of the two calls below, or -1 for sizes they refuse: 8
+ * bytes an element and 8 an element of the inner matrices, for the matrices that
+ * are worked on at a time (2^25 elements at most, or one matrix). */
+int64_t zsmr_orthogonalize_workspace(int64_t rows, int64_t cols, int64_t count);
+
+/* out[k] = the last X of x[k], rounded to out_dtype once, for `count` matrices of
+ * rows x cols: row_stride elements from row to row (at least cols), batch elements from
+ * matrix to matrix (any, as long as the matrices of out do not overlap).  Formats:
+ * ZSMR_FP16, ZSMR_BF16 or ZSMR_FP32. */
+int32_t zsmr_orthogonalize(const void* x, int32_t x_dtype, int64_t x_stride, int64_t x_batch,
+                           void* out, int32_t out_dtype, int64_t out_stride, int64_t out_batch,
+                           int64_t rows, int64_t cols, int64_t count, const zsmr_newton* ns,
+                           void* ws, int64_t ws_bytes, hipStream_t stream);
+
+/* lr, weight_decay, scale: finite, >= 0; 0 <= beta < 1; nesterov 0 or 1. */
+typedef struct zsmr_muon {
+    double lr, beta, weight_decay, scale;
+    int32_t nesterov, pad;
+} zsmr_muon;
+
+/* The shard step of matrices that a rank holds whole: `count` matrices of rows x
+ * cols, row by row and one behind the other, from element `begin` of the (rank,
+ * unit) piece on.  With g = mean over the ranks (zero_reduce_shard):
+ *   momentum = beta * momentum + g,  u = nesterov ? g + beta * momentum : momentum,
+ *   master = (1 - lr * weight_decay) * master - (lr * scale) * orthogonalised(u),
+ *   p16 = RNE16(master),
+ * every operation outside the products rounded to fp32.  Pointers and base_elem
+ * refer to the whole piece, and the call counts as zero_fused_step_range on these
+ * elements does.  ZSMR_ERR_ARG if the matrices reach past the piece, and at stage
+ * ZSMR_DP unless they are the whole vector.  A rank that holds nothing of the unit
+ * has no matrices: ZSMR_ERR_ARG unless count is 0, which does nothing. */
+int32_t zero_muon_step(zsmr_ctx* ctx, int32_t rank, int32_t unit, int64_t begin, int64_t rows,
+                       int64_t cols, int64_t count, const void* grads, int64_t row_stride,
+                       int64_t base_elem, float* master, float* momentum, void* p16_dst,
+                       const zsmr_muon* hp, const zsmr_newton* ns, void* ws, int64_t ws_bytes,
+                       hipStream_t stream);
+
+/* ---- scores of logits ------------------------------------------------------
+ * logits: n_tokens rows of vocab (at most 2^21) elements, ZSMR_FP16, ZSMR_BF16 or
+ * ZSMR_FP32, stride elements apart.  With z = scale * logit, in fp32,
+ *   lse = log sum_v exp z_v,  logprob = z_id - lse,  p_v = exp(z_v - lse),
+ *   entropy = -sum_v p_v log p_v.
+ * Logits of -infinity are masked: p = 0.  So are values of z below -3.0e38, which
+ * the lowest values of bf16 and fp32 are.  A row with nothing else has lse
+ * -infinity, entropy 0, logprob -infinity and a gradient of zeros.  A NaN makes a
+ * row's lse, logprob, entropy and gradient NaN.  An id outside [0, vocab) is
+ * padding: logprob 0, which has no gradient; entropy and alternatives are the
+ * row's.  scale: finite, > 0. */
+#define ZSMR_MAX_TOP 64
+
+/* Bytes of workspace, or -1 for sizes the call refuses. */
+int64_t zsmr_logprobs_workspace(int64_t n_tokens, int64_t vocab, int32_t top);
+
+/* logprob, lse, entropy: n_tokens fp32 each; any may be NULL, logprob has to be
+ * where ids is.  top (0 .. ZSMR_MAX_TOP, at most vocab): the alternatives of
+ * largest logit, the lowest index first among equal ones: n_tokens x top indices of
+ * top_bytes each (4 or 8) and their log probabilities in fp32; either may be NULL.
+ * Rows with fewer logits above -infinity end in -1 and -infinity; NaN is no
+ * alternative. */
+int32_t zsmr_logprobs(const void* logits, int64_t stride, int32_t dtype, const void* ids,
+                      int32_t id_bytes, int64_t n_tokens, int64_t vocab, float scale,
+                      float* logprob, float* lse, float* entropy, int32_t top, void* top_ids,
+                      int32_t top_bytes, float* top_logprobs, void* ws, int64_t ws_bytes,
+                      hipStream_t stream);
+
+/* dlogits = RNE(scale * (g * ([v = id] - p_v) - h * p_v * (log p_v + entropy))), the
+ * gradient of sum (g * logprob + h * entropy), in the format of the logits, whose
+ * memory it may share (the same address and stride).  g and h: n_tokens fp32 each, or
+ * NULL for zeros; entropy may be NULL where h is, ids where g is.  lse and entropy
+ * are what zsmr_logprobs left. */
+int32_t zsmr_logprobs_grad(const void* logits, int64_t stride, int32_t dtype, const void* ids,
+                           int32_t id_bytes, int64_t n_tokens, int64_t vocab, float scale,
+                           const float* lse, const float* entropy, const float* g, const float* h,
+                           void* dlogits, int64_t dlogits_stride, hipStream_t stream);
 
 #ifdef __cplusplus
 }

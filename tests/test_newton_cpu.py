@@ -1,0 +1,258 @@
+"""The orthogonalised update, its shard step and the scores of logits on a machine
+without a GPU: refusals before anything is launched, sizes of workspaces, what the
+binding checks, and the host arithmetic of the plans.  Addresses are placeholders
+that nothing reads."""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import pytest
+import torch
+
+import zero_sharded_mixed_reduce_amd as z
+from tests.test_xent_plan import compile_driver
+from zero_sharded_mixed_reduce_amd import ops
+
+A, B, C, D, W = 1 << 20, 2 << 20, 3 << 20, 4 << 20, 5 << 20     # 16-byte aligned
+BIG = 1 << 50
+L = ops._lib()
+ARG, DTYPE, ALIGN = z.ZSMR_ERR_ARG, z.ZSMR_ERR_DTYPE, z.ZSMR_ERR_ALIGN
+BF16, F32 = z.ZSMR_BF16, 3
+
+
+def newton(coefs=ops.NS_COEFS, eps=1e-7, steps=None):
+    ns = ops.zsmr_newton(eps, len(coefs) if steps is None else steps, 0)
+    for i, triple in enumerate(coefs):
+        ns.coef[i][:] = triple
+    return ns
+
+
+NS = newton()
+ORTHOGONALIZE = dict(x=A, xd=BF16, xs=64, xb=640, out=B, od=F32, os=64, ob=640, rows=10, cols=64, count=3, ns=NS, ws=W, wb=BIG, stream=None)
+NAN, INF = float("nan"), float("inf")
+BAD_NS = [newton(eps=-1.0), newton(eps=NAN), newton(eps=INF), newton(steps=0), newton(steps=17), newton(((NAN, 0, 0),)), newton(((0, INF, 0),)),
+          newton(((182.0, 0, 0),)), newton(((100.0, 0, 0), (2.0, 0, 0))), newton(((1.0, 0, 0), (1e308, 1e308, 1e308))), newton(((1.0, 1e6, -1e6),))]
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(x=None), ARG), (dict(out=None), ARG), (dict(rows=0), ARG), (dict(cols=0), ARG), (dict(rows=(1 << 18) + 1), ARG), (dict(rows=-1), ARG),
+    (dict(rows=1 << 17, cols=(1 << 16) + 1), ARG), (dict(count=-1), ARG), (dict(count=(1 << 20) + 1), ARG), (dict(xs=63), ARG), (dict(os=63), ARG),
+    (dict(xs=(1 << 21) + 1), ARG), (dict(xb=-1), ARG), (dict(ob=639), ARG), (dict(ob=64, os=191), ARG), (dict(ob=63, os=192), ARG),
+    (dict(xb=(1 << 40) + 1), ARG), (dict(ns=None), ARG), (dict(ws=None), ARG), (dict(wb=1000), ARG), (dict(xd=4), DTYPE), (dict(od=0), DTYPE),
+    (dict(x=A + 1), ALIGN), (dict(out=B + 2), ALIGN), (dict(x=A + 2, xd=F32), ALIGN), (dict(ws=W + 8), ALIGN)] + [(dict(ns=ns), ARG) for ns in BAD_NS])
+def test_orthogonalize_refusals(change, code):
+    assert L.zsmr_orthogonalize(*(ORTHOGONALIZE | change).values()) == code
+
+
+def test_nothing_to_orthogonalize():
+    assert L.zsmr_orthogonalize(*(ORTHOGONALIZE | dict(count=0, x=None, out=None, ws=None, wb=0)).values()) == 0
+    assert z.zsmr_orthogonalize_workspace(10, 10, 0) == 0
+
+
+def test_workspaces():
+    # X twice and the two inner matrices, 4 bytes an element
+    assert z.zsmr_orthogonalize_workspace(4096, 4096) >= 4 * 4 * 4096 ** 2
+    assert z.zsmr_orthogonalize_workspace(4096, 4096) < 4.1 * 4 * 4096 ** 2
+    assert z.zsmr_orthogonalize_workspace(100, 50, 7) == z.zsmr_orthogonalize_workspace(50, 100, 7) == z.zero_muon_workspace(50, 100, 7)
+    # a group's matrices at a time
+    assert z.zsmr_orthogonalize_workspace(1024, 1024, 1 << 20) < 6.5e8
+    assert z.zsmr_orthogonalize_workspace(1, 1, 1 << 20) < 6.5e8
+    for bad in ((0, 1, 1), (1, 0, 1), (1, 1, -1), ((1 << 18) + 1, 1, 1), (1 << 17, 1 << 17, 1), (1, 1, (1 << 20) + 1)):
+        with pytest.raises(z.ZsmrError):
+            z.zsmr_orthogonalize_workspace(*bad)
+    assert z.zsmr_logprobs_workspace(0, 10) == z.zsmr_logprobs_workspace(8192, 128256, 20) == 0
+    assert z.zsmr_logprobs_workspace(1, 128256, 20) >= 16 + 8 * 20
+    for bad in ((-1, 10, 0), (1, 0, 0), (1, 10, 11), (1, 100, 65), (1, 100, -1), ((1 << 24) + 1, 10, 0), (1, (1 << 21) + 1, 0)):
+        with pytest.raises(z.ZsmrError):
+            z.zsmr_logprobs_workspace(*bad)
+
+
+def test_muon_refusals_count_nothing():
+    hp = lambda **kw: ops.zsmr_muon(**(dict(lr=0.02, beta=0.9, weight_decay=0.1, scale=1.0, nesterov=1, pad=0) | kw))  # noqa: E731
+    ctx = z.zero_init_shards(3000, 3, z.ZSMR_ZERO3_OWNER, "bf16", units=[1000, 2000])
+    z.zero_set_unit_owners(ctx, [2, 0])
+    ok = dict(ctx=ctx.handle, rank=0, unit=1, begin=100, rows=10, cols=60, count=3, grads=A, stride=2000, base=0, master=B, momentum=C, p16=D,
+              hp=hp(), ns=NS, ws=W, wb=BIG, stream=None)
+    bad = [(dict(ctx=None), ARG), (dict(rank=3), ARG), (dict(rank=1), ARG), (dict(unit=2), ARG), (dict(begin=-1), ARG), (dict(begin=201), ARG),
+           (dict(rows=0), ARG), (dict(count=4), ARG), (dict(count=-1), ARG), (dict(grads=None), ARG), (dict(stride=1999), ARG), (dict(base=-1), ARG),
+           (dict(master=None), ARG), (dict(momentum=None), ARG), (dict(p16=None), ARG), (dict(hp=None), ARG), (dict(ns=None), ARG), (dict(ws=None), ARG),
+           (dict(wb=100), ARG), (dict(rows=1 << 18, cols=1 << 15, count=1 << 20), ARG), (dict(grads=A + 1), ALIGN), (dict(master=B + 2), ALIGN),
+           (dict(momentum=C + 1), ALIGN), (dict(p16=D + 1), ALIGN), (dict(ws=W + 4), ALIGN)]
+    bad += [(dict(hp=hp(**{k: v})), ARG) for k, v in (("lr", -1.0), ("lr", NAN), ("beta", 1.0), ("beta", -0.1), ("weight_decay", INF),
+                                                      ("weight_decay", -1.0), ("scale", -1.0), ("scale", NAN), ("nesterov", 2))]
+    bad += [(dict(ns=ns), ARG) for ns in BAD_NS]
+    for change, code in bad:
+        assert L.zero_muon_step(*(ok | change).values()) == code, change
+    # no matrices, also on a rank that holds nothing
+    assert L.zero_muon_step(*(ok | dict(count=0, grads=None, master=None, momentum=None, p16=None, ws=None)).values()) == 0
+    assert L.zero_muon_step(*(ok | dict(rank=1, begin=0, count=0)).values()) == 0
+    whole = z.zero_init_shards(1000, 2, z.ZSMR_DP, "bf16")
+    dp = ok | dict(ctx=whole.handle, unit=0, begin=0, rows=10, cols=50, count=1)
+    assert L.zero_muon_step(*dp.values()) == ARG            # half of a replica's vector
+    assert all(z.zero_counters(c, r)["traffic_elems"] == 0 for c in (ctx, whole) for r in range(2))
+
+
+LOGPROBS = dict(logits=A, stride=100, dtype=F32, ids=B, id_bytes=8, n=5, vocab=100, scale=1.0, logprob=C, lse=C, entropy=C, top=4, top_ids=D,
+                top_bytes=8, top_logprobs=D, ws=W, wb=BIG, stream=None)
+GRAD = dict(logits=A, stride=100, dtype=F32, ids=B, id_bytes=8, n=5, vocab=100, scale=1.0, lse=C, entropy=C, g=C, h=C, dlogits=D, ds=100, stream=None)
+COMMON = [(dict(logits=None), ARG), (dict(stride=99), ARG), (dict(stride=(1 << 21) + 1), ARG), (dict(dtype=0), DTYPE), (dict(dtype=4), DTYPE),
+          (dict(ids=None), ARG), (dict(id_bytes=2), ARG), (dict(n=-1), ARG), (dict(n=(1 << 24) + 1), ARG), (dict(vocab=0), ARG),
+          (dict(vocab=(1 << 21) + 1), ARG), (dict(scale=0.0), ARG), (dict(scale=-1.0), ARG), (dict(scale=NAN), ARG), (dict(scale=INF), ARG),
+          (dict(logits=A + 2), ALIGN), (dict(ids=B + 4), ALIGN), (dict(lse=C + 2), ALIGN), (dict(entropy=C + 1), ALIGN)]
+
+
+@pytest.mark.parametrize("change,code", COMMON + [
+    (dict(top=-1), ARG), (dict(top=65, vocab=100), ARG), (dict(top=11, vocab=10), ARG), (dict(top_bytes=2), ARG), (dict(logprob=C + 2), ALIGN),
+    (dict(top_ids=D + 4), ALIGN), (dict(top_logprobs=D + 2), ALIGN), (dict(vocab=10 ** 6, stride=10 ** 6, wb=10), ARG),
+    (dict(vocab=10 ** 6, stride=10 ** 6, ws=None), ARG), (dict(ws=W + 8), ALIGN)])
+def test_logprobs_refusals(change, code):
+    assert L.zsmr_logprobs(*(LOGPROBS | change).values()) == code
+
+
+@pytest.mark.parametrize("change,code", COMMON + [
+    (dict(dlogits=None), ARG), (dict(ds=99), ARG), (dict(lse=None), ARG), (dict(entropy=None), ARG), (dict(dlogits=A, ds=101), ARG),
+    (dict(dlogits=D + 1), ALIGN), (dict(g=C + 2), ALIGN), (dict(h=C + 2), ALIGN)])
+def test_logprobs_grad_refusals(change, code):
+    assert L.zsmr_logprobs_grad(*(GRAD | change).values()) == code
+
+
+def test_no_scores_launch_nothing():
+    assert L.zsmr_logprobs(*(LOGPROBS | dict(n=0, logits=None, ids=None)).values()) == 0
+    assert L.zsmr_logprobs(*(LOGPROBS | dict(logprob=None, ids=None, lse=None, entropy=None, top=0)).values()) == 0
+    assert L.zsmr_logprobs(*(LOGPROBS | dict(logprob=None, ids=None, lse=None, entropy=None, top_ids=None, top_logprobs=None)).values()) == 0
+    assert L.zsmr_logprobs_grad(*(GRAD | dict(n=0, logits=None, ids=None, lse=None, entropy=None, dlogits=None)).values()) == 0
+
+
+def test_binding_checks_tensors_before_the_library():
+    x, ws = torch.zeros(2, 6, 8), torch.zeros(64, dtype=torch.uint8)
+    for bad, kw, why in (((x, x[:1], ws), {}, "out"), ((x, x[:, :5], ws), {}, "out"), ((x[0, 0], x, ws), {}, "a matrix or a stack"),
+                         ((x.long(), x, ws), {}, "fp16, bf16 or fp32"), ((x.mT, x.mT, ws), {}, "contiguous"), ((x, x, ws[::2]), {}, "workspace"),
+                         ((x.as_strided((2, 6, 8), (48, 7, 1)), x, ws), {}, "overlap"), ((x, x, ws), {"coefs": ()}, "coefs"),
+                         ((x, x, ws), {"coefs": ((1.0, 2.0),)}, "coefs"), ((x, x, ws), {"coefs": ((1.0, 2.0, 3.0),) * 17}, "coefs"),
+                         ((x, x, ws), {"coefs": 3}, None), ((x, x, ws), {}, "host memory")):
+        with pytest.raises((ValueError, TypeError), match=why):
+            z.zsmr_orthogonalize(*bad, stream=0, **kw)
+    ctx = z.zero_init_shards(200, 2, z.ZSMR_ZERO2, "bf16")
+    rows, f, h = torch.zeros(2, 200, dtype=torch.bfloat16), torch.zeros(100), torch.zeros(100, dtype=torch.bfloat16)
+    ok = dict(ctx=ctx, rank=1, unit=0, begin=4, rows=8, cols=12, count=1, grads=rows, row_stride=200, base_elem=100, master=f, momentum=f, p16_dst=h, ws=ws,
+              lr=0.1, stream=0)
+    for change, why in ((dict(grads=rows[:1]), "grads"), (dict(base_elem=101), "grads"), (dict(master=f[:99]), "master"), (dict(momentum=h), "momentum"),
+                        (dict(p16_dst=h[1:]), "p16_dst"), (dict(count=1 << 64), "int64"), (dict(rank=1 << 40), "int32"), ({}, "host memory")):
+        with pytest.raises(ValueError, match=why):
+            z.zero_muon_step(**(ok | change))
+    with pytest.raises(z.ZsmrError) as e:       # past the piece: the library's own check
+        z.zero_muon_step(**(ok | dict(begin=5, grads=A, master=B, momentum=C, p16_dst=D, ws=W)))
+    assert e.value.code == ARG
+    t, ids, n3 = torch.zeros(3, 50), torch.zeros(3, dtype=torch.int64), torch.zeros(3)
+    top, val = torch.zeros(3, 4, dtype=torch.int64), torch.zeros(3, 4)
+    ok = dict(logits=t, ids=ids, logprob=n3, lse=n3, entropy=n3, ws=ws, stream=0)
+    for change, why in ((dict(logits=t[0]), "logits"), (dict(logits=t.t()), "token ids|contiguous"), (dict(logits=t.double()), "logits"),
+                        (dict(ids=ids[:2]), "token ids"), (dict(ids=ids.float()), "token ids"), (dict(lse=n3[:2]), "lse"),
+                        (dict(entropy=n3.double()), "entropy"), (dict(top_ids=top.float()), "top_ids"), (dict(top_ids=top[:2]), "top_ids"),
+                        (dict(top_ids=top, top_logprobs=val[:, :3].contiguous()), "top_logprobs"), (dict(top_logprobs=val.t()), "top_logprobs"),
+                        (dict(top_ids=torch.zeros(3, 65, dtype=torch.int64)), "top_ids"), ({}, "host memory")):
+        with pytest.raises(ValueError, match=why):
+            z.zsmr_logprobs(**(ok | change))
+    ok = dict(logits=t, ids=ids, lse=n3, entropy=n3, dlogits=t, stream=0)
+    for change, why in ((dict(dlogits=t[:2]), "dlogits"), (dict(dlogits=t.half()), "format"), (dict(dlogprob=n3[:1]), "dlogprob"),
+                        (dict(dentropy=ids), "dentropy"), ({}, "host memory")):
+        with pytest.raises(ValueError, match=why):
+            z.zsmr_logprobs_grad(**(ok | change))
+
+
+PLAN = r"""
+#include <cstdio>
+#include <cstdlib>
+#include <initializer_list>
+#include "zsmr_newton_plan.h"
+#include "zsmr_scores_plan.h"
+#define CHECK(c) do { if (!(c)) { std::printf("CHECK failed line %d: %s\n", __LINE__, #c); std::exit(1); } } while (0)
+using namespace zsmr;
+
+static void shape(int64_t rows, int64_t cols, int64_t count) {
+    const NsShape s = ns_shape(rows, cols, count);
+    CHECK(s.m <= s.n && s.m * s.n == rows * cols && s.tall == (rows > cols));
+    CHECK(s.mp >= s.m && s.mp % 32 == 0 && s.np >= s.n && s.np % 32 == 0);
+    CHECK(s.group >= 1 && s.group <= count && s.parts >= 1);
+    CHECK(s.group == 1 || s.group * s.m * s.n <= kNsGroupElems);
+    const NsSpace w = ns_space(s);
+    CHECK(w.x[1] - w.x[0] >= s.group * s.m * s.np * 4 && w.a - w.x[1] >= s.group * s.m * s.np * 4);
+    CHECK(w.x[1] - w.x[0] >= s.group * s.m * s.n * 4);      // the fp32 update
+    CHECK(w.b - w.a >= s.group * s.m * s.mp * 4 && w.partial - w.b >= s.group * s.m * s.mp * 4);
+    CHECK(w.bytes >= w.inverse + s.group * 8 && w.inverse - w.partial >= s.group * s.parts * 8);
+    for (int64_t at : {w.x[1], w.a, w.b, w.partial, w.inverse}) CHECK(at % 256 == 0);
+    // work items of a launch, byte offsets within an operand's tile
+    CHECK(s.group * s.parts < (int64_t(1) << 24) && s.group * ((s.m + 63) / 64) * ((s.np + 63) / 64) * 256 < (int64_t(1) << 32));
+    CHECK(s.group * ns_largest_grid(s) * kNsThreads < (int64_t(1) << 32));
+    CHECK(256 * s.np * 4 < (int64_t(1) << 31));
+}
+
+static void scores(int64_t tokens, int64_t vocab, int64_t top) {
+    const ScoreShape s = score_shape(tokens, vocab, top);
+    CHECK(s.splits >= 1 && s.segment % kScoreBlock == 0 && s.segment * s.splits >= vocab && s.segment * (s.splits - 1) < vocab);
+    CHECK(s.splits == 1 ? s.bytes == 0 : s.bytes >= tokens * s.splits * (16 + 8 * top));
+    CHECK(s.splits == 1 || tokens * s.splits <= 4096);
+}
+
+// The power of two that a factor rounded to fp32 stands for.
+static double power(double x) {
+    const double p = std::exp2(std::round(std::log2(x)));
+    CHECK(std::fabs(x / p - 1) < 1e-6);
+    return p;
+}
+
+// Every matrix stays in fp16's range: the polynomial on singular values, in double.
+static void scales(const double (*coef)[3], int steps) {
+    NsPass pass[ZSMR_MAX_NS_STEPS];
+    double first = 0;
+    CHECK(ns_passes(coef, steps, pass, &first));
+    CHECK(first >= 16384 && first <= 32768);
+    for (int k = 0; k <= 10000; ++k) {
+        double x = k / 10000.0, sx = first;
+        for (int i = 0; i < steps; ++i) {
+            const double a = x * x, sa = pass[i].a_mul * sx * sx, b = coef[i][1] * a + coef[i][2] * a * a;
+            CHECK(a * sa <= 32800);
+            const double sb = power(coef[i][2] != 0 ? pass[i].b_mul * sa * sa / coef[i][2] : coef[i][1] != 0 ? pass[i].b_old * sa / coef[i][1] : 32768);
+            CHECK(std::fabs(b) * sb <= 32800);
+            const double y = coef[i][0] * x + b * x, next = pass[i].x_mul * sb * sx;
+            CHECK(std::fabs(pass[i].x_old - coef[i][0] * next / sx) <= 1e-6 * std::fabs(pass[i].x_old));
+            CHECK(i + 1 == steps ? next == 1 : std::fabs(y) * next <= 32800);
+            x = std::fabs(y);
+            sx = next;
+        }
+    }
+}
+
+int main() {
+    for (int64_t r : {1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 700, 767, 1003, 1024, 1600, 2048, 4096, 6400, 14336, 65536, 262144})
+        for (int64_t c : {1, 5, 32, 64, 100, 128, 129, 192, 193, 320, 1000, 1600, 2049, 4096, 5000, 14336, 32768, 262144})
+            for (int64_t n : {1, 2, 7, 64, 1000, 16385, 1048576})
+                if (r * c <= ZSMR_MAX_MATRIX) shape(r, c, n);
+    for (int64_t t : {1, 2, 3, 16, 63, 64, 129, 255, 256, 511, 1023, 1024, 1025, 8192, 16777216})
+        for (int64_t v : {1, 2, 500, 511, 512, 513, 2048, 4095, 4096, 4097, 50257, 128256, 2097152})
+            for (int64_t k : {0, 1, 20, 64}) scores(t, v, k);
+    const double quintic[5][3] = {{3.4445, -4.7750, 2.0315}, {3.4445, -4.7750, 2.0315}, {3.4445, -4.7750, 2.0315}, {3.4445, -4.7750, 2.0315}, {3.4445, -4.7750, 2.0315}};
+    const double cubic[3][3] = {{1.5, -0.5, 0}, {1.5, -0.5, 0}, {1.5, -0.5, 0}}, line[2][3] = {{180, 0, 0}, {0.001, 0, 0}}, none[2][3] = {{0, 0, 0}, {2, -1, 0.3}};
+    const double odd[4][3] = {{-3, 2, -1}, {0.1, 0.5, -0.2}, {1, -1, 0.1}, {0, 0, 0.3}};
+    scales(quintic, 5);
+    scales(cubic, 3);
+    scales(line, 2);
+    scales(none, 2);
+    scales(odd, 4);
+    std::printf("plans passed\n");
+    return 0;
+}
+"""
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_plans(tmp_path):
+    exe = compile_driver(tmp_path, PLAN, ["-fsanitize=address,undefined", "-fno-sanitize-recover=all"])
+    env = dict(os.environ, ASAN_OPTIONS="halt_on_error=1:verify_asan_link_order=0")
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300, env=env)
+    assert r.returncode == 0 and "plans passed" in r.stdout, r.stdout + r.stderr
+
+
+def test_structures_match_the_header():
+    assert ctypes.sizeof(ops.zsmr_newton) == 16 + 16 * 24 and ctypes.sizeof(ops.zsmr_muon) == 40

@@ -502,7 +502,9 @@ def zsmr_set_xcd_balance(even_permille: int = XCD_BALANCE_DEFAULT) -> None:
 _OPS = ("zsmr_embed_lookup", "zsmr_embed_grad_workspace", "zsmr_embed_grad", "zsmr_xent_workspace",
         "zsmr_xent_forward", "zsmr_xent_backward", "zsmr_norm_workspace", "zsmr_grad_norm",
         "zsmr_clip_coef", "zsmr_clip_grads", "zsmr_clip_flatten", "zero_reduce_shard_sumsq",
-        "zero_clipped_step", "ZSMR_FP32")
+        "zero_clipped_step", "ZSMR_FP32", "zsmr_orthogonalize_workspace", "zsmr_orthogonalize",
+        "zero_muon_step", "zsmr_logprobs_workspace", "zsmr_logprobs", "zsmr_logprobs_grad",
+        "zero_muon_workspace", "NS_COEFS", "ZSMR_MAX_TOP")
 
 
 def __getattr__(name: str):

@@ -30,7 +30,8 @@ CSRC = os.path.join(PKG, "csrc")
 
 LIB = os.path.join(PKG, "libzsmr.so")
 LIB_SOURCES = ("zsmr_kernels.hip", "zsmr_api.cpp", "zsmr_norm.hip", "zsmr_embed.hip",
-               "zsmr_xent.hip", "zsmr_ops_api.cpp")
+               "zsmr_xent.hip", "zsmr_ops_api.cpp", "zsmr_newton.hip", "zsmr_newton_api.cpp",
+               "zsmr_scores.hip", "zsmr_scores_api.cpp")
 BINDING = os.path.join(PKG, "_ops.so")
 SYNTH_LIB = os.path.join(ROOT, "synth", "libzsmr_synth.so")
 CEILING_LIB = os.path.join(ROOT, "ceiling", "libzsmr_ceiling.so")

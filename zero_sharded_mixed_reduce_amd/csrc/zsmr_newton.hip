@@ -1,0 +1,691 @@
+// gfx950 kernels of the orthogonalised update and of the shard step that applies it.
+//
+//   X0 = x / (|x|_F + eps),  X' = a X + (b A + c A^2) X,  A = X X^T
+//
+// for each of a few (a, b, c): an odd polynomial that moves every singular value
+// towards 1.  X is the wide orientation, m <= n, so the inner matrices are m x m.
+// All of it is matrix products: A and A^2 are symmetric, of which only the tiles on
+// and below the diagonal are computed and written twice, so a pass does
+// m^2 n + m^3 + 2 m^2 n operations.
+//
+// Precision.  The first passes raise small singular values by a factor of several
+// hundred, and a rounding of X with them: with operands of one 16-bit rounding the
+// result is off by 2e-3 (fp16) or 2e-2 (bf16) of its norm.  So every matrix is held
+// as the sum of two fp16 parts, x = hi + lo, together 22 bits, and a product is three
+// matrix products of fp16, hi hi + lo hi + hi lo, summed in one fp32 accumulator:
+// the accuracy of fp32 operands at a third of the 16-bit matrix rate, where gfx950's
+// fp32 matrix instructions run at a sixteenth.  lo lo, 2^-22 of the result, is left
+// out.  Powers of two known beforehand keep all parts inside fp16's range
+// (zsmr_newton_plan.h).
+//
+// Layout.  32 columns of a row are 64 bytes of hi and 64 bytes of lo, side by side,
+// so a step of 32 k is one 128-byte line a row.  A product loads both parts of a
+// tile once for its three uses.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "zsmr_dev.h"
+#include "zsmr_mfma.h"
+#include "zsmr_newton_launch.h"
+#include "zsmr_ops_launch.h"
+
+#pragma clang fp contract(off)
+
+namespace zsmr {
+namespace {
+
+constexpr int kThreads = kNsThreads, kWaves = kThreads / 64;
+constexpr int T = kNsTile;
+
+// ---------------------------------------------------------------- split fp16 --
+struct Split8 {
+    u16x8 hi, lo;
+};
+__device__ __forceinline__ Split8 split8(f32x8 f) {
+    Split8 s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        s.hi[i] = narrow16<ZSMR_FP16>(f[i]);
+        s.lo[i] = narrow16<ZSMR_FP16>(f[i] - widen16<ZSMR_FP16>(s.hi[i]));
+    }
+    return s;
+}
+// Element (row, col) of a matrix whose rows are ld 16-bit values apart; col a
+// multiple of 8.
+__device__ __forceinline__ int64_t split_at(int64_t row, int64_t col, int64_t ld) {
+    return row * ld + (col >> 5) * 64 + (col & 31);
+}
+__device__ __forceinline__ void store_split(uint16_t* p, int64_t at, f32x8 f) {
+    const Split8 s = split8(f);
+    *reinterpret_cast<u16x8*>(p + at) = s.hi;
+    *reinterpret_cast<u16x8*>(p + at + 32) = s.lo;
+}
+__device__ __forceinline__ f32x8 load_split(const uint16_t* p, int64_t at) {
+    const u16x8 hi = *reinterpret_cast<const u16x8*>(p + at), lo = *reinterpret_cast<const u16x8*>(p + at + 32);
+    f32x8 f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = widen16<ZSMR_FP16>(hi[i]) + widen16<ZSMR_FP16>(lo[i]);
+    return f;
+}
+
+// ------------------------------------------------------------------ operands --
+// Both parts of R rows of an operand and 32 k of it, in LDS.
+//  k along rows: R rows of 128 bytes, hi and lo; the 16-byte chunk c of row r sits
+//    in slot c ^ (r & 7), so that the 8 rows a read touches at a time lie in
+//    different banks.
+//  OUTER, k is the row index in memory: 32 rows of R columns, 4 R bytes; the
+//    32-byte unit u of row k sits in slot u ^ f(k), f = k's bits 0, 1 and 3: the
+//    transposing read of a wave takes a 32-byte unit of 16 rows.
+// The loads read through a buffer descriptor whose bound makes rows past the
+// operand's end zero; columns are padded with zeros to whole steps.
+template <int R, bool OUTER, int WAVES>
+struct Operand {
+    static constexpr int kBytes = R * 128;
+    static constexpr int kLoads = R * 8 / (WAVES * 64);     // of each thread
+    static_assert(R * 8 % (WAVES * 64) == 0, "whole loads");
+    uint32_t off[kLoads];
+    const char* base;
+    int64_t left, step;
+
+    __device__ __forceinline__ static int swizzle(int k) { return ((k & 3) | ((k >> 3 & 1) << 2)) << 1; }
+
+    // at: the tile's first row of the product; k0: first k, a multiple of 32
+    __device__ __forceinline__ void init(const Mat& m, int64_t at, int64_t k0) {
+        const int64_t row_bytes = m.ld * 2;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int idx = i * (WAVES * 64) + (int)threadIdx.x;
+            if constexpr (OUTER) {
+                const int k = idx / (R / 4), chunk = idx % (R / 4) ^ swizzle(k);
+                off[i] = at * 4 + chunk * 16 < row_bytes ? (uint32_t)(k * row_bytes + chunk * 16) : 0x80000000u;
+            } else {
+                const int row = idx / 8, chunk = idx % 8 ^ (row & 7);
+                off[i] = at + row < m.rows ? (uint32_t)(row * row_bytes + chunk * 16) : 0x80000000u;
+            }
+        }
+        const char* p = reinterpret_cast<const char*>(m.p);
+        if constexpr (OUTER) {
+            base = p + k0 * row_bytes + at * 4;
+            left = (m.rows - k0) * row_bytes - at * 4;
+            step = kNsStep * row_bytes;
+        } else {
+            base = p + at * row_bytes + k0 * 4;
+            left = (m.rows - at) * row_bytes - k0 * 4;
+            step = kNsStep * 4;
+        }
+    }
+    // Start the loads of one step into `to` and move on; `on` false: the same
+    // instructions, which read nothing and write zeros.
+    __device__ __forceinline__ void load(char* to, bool on) {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+        const int bound = !on || left < 0 ? 0 : left > 0x7fffffff ? 0x7fffffff : (int)left;
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, bound, 0x00027000);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(to + (i * WAVES + wave) * 1024), 16, off[i], 0, 0, 0);
+        base += step;
+        left -= step;
+    }
+    // The operand registers of a lane for the 16 rows from `at` of the tile:
+    // k = 8 * (lane / 16) + 0..7, of hi (part 0) or lo (1).
+    __device__ __forceinline__ static u32x4 read(const char* t, int at, int part) {
+        const int lane = threadIdx.x % 64;
+        if constexpr (OUTER) {
+            const int k = lane / 16 * 8 + lane % 16 / 4;
+            const int chunk = (at / 32 * 8 + at % 32 / 8 + part * 4 + lane % 4 / 2) ^ swizzle(k);
+            const char* p = t + k * (R * 4) + chunk * 16 + (lane & 1) * 8;
+            const u32x2 a = read_transposed(p), b = read_transposed(p + 4 * (R * 4));
+            u32x4 r;
+            r[0] = a[0];
+            r[1] = a[1];
+            r[2] = b[0];
+            r[3] = b[1];
+            return r;
+        } else {
+            const int row = at + lane % 16;
+            return *reinterpret_cast<const u32x4*>(t + row * 128 + ((part * 4 + lane / 16) ^ (row & 7)) * 16);
+        }
+    }
+};
+
+// ------------------------------------------------------------------- product --
+enum : int { N_GRAM, N_SQUARE, N_UPDATE, N_LAST };
+
+// D[p, q] = sum_k P[p, k] Q[q, k] for each matrix of the group; a result's row is q.
+struct NsProduct {
+    Mat p, q;                       // of the first matrix
+    int64_t p_batch, q_batch;       // 16-bit values from matrix to matrix
+    int32_t steps, p_tiles, q_tiles, tiles, count;
+    float old_mul, mul;             // result = old_mul * old + mul * D
+    const uint16_t* old;            // of the result's shape and layout
+    uint16_t* dst;
+    int64_t ld, batch, rows, cols;  // of the result: ld of old and dst in 16-bit values
+    // N_LAST
+    int64_t first;                  // the group's first matrix
+    int32_t tall, apply, dtype;     // dtype: of out, or of p16
+    void* out;
+    int64_t out_stride, out_batch;  // in the matrices' own orientation
+    float* master;
+    float decay, rate;
+};
+
+// Eight results, or fewer, of row r from column c on, in the matrices' own
+// orientation.
+__device__ __forceinline__ void put_result(const NsProduct& p, int64_t matrix, int64_t r, int64_t c, int n, f32x8 f) {
+    if (n <= 0) return;
+    if (!p.apply) {
+        const int64_t e = matrix * p.out_batch + r * p.out_stride + c;
+        if (n >= 8) {
+            if (p.dtype == ZSMR_BF16) store8<ZSMR_BF16>(p.out, e, f);
+            else if (p.dtype == ZSMR_FP16) store8<ZSMR_FP16>(p.out, e, f);
+            else store8<ZSMR_FP32>(p.out, e, f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+                if (i < n) {
+                    if (p.dtype == ZSMR_BF16) store1<ZSMR_BF16>(p.out, e + i, f[i]);
+                    else if (p.dtype == ZSMR_FP16) store1<ZSMR_FP16>(p.out, e + i, f[i]);
+                    else store1<ZSMR_FP32>(p.out, e + i, f[i]);
+                }
+        }
+        return;
+    }
+    // master = decay * master - rate * update, every operation rounded to fp32
+    const int64_t e = (matrix * (p.tall ? p.cols : p.rows) + r) * (p.tall ? p.rows : p.cols) + c;
+    if (n >= 8) {
+        f32x8 w = load8<ZSMR_FP32>(p.master, e);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = w[i] * p.decay - p.rate * f[i];
+        store8<ZSMR_FP32>(p.master, e, w);
+        if (p.dtype == ZSMR_BF16) store8<ZSMR_BF16>(p.out, e, w);
+        else store8<ZSMR_FP16>(p.out, e, w);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (i < n) {
+                const float w = p.master[e + i] * p.decay - p.rate * f[i];
+                p.master[e + i] = w;
+                if (p.dtype == ZSMR_BF16) store1<ZSMR_BF16>(p.out, e + i, w);
+                else store1<ZSMR_FP16>(p.out, e + i, w);
+            }
+    }
+}
+
+// The largest r with r (r + 1) / 2 <= i.
+__device__ __forceinline__ int triangle_row(int i) {
+    int r = (int)((sqrtf(8.f * (float)i + 1.f) - 1.f) * 0.5f);
+    while ((int64_t)(r + 1) * (r + 2) / 2 <= i) ++r;
+    while ((int64_t)r * (r + 1) / 2 > i) --r;
+    return r;
+}
+
+template <int EPI>
+__global__ __launch_bounds__(kThreads, 2) void ns_product_kernel(NsProduct p) {
+#if defined(__HIP_DEVICE_COMPILE__)     // the scheduling hints have no host form
+    constexpr bool kSymmetric = EPI == N_GRAM || EPI == N_SQUARE, kOuter = !kSymmetric;
+    constexpr int WP = 2, TP = T / WP / 16, TQ = T / (kWaves / WP) / 16, STAGES = 2;
+    typedef Operand<T, kOuter, kWaves> P;
+    typedef Operand<T, false, kWaves> Q;
+    constexpr int kStage = P::kBytes + Q::kBytes;
+    __shared__ __attribute__((aligned(1024))) char smem[STAGES * kStage];
+    static_assert(STAGES * kStage >= T * T * 4, "the results leave through the same LDS");
+
+    // Consecutive workgroups go to the eight XCDs in turn; each XCD takes a
+    // contiguous run of tiles, in groups of 8 rows of tiles, so that the tiles it
+    // works on at a time share operands in its L2.
+    const int all = p.tiles * p.count, xcd = blockIdx.x % 8, each = all / 8, rem = all % 8;
+    int tile = xcd * each + min(xcd, rem) + (int)blockIdx.x / 8;
+    const int matrix = tile / p.tiles;
+    tile -= matrix * p.tiles;
+    constexpr int kGroup = 8;
+    int tp, tq;
+    if constexpr (kSymmetric) {
+        // rows tp of tiles, tq <= tp
+        const int first = triangle_row(tile) / kGroup * kGroup, height = min(kGroup, p.p_tiles - first);
+        tile -= first * (first + 1) / 2;
+        if (tile < first * height) {
+            tp = first + tile % height;
+            tq = tile / height;
+        } else {
+            tile -= first * height;
+            int column = 0;
+            while (tile >= height - column) tile -= height - column++;
+            tq = first + column;
+            tp = tq + tile;
+        }
+    } else {
+        const int group = tile / (kGroup * p.q_tiles), in_group = tile - group * kGroup * p.q_tiles;
+        const int height = min(kGroup, p.p_tiles - group * kGroup);
+        tp = group * kGroup + in_group % height;
+        tq = in_group / height;
+    }
+
+    P op;
+    Q oq;
+    op.init(Mat{p.p.p + matrix * p.p_batch, p.p.ld, p.p.rows, p.p.cols}, (int64_t)tp * T, 0);
+    oq.init(Mat{p.q.p + matrix * p.q_batch, p.q.ld, p.q.rows, p.q.cols}, (int64_t)tq * T, 0);
+
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, wp = wave % WP, wq = wave / WP;
+    f32x4 acc[TP][TQ];
+#pragma unroll
+    for (int i = 0; i < TP; ++i)
+#pragma unroll
+        for (int j = 0; j < TQ; ++j) acc[i][j] = 0.f;
+
+    // Two stages of LDS.  A step multiplies hi hi while it reads the lo parts, then
+    // waits for the next stage and lets this one be filled again, and multiplies
+    // lo hi and hi lo while it reads the next stage's hi parts into the other set
+    // of registers.
+    constexpr int kReads = TP * (kOuter ? 2 : 1) + TQ, kMfma = TP * TQ, kLoads = P::kLoads + Q::kLoads;
+    u32x4 ph[2][TP], qh[2][TQ], pl[TP], ql[TQ];
+    auto read = [&](u32x4* a, u32x4* b, const char* stage, int part) {
+#pragma unroll
+        for (int j = 0; j < TQ; ++j) b[j] = Q::read(stage + P::kBytes, (wq * TQ + j) * 16, part);
+#pragma unroll
+        for (int i = 0; i < TP; ++i) a[i] = P::read(stage, (wp * TP + i) * 16, part);
+    };
+    auto multiply = [&](const u32x4* a, const u32x4* b) {
+#pragma unroll
+        for (int i = 0; i < TP; ++i)
+#pragma unroll
+            for (int j = 0; j < TQ; ++j) acc[i][j] = mfma<ZSMR_FP16>(a[i], b[j], acc[i][j]);
+    };
+    char* const stage0 = smem;
+    char* const stage1 = smem + kStage;
+    op.load(stage0, true);
+    oq.load(stage0 + P::kBytes, true);
+    op.load(stage1, p.steps > 1);
+    oq.load(stage1 + P::kBytes, p.steps > 1);
+    ZSMR_WAIT(kLoads);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    read(ph[0], qh[0], stage0, 0);
+    auto step = [&](int s, char* cur, const char* next, u32x4* p0, u32x4* q0, u32x4* p1, u32x4* q1) {
+        read(pl, ql, cur, 1);
+        multiply(p0, q0);
+        interleave<kReads, 0, kMfma>();
+        ZSMR_WAIT(0);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        op.load(cur, s + STAGES < p.steps);
+        oq.load(cur + P::kBytes, s + STAGES < p.steps);
+        read(p1, q1, next, 0);
+        multiply(pl, q0);
+        multiply(p0, ql);
+        interleave<kReads, kLoads, 2 * kMfma>();
+    };
+    for (int s = 0; s < p.steps; s += 2) {
+        step(s, stage0, stage1, ph[0], qh[0], ph[1], qh[1]);
+        if (s + 1 == p.steps) break;
+        step(s + 1, stage1, stage0, ph[1], qh[1], ph[0], qh[0]);
+    }
+    ZSMR_WAIT(0);           // no load may still be on its way to this LDS
+    __syncthreads();
+
+    // acc[i][j][r] is D at p = 16 i + 4 (lane / 16) + r, q = 16 j + lane % 16 of the
+    // wave's part.  Results leave through LDS as [q][p] in fp32, the 16-byte chunk c
+    // of row q in slot c ^ f(q): rows are then read along p, columns along q, each
+    // with few bank conflicts.
+    float* const out = reinterpret_cast<float*>(smem);
+    auto at = [&](int q, int c) { return q * T + (c ^ ((q ^ q >> 3) & 31)) * 4; };
+#pragma unroll
+    for (int j = 0; j < TQ; ++j)
+#pragma unroll
+        for (int i = 0; i < TP; ++i)
+            *reinterpret_cast<f32x4*>(out + at((wq * TQ + j) * 16 + lane % 16, (wp * TP + i) * 4 + lane / 16)) = acc[i][j];
+    __syncthreads();
+    const int64_t p0 = (int64_t)tp * T, q0 = (int64_t)tq * T;
+    const uint16_t* old = p.old + matrix * p.batch;
+    uint16_t* dst = p.dst + matrix * p.batch;
+    const int64_t padded = p.ld / 2;
+    auto finish = [&](int64_t row, int64_t col, f32x8 d) {
+        if constexpr (EPI == N_GRAM) return d * p.mul;
+        else return load_split(old, split_at(row, col, p.ld)) * p.old_mul + d * p.mul;
+    };
+    // rows q of the result
+    for (int k = threadIdx.x; k < T * T / 8; k += kThreads) {
+        const int q = k / (T / 8), c = k % (T / 8);
+        if (q0 + q >= p.rows || p0 + c * 8 >= padded) continue;
+        f32x4* const lo = reinterpret_cast<f32x4*>(out + at(q, 2 * c));
+        f32x4* const hi = reinterpret_cast<f32x4*>(out + at(q, 2 * c + 1));
+        f32x8 d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            d[i] = (*lo)[i];
+            d[4 + i] = (*hi)[i];
+        }
+        d = finish(q0 + q, p0 + c * 8, d);
+        if constexpr (EPI != N_LAST) {
+            store_split(dst, split_at(q0 + q, p0 + c * 8, p.ld), d);
+        } else if (p.tall) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                (*lo)[i] = d[i];
+                (*hi)[i] = d[4 + i];
+            }
+        } else {
+            put_result(p, p.first + matrix, q0 + q, p0 + c * 8, (int)min((int64_t)8, p.cols - p0 - c * 8), d);
+        }
+    }
+    // rows p: the other side of a symmetric result, or a tall matrix
+    if (kSymmetric ? tp == tq : EPI != N_LAST || !p.tall) return;
+    __syncthreads();
+    for (int k = threadIdx.x; k < T * T / 8; k += kThreads) {
+        const int row = k / (T / 8), q = k % (T / 8) * 8;
+        const int64_t limit = kSymmetric ? p.rows : p.cols;
+        if (p0 + row >= limit || q0 + q >= (kSymmetric ? padded : p.rows)) continue;
+        f32x8 d;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = out[at(q + i, row / 4) + row % 4];
+        if constexpr (EPI == N_LAST) put_result(p, p.first + matrix, p0 + row, q0 + q, (int)min((int64_t)8, p.rows - q0 - q), d);
+        else store_split(dst, split_at(p0 + row, q0 + q, p.ld), finish(p0 + row, q0 + q, d));
+    }
+#endif
+}
+
+// ------------------------------------------------------------ before the products --
+// Squares are taken and summed in fp64, as for the gradient norm.
+__device__ __forceinline__ void add_squares(f32x8 f, double* s) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) *s = __builtin_fma((double)f[i], (double)f[i], *s);
+}
+
+// Partial sums of squares of the group's matrices: parts of each.
+template <int DT>
+__global__ __launch_bounds__(kThreads) void ns_sumsq_kernel(const void* x, int64_t stride, int64_t batch, int64_t rows, int64_t cols,
+                                                            int32_t row_threads, double* partial) {
+    const int64_t from = blockIdx.y * batch;
+    const int each = kThreads / row_threads, t = threadIdx.x % row_threads;
+    double s = 0;
+    for (int64_t r = (int64_t)blockIdx.x * each + threadIdx.x / row_threads; r < rows; r += (int64_t)gridDim.x * each)
+        for (int64_t c = t * 8; c < cols; c += row_threads * 8) {
+            const int64_t e = from + r * stride + c;
+            if (c + 8 <= cols) {
+                add_squares(load8<DT>(x, e), &s);
+            } else {
+                for (int64_t i = 0; i < cols - c; ++i) {
+                    const double f = load1<DT>(x, e + i);
+                    s = __builtin_fma(f, f, s);
+                }
+            }
+        }
+    s = block_sum<kThreads>(s);
+    if (threadIdx.x == 0) partial[blockIdx.y * gridDim.x + blockIdx.x] = s;
+}
+
+// The mean gradient over the ranks, the momentum, and the update u before it is
+// orthogonalised, with its partial sums of squares.  Rows are summed in rank
+// order, in fp32.
+struct MomentumArgs {
+    StepArgs step;                  // from the group's first matrix on
+    int64_t each;                   // elements of a matrix
+    int32_t nesterov;
+    float beta;
+    float* u;
+    double* partial;
+};
+__device__ __forceinline__ float momentum(const MomentumArgs& a, float g, float* m) {
+    const float sum = a.step.inv_pow2 ? g * a.step.inv_nf : g / a.step.nf;
+    *m = a.beta * *m + sum;
+    return a.nesterov ? sum + a.beta * *m : *m;
+}
+constexpr int kRows = 8;
+template <int DT>
+__global__ __launch_bounds__(kThreads) void ns_momentum_kernel(MomentumArgs a) {
+    const int64_t from = blockIdx.y * a.each;
+    double s = 0;
+    for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8; i < a.each; i += (int64_t)gridDim.x * kThreads * 8) {
+        const int64_t e = from + i;
+        const uint16_t* p = a.step.grads + e;
+        if (i + 8 <= a.each) {
+            f32x8 g = -0.0f;            // -0 + x is x for every x
+            int r = 0;
+            for (; r + kRows <= a.step.nrows; r += kRows) {
+                u16x8 h[kRows];
+#pragma unroll
+                for (int k = 0; k < kRows; ++k)
+                    h[k] = __builtin_nontemporal_load(reinterpret_cast<const u16x8_any*>(p + (int64_t)(r + k) * a.step.row_stride));
+#pragma unroll
+                for (int k = 0; k < kRows; ++k)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) g[j] += widen16<DT>(h[k][j]);
+            }
+            for (; r < a.step.nrows; ++r) {
+                const u16x8 h = *reinterpret_cast<const u16x8_any*>(p + (int64_t)r * a.step.row_stride);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) g[j] += widen16<DT>(h[j]);
+            }
+            f32x8 m = load8<ZSMR_FP32>(a.step.m, e), u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float mj = m[j];
+                u[j] = momentum(a, g[j], &mj);
+                m[j] = mj;
+            }
+            store8<ZSMR_FP32>(a.step.m, e, m);
+            store8<ZSMR_FP32>(a.u, e, u);
+            add_squares(u, &s);
+        } else {
+            for (int64_t j = 0; j < a.each - i; ++j) {
+                float g = widen16<DT>(p[j]);
+                for (int r = 1; r < a.step.nrows; ++r) g += widen16<DT>(p[(int64_t)r * a.step.row_stride + j]);
+                const float u = momentum(a, g, a.step.m + e + j);
+                a.u[e + j] = u;
+                s = __builtin_fma((double)u, (double)u, s);
+            }
+        }
+    }
+    s = block_sum<kThreads>(s);
+    if (threadIdx.x == 0) a.partial[blockIdx.y * gridDim.x + blockIdx.x] = s;
+}
+
+// first / (norm + eps) of each matrix; a matrix of zeros stays one with eps 0 too.
+__global__ __launch_bounds__(64) void ns_norm_kernel(const double* partial, int32_t parts, double eps, double first, double* inverse) {
+    double s = 0;
+    for (int i = threadIdx.x; i < parts; i += 64) s += partial[(int64_t)blockIdx.x * parts + i];
+    s = block_sum<64>(s);
+    if (threadIdx.x == 0) {
+        const double norm = sqrt(s) + eps;
+        inverse[blockIdx.x] = norm == 0 ? 0 : first / norm;
+    }
+}
+
+// X0 in two fp16 parts and in the wide orientation.  A workgroup takes 64 rows and
+// 64 columns of it; a tall matrix is turned in LDS.
+struct PackArgs {
+    const void* x;
+    int64_t stride, batch, m, n, np;
+    const double* inverse;
+    uint16_t* dst;
+    int32_t tiles_n, tiles, tall;
+};
+template <int DT>
+__global__ __launch_bounds__(kThreads) void ns_pack_kernel(PackArgs a) {
+    __shared__ float turned[64][65];
+    const int64_t matrix = blockIdx.x / a.tiles;
+    const int tile = blockIdx.x % a.tiles;
+    const int64_t m0 = tile / a.tiles_n * 64, n0 = (int64_t)(tile % a.tiles_n) * 64;
+    const double inverse = a.inverse[matrix];
+    const int64_t rows = a.tall ? a.n : a.m, cols = a.tall ? a.m : a.n, r0 = a.tall ? n0 : m0, c0 = a.tall ? m0 : n0;
+    uint16_t* dst = a.dst + matrix * a.m * a.np * 2;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int r = k * 32 + threadIdx.x / 8, c = threadIdx.x % 8 * 8;
+        f32x8 f = 0.f;
+        if (r0 + r < rows) {
+            const int64_t e = matrix * a.batch + (r0 + r) * a.stride + c0 + c;
+            if (c0 + c + 8 <= cols) {
+                f = load8<DT>(a.x, e);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 7; ++i)
+                    if (c0 + c + i < cols) f[i] = load1<DT>(a.x, e + i);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = (float)((double)f[i] * inverse);
+        if (!a.tall) {
+            if (r0 + r < rows && c0 + c < a.np) store_split(dst, split_at(r0 + r, c0 + c, a.np * 2), f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) turned[c + i][r] = f[i];
+        }
+    }
+    if (!a.tall) return;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int r = k * 32 + threadIdx.x / 8, c = threadIdx.x % 8 * 8;
+        if (m0 + r >= a.m || n0 + c >= a.np) continue;
+        f32x8 f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = turned[r][c + i];
+        store_split(dst, split_at(m0 + r, n0 + c, a.np * 2), f);
+    }
+}
+
+// ------------------------------------------------------------------ launches --
+struct Space {
+    uint16_t *x[2], *a, *b;
+    double *partial, *inverse;
+};
+Space space_of(const NsShape& s, void* ws) {
+    const NsSpace w = ns_space(s);
+    char* p = static_cast<char*>(ws);
+    Space r;
+    for (int i = 0; i < 2; ++i) r.x[i] = reinterpret_cast<uint16_t*>(p + w.x[i]);
+    r.a = reinterpret_cast<uint16_t*>(p + w.a);
+    r.b = reinterpret_cast<uint16_t*>(p + w.b);
+    r.partial = reinterpret_cast<double*>(p + w.partial);
+    r.inverse = reinterpret_cast<double*>(p + w.inverse);
+    return r;
+}
+
+template <typename F>
+void of_dtype(int32_t dtype, F each) {
+    if (dtype == ZSMR_BF16) each(std::integral_constant<int, ZSMR_BF16>());
+    else if (dtype == ZSMR_FP16) each(std::integral_constant<int, ZSMR_FP16>());
+    else each(std::integral_constant<int, ZSMR_FP32>());
+}
+
+// From the partial sums on, for `count` matrices from the `first` one on.
+void passes(const NewtonArgs& a, const Space& w, const void* x, int32_t dtype, int64_t stride, int64_t batch, int64_t first, int count,
+            hipStream_t stream) {
+    const NsShape& s = a.shape;
+    ns_norm_kernel<<<count, 64, 0, stream>>>(w.partial, s.parts, a.eps, a.first, w.inverse);
+    PackArgs pack{};
+    pack.x = x;
+    pack.stride = stride;
+    pack.batch = batch;
+    pack.m = s.m;
+    pack.n = s.n;
+    pack.np = s.np;
+    pack.inverse = w.inverse;
+    pack.dst = w.x[0];
+    pack.tiles_n = (int32_t)((s.np + 63) / 64);
+    pack.tiles = (int32_t)((s.m + 63) / 64) * pack.tiles_n;
+    pack.tall = s.tall;
+    of_dtype(dtype, [&](auto dt) { ns_pack_kernel<decltype(dt)::value><<<pack.tiles * count, kThreads, 0, stream>>>(pack); });
+
+    NsProduct p{};
+    p.count = count;
+    p.first = first;
+    p.tall = s.tall;
+    p.apply = a.step.master != nullptr;
+    p.dtype = p.apply ? a.param_dtype : a.out_dtype;
+    p.out = p.apply ? a.step.p16 : a.out;
+    p.out_stride = a.out_stride;
+    p.out_batch = a.out_batch;
+    p.master = a.step.master;
+    p.decay = a.decay;
+    p.rate = a.rate;
+    const int64_t xb = s.m * s.np * 2, ab = s.m * s.mp * 2;
+    for (int i = 0; i < a.steps; ++i) {
+        const NsPass& pass = a.pass[i];
+        uint16_t *from = w.x[i % 2], *to = w.x[1 - i % 2];
+        const Mat mx{from, s.np * 2, s.m, s.np * 2}, ma{w.a, s.mp * 2, s.m, s.mp * 2}, mb{w.b, s.mp * 2, s.m, s.mp * 2};
+        p.p_tiles = p.q_tiles = (int32_t)s.m_tiles;
+        p.tiles = (int32_t)(s.m_tiles * (s.m_tiles + 1) / 2);
+        p.rows = p.cols = s.m;
+        p.ld = s.mp * 2;
+        p.batch = ab;
+        // A
+        p.p = p.q = mx;
+        p.p_batch = p.q_batch = xb;
+        p.steps = (int32_t)(s.np / kNsStep);
+        p.dst = w.a;
+        p.mul = pass.a_mul;
+        ns_product_kernel<N_GRAM><<<p.tiles * count, kThreads, 0, stream>>>(p);
+        // B
+        p.p = p.q = ma;
+        p.p_batch = p.q_batch = ab;
+        p.steps = (int32_t)(s.mp / kNsStep);
+        p.old = w.a;
+        p.dst = w.b;
+        p.old_mul = pass.b_old;
+        p.mul = pass.b_mul;
+        ns_product_kernel<N_SQUARE><<<p.tiles * count, kThreads, 0, stream>>>(p);
+        // X': columns of X are the product's p, rows of B its q
+        p.p = mx;
+        p.p_batch = xb;
+        p.q = mb;
+        p.p_tiles = (int32_t)s.n_tiles;
+        p.tiles = (int32_t)(s.n_tiles * s.m_tiles);
+        p.cols = s.n;
+        p.ld = s.np * 2;
+        p.batch = xb;
+        p.old = from;
+        p.dst = to;
+        p.old_mul = pass.x_old;
+        p.mul = pass.x_mul;
+        if (i + 1 < a.steps) ns_product_kernel<N_UPDATE><<<p.tiles * count, kThreads, 0, stream>>>(p);
+        else ns_product_kernel<N_LAST><<<p.tiles * count, kThreads, 0, stream>>>(p);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_orthogonalize(const NewtonArgs& a, void* ws, hipStream_t stream) {
+    const NsShape& s = a.shape;
+    const Space w = space_of(s, ws);
+    const int64_t rows = s.tall ? s.n : s.m, cols = s.tall ? s.m : s.n;
+    int32_t row_threads = 1;
+    while (row_threads < kThreads && row_threads * 8 < cols) row_threads *= 2;
+    for (int64_t first = 0; first < s.count; first += s.group) {
+        const int count = (int)std::min(s.group, s.count - first);
+        const char* x = static_cast<const char*>(a.x) + first * a.x_batch * (a.x_dtype == ZSMR_FP32 ? 4 : 2);
+        of_dtype(a.x_dtype, [&](auto dt) {
+            ns_sumsq_kernel<decltype(dt)::value><<<dim3(s.parts, count), kThreads, 0, stream>>>(x, a.x_stride, a.x_batch, rows, cols,
+                                                                                               row_threads, w.partial);
+        });
+        passes(a, w, x, a.x_dtype, a.x_stride, a.x_batch, first, count, stream);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_muon(const NewtonArgs& a, void* ws, hipStream_t stream) {
+    const NsShape& s = a.shape;
+    const Space w = space_of(s, ws);
+    const int64_t each = s.m * s.n, cols = s.tall ? s.m : s.n;
+    float* const u = reinterpret_cast<float*>(w.x[1]);
+    for (int64_t first = 0; first < s.count; first += s.group) {
+        const int count = (int)std::min(s.group, s.count - first);
+        MomentumArgs m{};
+        m.step = a.step;
+        m.step.grads += first * each;
+        m.step.m += first * each;
+        m.each = each;
+        m.nesterov = a.nesterov;
+        m.beta = a.beta;
+        m.u = u;
+        m.partial = w.partial;
+        if (a.grad_dtype == ZSMR_BF16) ns_momentum_kernel<ZSMR_BF16><<<dim3(s.parts, count), kThreads, 0, stream>>>(m);
+        else ns_momentum_kernel<ZSMR_FP16><<<dim3(s.parts, count), kThreads, 0, stream>>>(m);
+        passes(a, w, u, ZSMR_FP32, cols, each, first, count, stream);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace zsmr

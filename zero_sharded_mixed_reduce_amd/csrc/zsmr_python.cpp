@@ -312,6 +312,148 @@ int32_t clip_flatten(Args a) {          // addresses, numels, dtypes, coef, flat
                              stream_of(a[5]));
 }
 
+// The triples of an odd polynomial's steps.
+zsmr_newton newton(PyObject* coefs, PyObject* eps) {
+    zsmr_newton ns{};
+    ns.eps = as_double(eps);
+    Ref steps(PySequence_Fast(coefs, "coefs: a sequence of triples is required"));
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(steps.p);
+    if (n < 1 || n > ZSMR_MAX_NS_STEPS) {
+        PyErr_Format(PyExc_ValueError, "coefs: 1 to %d triples are required, got %zd", ZSMR_MAX_NS_STEPS, n);
+        fail();
+    }
+    ns.steps = (int32_t)n;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        Ref triple(PySequence_Fast(PySequence_Fast_GET_ITEM(steps.p, i), "coefs: a sequence of triples is required"));
+        if (PySequence_Fast_GET_SIZE(triple.p) != 3) {
+            PyErr_SetString(PyExc_ValueError, "coefs: a sequence of triples is required");
+            fail();
+        }
+        for (int k = 0; k < 3; ++k) ns.coef[i][k] = as_double(PySequence_Fast_GET_ITEM(triple.p, k));
+    }
+    return ns;
+}
+
+// A matrix, or a stack of them, of any format; elements of a row contiguous.
+struct Stack {
+    int64_t count = 1, rows = 0, cols = 0, stride = 0, batch = 0;
+    int32_t dtype = 0;
+    PyObject* x;
+    const char* what;
+    Stack(PyObject* t, const char* name) : x(t), what(name) {
+        Shape shape(t);
+        Ref format(PyObject_GetAttr(t, n_dtype));
+        dtype = code_of(format.p);
+        if ((shape.dims != 2 && shape.dims != 3) || !dtype) {
+            PyErr_Format(PyExc_ValueError, "%s: a matrix or a stack of matrices of fp16, bf16 or fp32 is required, got %S of %S", what,
+                         format.p, shape.size.p);
+            fail();
+        }
+        const int d = (int)shape.dims - 2;
+        if (d) count = shape[0];
+        rows = shape[d];
+        cols = shape[d + 1];
+        Ref strides(PyObject_CallMethodNoArgs(t, n_stride));
+        stride = rows > 1 ? as_int(PyTuple_GET_ITEM(strides.p, d)) : cols;
+        batch = count > 1 ? as_int(PyTuple_GET_ITEM(strides.p, 0)) : 0;
+        if (cols > 1 && as_int(PyTuple_GET_ITEM(strides.p, d + 1)) != 1) {
+            PyErr_Format(PyExc_ValueError, "%s: elements of a row must be contiguous", what);
+            fail();
+        }
+        if (stride < cols) {
+            PyErr_Format(PyExc_ValueError, "%s: rows overlap", what);
+            fail();
+        }
+    }
+    void same_as(const Stack& o, bool format) const {
+        if (count != o.count || rows != o.rows || cols != o.cols) {
+            PyErr_Format(PyExc_ValueError, "%s: %lld x %lld x %lld, %s has %lld x %lld x %lld", what, (long long)count, (long long)rows,
+                         (long long)cols, o.what, (long long)o.count, (long long)o.rows, (long long)o.cols);
+            fail();
+        }
+        if (format && dtype != o.dtype) {
+            PyErr_Format(PyExc_ValueError, "%s: %s has another format", what, o.what);
+            fail();
+        }
+    }
+    void* at() const { return address(x, what); }
+};
+
+int32_t orthogonalize(Args a) {         // x, out, ws, coefs, eps, stream
+    Stack x(a[0], "x"), out(a[1], "out");
+    out.same_as(x, false);
+    const zsmr_newton ns = newton(a[3], a[4]);
+    Vector ws(a[2], 0, nullptr, "workspace");
+    return zsmr_orthogonalize(x.at(), x.dtype, x.stride, x.batch, out.at(), out.dtype, out.stride, out.batch, x.rows, x.cols, x.count,
+                              &ns, ws.at(), ws.bytes, stream_of(a[5]));
+}
+
+// Given tokens, or none.
+struct MaybeIds {
+    int64_t n = -1;
+    int32_t bytes = 8;
+    PyObject* x;
+    explicit MaybeIds(PyObject* t, int64_t rows) : x(t) {
+        if (t == Py_None) return;
+        Ids ids(t);
+        n = ids.n;
+        bytes = ids.bytes;
+        if (n != rows) {
+            PyErr_Format(PyExc_ValueError, "token ids: %lld are required, got %lld", (long long)rows, (long long)n);
+            fail();
+        }
+    }
+    void* at() const { return x == Py_None ? nullptr : address(x, "token ids"); }
+};
+
+Stack logits_of(PyObject* t, const char* what) {
+    Shape shape(t);
+    if (shape.dims != 2) {
+        PyErr_Format(PyExc_ValueError, "%s: n_tokens x vocab is required, got %S", what, shape.size.p);
+        fail();
+    }
+    return Stack(t, what);
+}
+
+int32_t logprobs(Args a) {  // logits, ids, logprob, lse, entropy, ws, top_ids, top_logprobs, scale, stream
+    const Stack logits = logits_of(a[0], "logits");
+    const int64_t n = logits.rows;
+    MaybeIds ids(a[1], n);
+    Vector logprob(a[2], n, t_fp32, "logprob"), lse(a[3], n, t_fp32, "lse"), entropy(a[4], n, t_fp32, "entropy");
+    Vector ws(a[5], 0, nullptr, "workspace");
+    int64_t top = -1;
+    int32_t top_bytes = 8;
+    for (int i = 6; i < 8; ++i) {
+        if (a[i] == Py_None) continue;
+        const char* what = i == 6 ? "top_ids" : "top_logprobs";
+        Shape shape(a[i]);
+        Ref format(PyObject_GetAttr(a[i], n_dtype));
+        const bool fits = i == 6 ? format.p == t_int32 || format.p == t_int64 : format.p == t_fp32;
+        if (i == 6) top_bytes = format.p == t_int32 ? 4 : 8;
+        if (shape.dims != 2 || shape[0] != n || !fits || (top >= 0 && shape[1] != top) || shape[1] > ZSMR_MAX_TOP || !contiguous(a[i])) {
+            PyErr_Format(PyExc_ValueError, "%s: contiguous n_tokens x top %s are required, got %S of %S", what,
+                         i == 6 ? "int32 or int64" : "fp32", format.p, shape.size.p);
+            fail();
+        }
+        top = shape[1];
+    }
+    return zsmr_logprobs(logits.at(), logits.stride, logits.dtype, ids.at(), ids.bytes, n, logits.cols, (float)as_double(a[8]),
+                         (float*)logprob.at(), (float*)lse.at(), (float*)entropy.at(), top < 0 ? 0 : (int32_t)top,
+                         a[6] == Py_None ? nullptr : address(a[6], "top_ids"), top_bytes,
+                         a[7] == Py_None ? nullptr : (float*)address(a[7], "top_logprobs"), ws.at(), ws.bytes, stream_of(a[9]));
+}
+
+int32_t logprobs_grad(Args a) {  // logits, ids, lse, entropy, dlogits, dlogprob, dentropy, scale, stream
+    const Stack logits = logits_of(a[0], "logits"), dlogits = logits_of(a[4], "dlogits");
+    dlogits.same_as(logits, true);
+    const int64_t n = logits.rows;
+    MaybeIds ids(a[1], n);
+    Vector lse(a[2], n, t_fp32, "lse"), entropy(a[3], n, t_fp32, "entropy"), g(a[5], n, t_fp32, "dlogprob"), h(a[6], n, t_fp32, "dentropy");
+    return zsmr_logprobs_grad(logits.at(), logits.stride, logits.dtype, ids.at(), ids.bytes, n, logits.cols, (float)as_double(a[7]),
+                              (float*)lse.at(), (float*)entropy.at(), (float*)g.at(), (float*)h.at(), dlogits.at(), dlogits.stride,
+                              stream_of(a[8]));
+}
+
 zsmr_ctx* context(PyObject* handle) { return handle == Py_None ? nullptr : (zsmr_ctx*)(intptr_t)as_int(handle); }
 
 // Elements of the (rank, unit) piece, or 0 where the layout refuses the pair
@@ -335,6 +477,31 @@ int32_t reduce_shard_sumsq(Args a) {    // ctx, rank, unit, grads, stride, base,
     Vector sumsq(a[8], 1, t_fp64, "sumsq"), ws(a[9], 0, nullptr, "workspace");
     return zero_reduce_shard_sumsq(ctx, rank, unit, grads.at(), stride, base, truth(a[6]), (float*)g.at(), (double*)sumsq.at(),
                                    ws.at(), ws.bytes, stream_of(a[10]));
+}
+
+int32_t muon_step(Args a) {     // ctx, rank, unit, begin, rows, cols, count, grads, stride, base, master, momentum, p16, ws,
+                                // lr, beta, weight_decay, scale, nesterov, coefs, eps, stream
+    zsmr_ctx* ctx = context(a[0]);
+    const int32_t rank = as_int32(a[1]), unit = as_int32(a[2]);
+    const int64_t begin = as_int(a[3]), rows = as_int(a[4]), cols = as_int(a[5]), count = as_int(a[6]), stride = as_int(a[8]), base = as_int(a[9]);
+    const zsmr_muon hp{as_double(a[14]), as_double(a[15]), as_double(a[16]), as_double(a[17]), truth(a[18]), 0};
+    const zsmr_newton ns = newton(a[19], a[20]);
+    // elements from the piece's first on that the call touches; what it refuses anyway touches nothing
+    int64_t end = 0, reach = 0;
+    const int64_t n = piece_of(ctx, rank, unit);
+    if (begin >= 0 && rows > 0 && cols > 0 && count > 0 && rows <= ZSMR_MAX_SIDE && cols <= ZSMR_MAX_SIDE && count <= ZSMR_MAX_MATRICES) {
+        const __int128 all = (__int128)begin + (__int128)rows * cols * count;
+        if (all <= n) end = (int64_t)all;
+    }
+    zsmr_layout_info info{};
+    if (end > 0 && base >= 0 && stride >= 0 && zero_layout_info(ctx, &info) == ZSMR_OK) {
+        const __int128 all = (__int128)base + (__int128)(info.world - 1) * stride + end;
+        reach = all > INT64_MAX / 4 ? INT64_MAX / 4 : (int64_t)all;
+    }
+    Vector grads(a[7], 2 * reach, nullptr, "grads"), master(a[10], 4 * end, nullptr, "master"), m(a[11], 4 * end, nullptr, "momentum");
+    Vector p16(a[12], 2 * end, nullptr, "p16_dst"), ws(a[13], 0, nullptr, "workspace");
+    return zero_muon_step(ctx, rank, unit, begin, rows, cols, count, grads.at(), stride, base, (float*)master.at(), (float*)m.at(),
+                          p16.at(), &hp, &ns, ws.at(), ws.bytes, stream_of(a[21]));
 }
 
 int32_t clipped_step(Args a) {  // ctx, rank, unit, g, coef, master, m, v, p16, t, lr, beta1, beta2, eps, stream
@@ -362,7 +529,9 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 #define ENTRY(f, n) {#f, (PyCFunction)(void (*)(void))entry<f, n>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(embed_lookup, 5),  ENTRY(embed_grad, 7),   ENTRY(xent_forward, 8),        ENTRY(xent_backward, 11),
                          ENTRY(grad_norm, 8),     ENTRY(clip_coef, 6),    ENTRY(clip_grads, 5),          ENTRY(clip_flatten, 6),
-                         ENTRY(reduce_shard_sumsq, 11), ENTRY(clipped_step, 15), {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(reduce_shard_sumsq, 11), ENTRY(clipped_step, 15),
+                         ENTRY(orthogonalize, 6), ENTRY(muon_step, 22),   ENTRY(logprobs, 10),            ENTRY(logprobs_grad, 9),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -25,10 +25,22 @@ _z.load()                       # raises ImportError if the libraries have not b
 from . import _ops  # noqa: E402  (the native half: checks of tensors, calls of libzsmr.so)
 
 ZSMR_FP32 = 3
+ZSMR_MAX_TOP, MAX_NS_STEPS = 64, 16
+# the odd quintic that takes small singular values up and leaves large ones about 1
+NS_COEFS = ((3.4445, -4.7750, 2.0315),) * 5
 TENSOR_CODES = {torch.float16: _z.ZSMR_FP16, torch.bfloat16: _z.ZSMR_BF16, torch.float32: ZSMR_FP32}
 
 _i32, _i64, _vp, _f32, _f64 = (ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float,
                                ctypes.c_double)
+
+class zsmr_newton(ctypes.Structure):
+    _fields_ = [("eps", _f64), ("steps", _i32), ("pad", _i32), ("coef", (_f64 * 3) * MAX_NS_STEPS)]
+
+
+class zsmr_muon(ctypes.Structure):
+    _fields_ = [("lr", _f64), ("beta", _f64), ("weight_decay", _f64), ("scale", _f64),
+                ("nesterov", _i32), ("pad", _i32)]
+
 
 # name -> (restype, argtypes); the list is the ABI of include/zsmr_ops.h
 SIGNATURES = {
@@ -50,6 +62,17 @@ SIGNATURES = {
                                        _vp]),
     "zero_clipped_step": (_i32, [_vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
                                  ctypes.POINTER(_z.zsmr_adam), _vp]),
+    "zsmr_orthogonalize_workspace": (_i64, [_i64, _i64, _i64]),
+    "zsmr_orthogonalize": (_i32, [_vp, _i32, _i64, _i64, _vp, _i32, _i64, _i64, _i64, _i64, _i64,
+                                  ctypes.POINTER(zsmr_newton), _vp, _i64, _vp]),
+    "zero_muon_step": (_i32, [_vp, _i32, _i32, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp,
+                              _vp, ctypes.POINTER(zsmr_muon), ctypes.POINTER(zsmr_newton), _vp, _i64,
+                              _vp]),
+    "zsmr_logprobs_workspace": (_i64, [_i64, _i64, _i32]),
+    "zsmr_logprobs": (_i32, [_vp, _i64, _i32, _vp, _i32, _i64, _i64, _f32, _vp, _vp, _vp, _i32, _vp,
+                             _i32, _vp, _vp, _i64, _vp]),
+    "zsmr_logprobs_grad": (_i32, [_vp, _i64, _i32, _vp, _i32, _i64, _i64, _f32, _vp, _vp, _vp, _vp,
+                                  _vp, _i64, _vp]),
 }
 
 _LIB = None
@@ -169,3 +192,56 @@ def zero_clipped_step(ctx, rank: int, unit: int, g, coef, master, m, v, p16_dst,
                              beta2, eps, stream)
     if code:
         _z._check(code, "zero_clipped_step")
+
+
+def zsmr_orthogonalize_workspace(rows: int, cols: int, count: int = 1) -> int:
+    return _size(_lib().zsmr_orthogonalize_workspace(int(rows), int(cols), int(count)),
+                 "zsmr_orthogonalize_workspace")
+
+
+def zsmr_orthogonalize(x, out, ws, coefs=NS_COEFS, eps: float = 1e-7, stream=None) -> None:
+    """x, out: a matrix or a stack of them (count x rows x cols), fp16, bf16 or fp32
+    each, elements of a row contiguous; coefs: a triple (a, b, c) for each step."""
+    code = _ops.orthogonalize(x, out, ws, coefs, eps, stream)
+    if code:
+        _z._check(code, "zsmr_orthogonalize")
+
+
+def zero_muon_workspace(rows: int, cols: int, count: int = 1) -> int:
+    """Bytes of workspace of zero_muon_step: those of zsmr_orthogonalize."""
+    return zsmr_orthogonalize_workspace(rows, cols, count)
+
+
+def zero_muon_step(ctx, rank: int, unit: int, begin: int, rows: int, cols: int, count: int, grads,
+                   row_stride: int, base_elem: int, master, momentum, p16_dst, ws, lr: float,
+                   beta: float = 0.95, weight_decay: float = 0.0, scale: float = 1.0,
+                   nesterov: bool = True, coefs=NS_COEFS, eps: float = 1e-7, stream=None) -> None:
+    code = _ops.muon_step(ctx.handle, rank, unit, begin, rows, cols, count, grads, row_stride,
+                          base_elem, master, momentum, p16_dst, ws, lr, beta, weight_decay, scale,
+                          nesterov, coefs, eps, stream)
+    if code:
+        _z._check(code, "zero_muon_step")
+
+
+def zsmr_logprobs_workspace(n_tokens: int, vocab: int, top: int = 0) -> int:
+    return _size(_lib().zsmr_logprobs_workspace(int(n_tokens), int(vocab), int(top)),
+                 "zsmr_logprobs_workspace")
+
+
+def zsmr_logprobs(logits, ids, logprob, lse, entropy, ws, top_ids=None, top_logprobs=None,
+                  scale: float = 1.0, stream=None) -> None:
+    """logits: n_tokens x vocab, fp16, bf16 or fp32; ids: n_tokens int32 or int64, or
+    None (then logprob is None too); logprob, lse, entropy: n_tokens fp32 or None;
+    top_ids, top_logprobs: contiguous, n_tokens x top of int32 or int64 and of fp32, or
+    None."""
+    code = _ops.logprobs(logits, ids, logprob, lse, entropy, ws, top_ids, top_logprobs, scale, stream)
+    if code:
+        _z._check(code, "zsmr_logprobs")
+
+
+def zsmr_logprobs_grad(logits, ids, lse, entropy, dlogits, dlogprob=None, dentropy=None,
+                       scale: float = 1.0, stream=None) -> None:
+    """dlogprob, dentropy: n_tokens fp32 or None (zeros); dlogits may be logits."""
+    code = _ops.logprobs_grad(logits, ids, lse, entropy, dlogits, dlogprob, dentropy, scale, stream)
+    if code:
+        _z._check(code, "zsmr_logprobs_grad")
