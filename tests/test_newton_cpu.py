@@ -29,7 +29,7 @@ def newton(coefs=ops.NS_COEFS, eps=1e-7, steps=None):
 
 
 NS = newton()
-ORTHOGONALIZE = dict(x=A, xd=BF16, xs=64, xb=640, out=B, od=F32, os=64, ob=640, rows=10, cols=64, count=3, ns=NS, ws=W, wb=BIG, stream=None)
+ORTHOGONALIZE = dict(x=A, xd=BF16, xs=180, xb=36000, out=B, od=F32, os=180, ob=36000, rows=200, cols=180, count=3, ns=NS, ws=W, wb=BIG, stream=None)
 NAN, INF = float("nan"), float("inf")
 BAD_NS = [newton(eps=-1.0), newton(eps=NAN), newton(eps=INF), newton(steps=0), newton(steps=17), newton(((NAN, 0, 0),)), newton(((0, INF, 0),)),
           newton(((182.0, 0, 0),)), newton(((100.0, 0, 0), (2.0, 0, 0))), newton(((1.0, 0, 0), (1e308, 1e308, 1e308))), newton(((1.0, 1e6, -1e6),))]
@@ -37,8 +37,8 @@ BAD_NS = [newton(eps=-1.0), newton(eps=NAN), newton(eps=INF), newton(steps=0), n
 
 @pytest.mark.parametrize("change,code", [
     (dict(x=None), ARG), (dict(out=None), ARG), (dict(rows=0), ARG), (dict(cols=0), ARG), (dict(rows=(1 << 18) + 1), ARG), (dict(rows=-1), ARG),
-    (dict(rows=1 << 17, cols=(1 << 16) + 1), ARG), (dict(count=-1), ARG), (dict(count=(1 << 20) + 1), ARG), (dict(xs=63), ARG), (dict(os=63), ARG),
-    (dict(xs=(1 << 21) + 1), ARG), (dict(xb=-1), ARG), (dict(ob=639), ARG), (dict(ob=64, os=191), ARG), (dict(ob=63, os=192), ARG),
+    (dict(rows=1 << 17, cols=(1 << 16) + 1), ARG), (dict(count=-1), ARG), (dict(count=(1 << 20) + 1), ARG), (dict(xs=179), ARG), (dict(os=179), ARG),
+    (dict(xs=(1 << 21) + 1), ARG), (dict(xb=-1), ARG), (dict(ob=35999), ARG), (dict(ob=180, os=539), ARG), (dict(ob=179, os=540), ARG),
     (dict(xb=(1 << 40) + 1), ARG), (dict(ns=None), ARG), (dict(ws=None), ARG), (dict(wb=1000), ARG), (dict(xd=4), DTYPE), (dict(od=0), DTYPE),
     (dict(x=A + 1), ALIGN), (dict(out=B + 2), ALIGN), (dict(x=A + 2, xd=F32), ALIGN), (dict(ws=W + 8), ALIGN)] + [(dict(ns=ns), ARG) for ns in BAD_NS])
 def test_orthogonalize_refusals(change, code):
@@ -54,7 +54,8 @@ def test_workspaces():
     # X twice and the two inner matrices, 4 bytes an element
     assert z.zsmr_orthogonalize_workspace(4096, 4096) >= 4 * 4 * 4096 ** 2
     assert z.zsmr_orthogonalize_workspace(4096, 4096) < 4.1 * 4 * 4096 ** 2
-    assert z.zsmr_orthogonalize_workspace(100, 50, 7) == z.zsmr_orthogonalize_workspace(50, 100, 7) == z.zero_muon_workspace(50, 100, 7)
+    assert z.zsmr_orthogonalize_workspace(300, 150, 7) == z.zsmr_orthogonalize_workspace(150, 300, 7) == z.zero_muon_workspace(150, 300, 7) > 0
+    assert z.zsmr_orthogonalize_workspace(128, 128, 1000) == 0      # in a CU's LDS
     # a group's matrices at a time
     assert z.zsmr_orthogonalize_workspace(1024, 1024, 1 << 20) < 6.5e8
     assert z.zsmr_orthogonalize_workspace(1, 1, 1 << 20) < 6.5e8
@@ -70,12 +71,12 @@ def test_workspaces():
 
 def test_muon_refusals_count_nothing():
     hp = lambda **kw: ops.zsmr_muon(**(dict(lr=0.02, beta=0.9, weight_decay=0.1, scale=1.0, nesterov=1, pad=0) | kw))  # noqa: E731
-    ctx = z.zero_init_shards(3000, 3, z.ZSMR_ZERO3_OWNER, "bf16", units=[1000, 2000])
+    ctx = z.zero_init_shards(201000, 3, z.ZSMR_ZERO3_OWNER, "bf16", units=[1000, 200000])
     z.zero_set_unit_owners(ctx, [2, 0])
-    ok = dict(ctx=ctx.handle, rank=0, unit=1, begin=100, rows=10, cols=60, count=3, grads=A, stride=2000, base=0, master=B, momentum=C, p16=D,
+    ok = dict(ctx=ctx.handle, rank=0, unit=1, begin=100, rows=200, cols=300, count=3, grads=A, stride=200000, base=0, master=B, momentum=C, p16=D,
               hp=hp(), ns=NS, ws=W, wb=BIG, stream=None)
-    bad = [(dict(ctx=None), ARG), (dict(rank=3), ARG), (dict(rank=1), ARG), (dict(unit=2), ARG), (dict(begin=-1), ARG), (dict(begin=201), ARG),
-           (dict(rows=0), ARG), (dict(count=4), ARG), (dict(count=-1), ARG), (dict(grads=None), ARG), (dict(stride=1999), ARG), (dict(base=-1), ARG),
+    bad = [(dict(ctx=None), ARG), (dict(rank=3), ARG), (dict(rank=1), ARG), (dict(unit=2), ARG), (dict(begin=-1), ARG), (dict(begin=20001), ARG),
+           (dict(rows=0), ARG), (dict(count=4), ARG), (dict(count=-1), ARG), (dict(grads=None), ARG), (dict(stride=199999), ARG), (dict(base=-1), ARG),
            (dict(master=None), ARG), (dict(momentum=None), ARG), (dict(p16=None), ARG), (dict(hp=None), ARG), (dict(ns=None), ARG), (dict(ws=None), ARG),
            (dict(wb=100), ARG), (dict(rows=1 << 18, cols=1 << 15, count=1 << 20), ARG), (dict(grads=A + 1), ALIGN), (dict(master=B + 2), ALIGN),
            (dict(momentum=C + 1), ALIGN), (dict(p16=D + 1), ALIGN), (dict(ws=W + 4), ALIGN)]
@@ -177,6 +178,10 @@ static void shape(int64_t rows, int64_t cols, int64_t count) {
     CHECK(s.group >= 1 && s.group <= count && s.parts >= 1);
     CHECK(s.group == 1 || s.group * s.m * s.n <= kNsGroupElems);
     const NsSpace w = ns_space(s);
+    if (s.small) {      // a form that holds it
+        CHECK(s.m <= (s.small == 3 ? 128 : 64) && s.n <= (s.small == 1 ? 64 : s.small == 2 ? 256 : 128) && w.bytes == 0);
+        return;
+    }
     CHECK(w.x[1] - w.x[0] >= s.group * s.m * s.np * 4 && w.a - w.x[1] >= s.group * s.m * s.np * 4);
     CHECK(w.x[1] - w.x[0] >= s.group * s.m * s.n * 4);      // the fp32 update
     CHECK(w.b - w.a >= s.group * s.m * s.mp * 4 && w.partial - w.b >= s.group * s.m * s.mp * 4);

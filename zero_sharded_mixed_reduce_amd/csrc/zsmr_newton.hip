@@ -426,10 +426,10 @@ struct MomentumArgs {
     float* u;
     double* partial;
 };
-__device__ __forceinline__ float momentum(const MomentumArgs& a, float g, float* m) {
-    const float sum = a.step.inv_pow2 ? g * a.step.inv_nf : g / a.step.nf;
-    *m = a.beta * *m + sum;
-    return a.nesterov ? sum + a.beta * *m : *m;
+__device__ __forceinline__ float momentum(const StepArgs& s, float beta, int32_t nesterov, float g, float* m) {
+    const float sum = s.inv_pow2 ? g * s.inv_nf : g / s.nf, next = beta * *m + sum;
+    *m = next;
+    return nesterov ? sum + beta * next : next;
 }
 constexpr int kRows = 8;
 template <int DT>
@@ -461,7 +461,7 @@ __global__ __launch_bounds__(kThreads) void ns_momentum_kernel(MomentumArgs a) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 float mj = m[j];
-                u[j] = momentum(a, g[j], &mj);
+                u[j] = momentum(a.step, a.beta, a.nesterov, g[j], &mj);
                 m[j] = mj;
             }
             store8<ZSMR_FP32>(a.step.m, e, m);
@@ -471,7 +471,7 @@ __global__ __launch_bounds__(kThreads) void ns_momentum_kernel(MomentumArgs a) {
             for (int64_t j = 0; j < a.each - i; ++j) {
                 float g = widen16<DT>(p[j]);
                 for (int r = 1; r < a.step.nrows; ++r) g += widen16<DT>(p[(int64_t)r * a.step.row_stride + j]);
-                const float u = momentum(a, g, a.step.m + e + j);
+                const float u = momentum(a.step, a.beta, a.nesterov, g, a.step.m + e + j);
                 a.u[e + j] = u;
                 s = __builtin_fma((double)u, (double)u, s);
             }
@@ -481,15 +481,16 @@ __global__ __launch_bounds__(kThreads) void ns_momentum_kernel(MomentumArgs a) {
     if (threadIdx.x == 0) a.partial[blockIdx.y * gridDim.x + blockIdx.x] = s;
 }
 
-// first / (norm + eps) of each matrix; a matrix of zeros stays one with eps 0 too.
+// first / (norm + eps) of a matrix; a matrix of zeros stays one with eps 0 too.
+__device__ __forceinline__ double inverse_norm(double sum, double eps, double first) {
+    const double norm = sqrt(sum) + eps;
+    return norm == 0 ? 0 : first / norm;
+}
 __global__ __launch_bounds__(64) void ns_norm_kernel(const double* partial, int32_t parts, double eps, double first, double* inverse) {
     double s = 0;
     for (int i = threadIdx.x; i < parts; i += 64) s += partial[(int64_t)blockIdx.x * parts + i];
     s = block_sum<64>(s);
-    if (threadIdx.x == 0) {
-        const double norm = sqrt(s) + eps;
-        inverse[blockIdx.x] = norm == 0 ? 0 : first / norm;
-    }
+    if (threadIdx.x == 0) inverse[blockIdx.x] = inverse_norm(s, eps, first);
 }
 
 // X0 in two fp16 parts and in the wide orientation.  A workgroup takes 64 rows and
@@ -546,7 +547,350 @@ __global__ __launch_bounds__(kThreads) void ns_pack_kernel(PackArgs a) {
     }
 }
 
+// ------------------------------------------------------------ small matrices --
+// A workgroup takes a whole matrix through every pass.  X is in LDS as two fp16
+// parts, and in fp32 in registers: a wave owns up to PARTS blocks of FP x FQ tiles of
+// 16 columns and 16 rows, a lane four consecutive columns of a row of each tile.  The
+// inner matrix is in LDS once, A and then B.  Rows and columns past the matrix are zeros.
+struct SmallArgs {
+    NewtonArgs a;
+    int64_t first;                  // matrix
+};
+// The 16-byte chunk c of row r sits in slot c ^ f(r): 8 rows read at one chunk fall
+// into different banks, and so do the 32 bytes that a transposing read takes of each of
+// 4 rows.
+__device__ __forceinline__ int small_slot(int row, int chunk) { return chunk ^ ((row & 3) << 1 | (row >> 2 & 1)); }
+// Where a lane reads its operand registers of 16 rows (or, OUTER, columns) and k =
+// 8 (lane / 16) + 0..7 of the hi parts at the matrix's corner; LD: bytes of a row.  The
+// lo parts are 64 bytes on or back (the slot's bit 2), 16 rows, 32 k and 32 columns on
+// are fixed distances away.
+template <int LD, bool OUTER>
+__device__ __forceinline__ int small_lane() {
+    const int lane = threadIdx.x % 64;
+    if constexpr (OUTER) {
+        const int row = lane / 16 * 8 + lane % 16 / 4;
+        return row * LD + small_slot(row, lane % 4 / 2) * 16 + (lane & 1) * 8;
+    } else {
+        const int row = lane % 16;
+        return row * LD + small_slot(row, lane / 16) * 16;
+    }
+}
+// t: the corner of the 16 rows (columns) and 32 k; at: small_lane(), moved for the lo
+// parts and for columns 16..31 of 32.
+template <int LD, bool OUTER>
+__device__ __forceinline__ u32x4 small_read(const char* t, int at) {
+    if constexpr (OUTER) {
+        // row + 4 has the other f's bit 0
+        const u32x2 a = read_transposed(t + at), b = read_transposed(t + 4 * LD + (at ^ 16));
+        u32x4 r;
+        r[0] = a[0];
+        r[1] = a[1];
+        r[2] = b[0];
+        r[3] = b[1];
+        return r;
+    } else {
+        return *reinterpret_cast<const u32x4*>(t + at);
+    }
+}
+// Four columns from col on of a row, in both parts.
+template <int LD>
+__device__ __forceinline__ void small_store(char* t, int row, int col, f32x4 f) {
+    u16x4 hi, lo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        hi[i] = narrow16<ZSMR_FP16>(f[i]);
+        lo[i] = narrow16<ZSMR_FP16>(f[i] - widen16<ZSMR_FP16>(hi[i]));
+    }
+    char* const p = t + row * LD + col / 32 * 128 + (col & 4) * 2;
+    const int slot = small_slot(row, col % 32 / 8) * 16;
+    *reinterpret_cast<u16x4*>(p + slot) = hi;
+    *reinterpret_cast<u16x4*>(p + (slot ^ 64)) = lo;
+}
+
+// Up to four elements in memory, `step` apart; those past `count` are zeros.
+template <int DT>
+__device__ __forceinline__ f32x4 load4(const void* p, int64_t e, int64_t step, int count) {
+    f32x4 f = 0.f;
+    if (step == 1 && count >= 4) {
+        if constexpr (DT == ZSMR_FP32) return *reinterpret_cast<const f32x4_any*>(static_cast<const float*>(p) + e);
+        const u16x4 h = *reinterpret_cast<const u16x4_any*>(static_cast<const uint16_t*>(p) + e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = widen16<DT>(h[i]);
+        return f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < count) f[i] = load1<DT>(p, e + i * step);
+    return f;
+}
+template <int DT>
+__device__ __forceinline__ void store4(void* p, int64_t e, int64_t step, int count, f32x4 f) {
+    if (step == 1 && count >= 4) {
+        if constexpr (DT == ZSMR_FP32) {
+            *reinterpret_cast<f32x4_any*>(static_cast<float*>(p) + e) = f;
+        } else {
+            u16x4 h;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = narrow16<DT>(f[i]);
+            *reinterpret_cast<u16x4_any*>(static_cast<uint16_t*>(p) + e) = h;
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < count) store1<DT>(p, e + i * step, f[i]);
+}
+template <typename F>
+__device__ __forceinline__ void by_dtype(int32_t dtype, F each) {
+    if (dtype == ZSMR_BF16) each(std::integral_constant<int, ZSMR_BF16>());
+    else if (dtype == ZSMR_FP16) each(std::integral_constant<int, ZSMR_FP16>());
+    else each(std::integral_constant<int, ZSMR_FP32>());
+}
+
+// A matrix of at most MP x NP.
+template <int MP, int NP, int WAVES, int FP, int FQ>
+__global__ __launch_bounds__(WAVES * 64) void ns_small_kernel(SmallArgs s) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    __shared__ __attribute__((aligned(1024))) char smem[MP * NP * 4 + MP * MP * 4];
+    __shared__ double norm;
+    constexpr int kCols = FP * 16, kRows = FQ * 16, PARTS = MP / kRows * (NP / kCols) / WAVES, XLD = NP * 4, ALD = MP * 4;
+    static_assert(PARTS * WAVES == MP / kRows * (NP / kCols) && MP / kRows * (MP / kCols) <= WAVES && FP % 2 == 0, "blocks for every wave");
+    const NewtonArgs& a = s.a;
+    const NsShape& shape = a.shape;
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int m = (int)shape.m, n = (int)shape.n, mb = (int)shape.mp / kRows, nb = (int)((shape.np + kCols - 1) / kCols);
+    char* const xs = smem;
+    char* const as = smem + MP * XLD;
+    const int64_t matrix = s.first + blockIdx.x;
+    const bool tall = shape.tall;
+
+    // Part t of the wave, tile (i, j) of it: columns p from p0 + 16 i on, rows q from q0 + 16 j.
+    struct Place {
+        int row, col;
+    };
+    auto place = [&](int id, int i, int j) {
+        return Place{id % mb * kRows + j * 16 + lane % 16, id / mb * kCols + i * 16 + lane / 16 * 4};
+    };
+    auto tiles = [&](int parts, int limit, auto each) {
+#pragma unroll
+        for (int t = 0; t < PARTS; ++t) {
+            const int id = wave + t * WAVES;
+            if (t >= parts || id >= limit) continue;
+#pragma unroll
+            for (int i = 0; i < FP; ++i)
+#pragma unroll
+                for (int j = 0; j < FQ; ++j) each(t, i, j, place(id, i, j));
+        }
+    };
+    // Element (row, col) of the wide orientation, and the step to the next column.
+    const int64_t step = tall ? (a.step.master ? m : a.x_stride) : 1, out_step = tall ? (a.step.master ? m : a.out_stride) : 1;
+    auto at = [&](Place p, int64_t stride, int64_t batch) {
+        return matrix * batch + (tall ? p.col * stride + p.row : p.row * stride + p.col);
+    };
+    const int64_t own = tall ? m : n, each_matrix = shape.m * shape.n;     // of matrices behind each other
+
+    f32x4 x[PARTS][FP][FQ];
+    double sum = 0;
+#pragma unroll
+    for (int t = 0; t < PARTS; ++t)
+#pragma unroll
+        for (int i = 0; i < FP; ++i)
+#pragma unroll
+            for (int j = 0; j < FQ; ++j) x[t][i][j] = 0.f;
+    if (a.step.master) {
+        tiles(PARTS, mb * nb, [&](int t, int i, int j, Place p) {
+            const int count = p.row < m ? n - p.col : 0;
+            if (count <= 0) return;
+            const int64_t e = at(p, own, each_matrix);
+            f32x4 g = -0.0f, w = load4<ZSMR_FP32>(a.step.m, e, step, count);         // -0 + x is x for every x
+            by_dtype(a.grad_dtype, [&](auto dt) {
+#pragma unroll 4
+                for (int r = 0; r < a.step.nrows; ++r) g += load4<decltype(dt)::value>(a.step.grads + r * a.step.row_stride, e, step, count);
+            });
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float next = w[r];
+                const float u = momentum(a.step, a.beta, a.nesterov, g[r], &next);
+                w[r] = next;
+                if (r < count) x[t][i][j][r] = u;
+            }
+            store4<ZSMR_FP32>(a.step.m, e, step, count, w);
+        });
+    } else {
+        by_dtype(a.x_dtype, [&](auto dt) {
+            tiles(PARTS, mb * nb, [&](int t, int i, int j, Place p) {
+                if (p.row < m) x[t][i][j] = load4<decltype(dt)::value>(a.x, at(p, a.x_stride, a.x_batch), step, n - p.col);
+            });
+        });
+    }
+#pragma unroll
+    for (int t = 0; t < PARTS; ++t)
+#pragma unroll
+        for (int i = 0; i < FP; ++i)
+#pragma unroll
+            for (int j = 0; j < FQ; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sum = __builtin_fma((double)x[t][i][j][r], (double)x[t][i][j][r], sum);
+    sum = block_sum<WAVES * 64>(sum);
+    if (threadIdx.x == 0) norm = inverse_norm(sum, a.eps, a.first);
+    __syncthreads();
+    const double inverse = norm;
+    auto store_x = [&]() {
+        tiles(PARTS, mb * nb, [&](int t, int i, int j, Place p) {
+            if (p.col < (int)shape.np) small_store<XLD>(xs, p.row, p.col, x[t][i][j]);
+        });
+    };
+#pragma unroll
+    for (int t = 0; t < PARTS; ++t)
+#pragma unroll
+        for (int i = 0; i < FP; ++i)
+#pragma unroll
+            for (int j = 0; j < FQ; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[t][i][j][r] = (float)((double)x[t][i][j][r] * inverse);
+    store_x();
+    __syncthreads();
+
+    // A part of D[p, q] = sum_k P[p, k] Q[q, k], over `steps` of 32 k; OUTER: k is P's
+    // row index.  The next step's operands are read while this one's are multiplied.
+    // Columns past a block's matrix are read from elsewhere in LDS and not stored.
+    f32x4 acc[FP][FQ];
+    struct Operands {
+        u32x4 ph[FP], pl[FP], qh[FQ], ql[FQ];
+    };
+    auto product = [&](auto outer, auto p_ld, const char* p, int p0, auto q_ld, const char* q, int q0, int steps) {
+        constexpr bool OUTER = decltype(outer)::value;
+        constexpr int PLD = decltype(p_ld)::value, QLD = decltype(q_ld)::value;
+#pragma unroll
+        for (int i = 0; i < FP; ++i)
+#pragma unroll
+            for (int j = 0; j < FQ; ++j) acc[i][j] = 0.f;
+        p += OUTER ? p0 * 4 : p0 * PLD;
+        q += q0 * QLD;
+        const int pa = small_lane<PLD, OUTER>(), qa = small_lane<QLD, false>();
+        auto read = [&](Operands& o, int k) {
+            const char* const pk = p + k * (OUTER ? 32 * PLD : 128);
+            const char* const qk = q + k * 128;
+#pragma unroll
+            for (int i = 0; i < FP; ++i) {
+                const char* const t = pk + (OUTER ? i / 2 * 128 : i * 16 * PLD);
+                const int at = OUTER ? pa ^ (i % 2 * 32) : pa;
+                o.ph[i] = small_read<PLD, OUTER>(t, at);
+                o.pl[i] = small_read<PLD, OUTER>(t, at ^ 64);
+            }
+#pragma unroll
+            for (int j = 0; j < FQ; ++j) {
+                o.qh[j] = small_read<QLD, false>(qk + j * 16 * QLD, qa);
+                o.ql[j] = small_read<QLD, false>(qk + j * 16 * QLD, qa ^ 64);
+            }
+            asm volatile("" ::: "memory");      // the reads stay ahead of what follows
+        };
+        auto multiply = [&](const u32x4* a, const u32x4* b) {
+#pragma unroll
+            for (int i = 0; i < FP; ++i)
+#pragma unroll
+                for (int j = 0; j < FQ; ++j) acc[i][j] = mfma<ZSMR_FP16>(a[i], b[j], acc[i][j]);
+        };
+        Operands o0, o1;
+        read(o0, 0);
+        for (int k = 0; k < steps; k += 2) {
+            read(o1, min(k + 1, steps - 1));        // always: a branch would make all reads wait at its end
+            multiply(o0.ph, o0.qh);
+            multiply(o0.pl, o0.qh);
+            multiply(o0.ph, o0.ql);
+            if (k + 1 == steps) break;
+            read(o0, min(k + 2, steps - 1));
+            multiply(o1.ph, o1.qh);
+            multiply(o1.pl, o1.qh);
+            multiply(o1.ph, o1.ql);
+        }
+    };
+    // A wave has one part of the inner matrix: there are no more than waves.
+    const bool mine = wave < mb * (((int)shape.mp + kCols - 1) / kCols);
+    const int p0 = wave / mb * kCols, q0 = wave % mb * kRows;
+    auto store_inner = [&](const f32x4 (&f)[FP][FQ]) {
+        if (!mine) return;
+#pragma unroll
+        for (int i = 0; i < FP; ++i)
+#pragma unroll
+            for (int j = 0; j < FQ; ++j) {
+                const Place p = place(wave, i, j);
+                if (p.col < (int)shape.mp) small_store<ALD>(as, p.row, p.col, f[i][j]);
+            }
+    };
+    constexpr std::true_type kRowsOfK;
+    constexpr std::false_type kAlongK;
+    constexpr std::integral_constant<int, XLD> xld;
+    constexpr std::integral_constant<int, ALD> ald;
+    const int x_steps = (int)shape.np / 32, a_steps = (int)shape.mp / 32;
+    for (int pass = 0; pass < a.steps; ++pass) {
+        const NsPass k = a.pass[pass];
+        f32x4 inner[FP][FQ];
+        // A, then B over it
+        if (mine) {
+            product(kAlongK, xld, xs, p0, xld, xs, q0, x_steps);
+#pragma unroll
+            for (int i = 0; i < FP; ++i)
+#pragma unroll
+                for (int j = 0; j < FQ; ++j) inner[i][j] = acc[i][j] * k.a_mul;
+        }
+        store_inner(inner);
+        __syncthreads();
+        if (mine) {
+            product(kAlongK, ald, as, p0, ald, as, q0, a_steps);
+#pragma unroll
+            for (int i = 0; i < FP; ++i)
+#pragma unroll
+                for (int j = 0; j < FQ; ++j) inner[i][j] = inner[i][j] * k.b_old + acc[i][j] * k.b_mul;
+        }
+        __syncthreads();
+        store_inner(inner);
+        __syncthreads();
+        // X', which stays in registers until every wave has read X
+#pragma unroll
+        for (int t = 0; t < PARTS; ++t) {
+            const int id = wave + t * WAVES;
+            if (id >= mb * nb) continue;
+            product(kRowsOfK, xld, xs, id / mb * kCols, ald, as, id % mb * kRows, a_steps);
+#pragma unroll
+            for (int i = 0; i < FP; ++i)
+#pragma unroll
+                for (int j = 0; j < FQ; ++j) x[t][i][j] = x[t][i][j] * k.x_old + acc[i][j] * k.x_mul;
+        }
+        if (pass + 1 == a.steps) break;
+        __syncthreads();
+        store_x();
+        __syncthreads();
+    }
+    tiles(PARTS, mb * nb, [&](int t, int i, int j, Place p) {
+        const int count = p.row < m ? n - p.col : 0;
+        if (count <= 0) return;
+        if (a.step.master) {
+            const int64_t e = at(p, own, each_matrix);
+            f32x4 w = load4<ZSMR_FP32>(a.step.master, e, step, count);
+            w = w * a.decay - a.rate * x[t][i][j];
+            store4<ZSMR_FP32>(a.step.master, e, step, count, w);
+            by_dtype(a.param_dtype, [&](auto dt) { store4<decltype(dt)::value>(a.step.p16, e, step, count, w); });
+        } else {
+            by_dtype(a.out_dtype, [&](auto dt) { store4<decltype(dt)::value>(a.out, at(p, a.out_stride, a.out_batch), out_step, count, x[t][i][j]); });
+        }
+    });
+#endif
+}
+
 // ------------------------------------------------------------------ launches --
+hipError_t launch_small(const NewtonArgs& a, hipStream_t stream) {
+    SmallArgs s{};
+    s.a = a;
+    launch_rows(a.shape.count, 512, [&](int64_t first, int64_t count) {
+        s.first = first;
+        if (a.shape.small == 1) ns_small_kernel<64, 64, 8, 2, 1><<<(unsigned)count, 512, 0, stream>>>(s);
+        else if (a.shape.small == 2) ns_small_kernel<64, 256, 8, 4, 2><<<(unsigned)count, 512, 0, stream>>>(s);
+        else ns_small_kernel<128, 128, 8, 4, 2><<<(unsigned)count, 512, 0, stream>>>(s);
+    });
+    return hipGetLastError();
+}
+
 struct Space {
     uint16_t *x[2], *a, *b;
     double *partial, *inverse;
@@ -649,6 +993,7 @@ void passes(const NewtonArgs& a, const Space& w, const void* x, int32_t dtype, i
 
 hipError_t launch_orthogonalize(const NewtonArgs& a, void* ws, hipStream_t stream) {
     const NsShape& s = a.shape;
+    if (s.small) return launch_small(a, stream);
     const Space w = space_of(s, ws);
     const int64_t rows = s.tall ? s.n : s.m, cols = s.tall ? s.m : s.n;
     int32_t row_threads = 1;
@@ -667,6 +1012,7 @@ hipError_t launch_orthogonalize(const NewtonArgs& a, void* ws, hipStream_t strea
 
 hipError_t launch_muon(const NewtonArgs& a, void* ws, hipStream_t stream) {
     const NsShape& s = a.shape;
+    if (s.small) return launch_small(a, stream);
     const Space w = space_of(s, ws);
     const int64_t each = s.m * s.n, cols = s.tall ? s.m : s.n;
     float* const u = reinterpret_cast<float*>(w.x[1]);

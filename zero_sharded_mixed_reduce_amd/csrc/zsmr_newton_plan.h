@@ -24,11 +24,18 @@ struct NsShape {
     int64_t count, group;               // matrices; of a group, whose launches they share
     int parts;                          // partial sums of squares of a matrix
     int64_t m_tiles, n_tiles;
+    int small;                          // the form of a matrix that stays in LDS, or 0
 };
 
 // A group's matrices have 2^25 elements at most (or are one): enough to fill the
 // CUs many times over, while the workspace stays below 600 MB for any count.
 constexpr int64_t kNsGroupElems = int64_t(1) << 25;
+
+// A matrix that fits a CU's LDS with its inner matrix is one workgroup's: every pass
+// without a launch.  Up to 64 x 64 (1), 64 x 256 (2) and 128 x 128 (3).
+inline int ns_small(int64_t m, int64_t n) {
+    return m <= 64 ? n <= 64 ? 1 : n <= 256 ? 2 : 0 : n <= 128 ? 3 : 0;
+}
 inline NsShape ns_shape(int64_t rows, int64_t cols, int64_t count) {
     NsShape s{};
     s.tall = rows > cols;
@@ -37,6 +44,7 @@ inline NsShape ns_shape(int64_t rows, int64_t cols, int64_t count) {
     s.mp = ns_ceil(s.m, kNsStep);
     s.np = ns_ceil(s.n, kNsStep);
     s.count = count;
+    s.small = ns_small(s.m, s.n);
     s.group = std::max<int64_t>(1, std::min({count, kNsGroupElems / (s.m * s.n), int64_t(1) << 14}));
     // a workgroup of the sums takes 2,048 elements at a time
     s.parts = (int)std::min<int64_t>((s.m * s.n + 2047) / 2048, std::max<int64_t>(1, 1024 / s.group));
@@ -56,6 +64,7 @@ struct NsSpace {
 };
 inline NsSpace ns_space(const NsShape& s) {
     NsSpace w{};
+    if (s.small) return w;
     auto take = [&](int64_t bytes) {
         const int64_t at = w.bytes;
         w.bytes += ns_ceil(bytes, 256);
