@@ -30,8 +30,9 @@ def gen(seed):
     return g
 
 
-def polynomial(x, coefs=NS_COEFS, eps=1e-7, noise=None):
-    """In 64 bits; noise: a generator of rounding errors."""
+def polynomial(x, coefs=NS_COEFS, eps=1e-7, noise=None, groups=()):
+    """In 64 bits; noise: a generator of rounding errors; groups: steps that share one
+    X X^T, as the kernels' do for 16-bit results of matrices that are not square."""
     x = x.double()
     tall = x.shape[-2] > x.shape[-1]
     x = x.mT.contiguous() if tall else x.contiguous()
@@ -51,20 +52,38 @@ def polynomial(x, coefs=NS_COEFS, eps=1e-7, noise=None):
         size = 2.0 ** -24 * (3 * p.shape[-1] / 32 + 1) ** 0.5 + 2.0 ** -22
         return r + (p.abs() @ q.abs()) * size * (torch.rand(r.shape, generator=noise, device="cuda", dtype=torch.float64) * 2 - 1)
 
-    for a, b, c in coefs:
-        if noise is not None:       # the coefficients, and the last additions, in fp32
-            a, b, c = (k * (1 + 2.0 ** -23 * (2 * float(torch.rand((), generator=noise, device="cuda")) - 1)) for k in (a, b, c))
+    coefs = list(coefs)
+    groups = list(groups) or [1] * len(coefs)
+    while coefs:
         x = held(x)
-        gram = held(product(x, x.mT.contiguous()))
-        x = a * x + product(held(b * gram + c * product(gram, gram)), x)
+        gram, total, total_a = held(product(x, x.mT.contiguous())), None, 1.0
+        now, coefs = coefs[:groups[0]], coefs[groups[0]:]
+        groups = groups[1:] or [2]
+        for j, (a, b, c) in enumerate(now):
+            if noise is not None:       # the coefficients, and the last additions, in fp32
+                a, b, c = (k * (1 + 2.0 ** -23 * (2 * float(torch.rand((), generator=noise, device="cuda")) - 1)) for k in (a, b, c))
+            part = held(b * gram + c * product(gram, gram))
+            # the product of a I + part over the steps is total_a I + total
+            total = part if total is None else held(total_a * part + a * total + product(total, part))
+            total_a *= a
+            if j + 1 < len(now):
+                half = held(a * gram + product(gram, part))
+                gram = held(a * half + product(half, part))
+        x = total_a * x + product(total, x)
     return x.mT if tall else x
+
+
+def grouped(x, dtype, coefs):
+    """The longest groups of steps a call may form."""
+    n, m = max(x.shape[-2:]), min(x.shape[-2:])
+    return (3, 2) if dtype is not F32 and 5 * n >= 6 * m and len(coefs) > 1 else ()
 
 
 def allowed(x, dtype, coefs=NS_COEFS, eps=1e-7):
     """The exact result, and the errors a result of `dtype` may have: of each
     element, and in the 2-norm of each matrix."""
     exact = polynomial(x, coefs, eps)
-    off = torch.stack([(polynomial(x, coefs, eps, gen(k)) - exact).square().sum((-2, -1), keepdim=True).sqrt() for k in range(8)]).amax(0)
+    off = torch.stack([(polynomial(x, coefs, eps, gen(k), grouped(x, dtype, coefs)) - exact).square().sum((-2, -1), keepdim=True).sqrt() for k in range(8)]).amax(0)
     step = exact.abs() * HALF_STEP[dtype] + TINY[dtype]
     each = step + 10 * 4 * off / (x.shape[-1] * x.shape[-2]) ** 0.5
     return exact, each * 1.001 + 1e-30, 4 * off + step.square().sum((-2, -1), keepdim=True).sqrt() + 1e-30
@@ -122,6 +141,22 @@ def test_stacks(count, rows, cols):
 def test_more_matrices_than_a_group_holds():
     x = matrices(8, 70, 512, 1024, dtype=BF16)          # 64 of them are 2^25 elements
     agrees(call(x, torch.empty_like(x)), x)
+
+
+@pytest.mark.parametrize("rows,cols,count", [(200, 240, 1), (130, 700, 3), (700, 130, 2), (513, 1100, 1), (1100, 513, 1), (1290, 1290, 1), (640, 640, 7),
+                                             (2100, 300, 1), (65, 6000, 1)])
+def test_steps_in_groups_and_split_products(rows, cols, count):
+    for rank in (None, 20):
+        x = matrices(rows + cols, count, rows, cols, rank=rank)
+        for dtype in (F16, F32):
+            agrees(call(x, torch.empty(x.shape, device="cuda", dtype=dtype)), x)
+
+
+@pytest.mark.parametrize("coefs", [((2.0, -1.5, 0.5),) * 7, ((3.9, -5.9, 2.5), (3.4, -4.6, 1.9)), ((20.0, -30.0, 12.0), (0.15, 0.0, 0.0), (1.5, -0.5, 0.0)),
+                                   ((3.4445, -4.7750, 2.0315),) * 4, ((1.0, 0.0, 0.0),) * 3, ((-2.0, 1.5, -0.5),) * 5])
+def test_other_polynomials_in_groups(coefs):
+    x = matrices(9, 140, 300)
+    agrees(call(x, torch.empty(140, 300, device="cuda", dtype=F16), coefs=coefs), x, coefs)
 
 
 @pytest.mark.parametrize("rows,cols", [(40, 72), (72, 40), (129, 131)])
@@ -232,7 +267,7 @@ def check_step(ctx, rank, unit, begin, rows, cols, count, s, lr=0.02, beta=0.9, 
     m = b * before["momentum"][part] + g
     assert torch.equal(s["momentum"][part], m)
     u = (g + b * m if nesterov else m).view(count, rows, cols)
-    exact, each, _ = allowed(u, F32)
+    exact, each, _ = allowed(u, F16)        # steps in groups, as for a 16-bit result
     old = before["master"][part].double()
     want = old * (1 - lr * weight_decay) - lr * scale * exact.reshape(-1)
     # three roundings: of master times decay, of rate times update, of the difference; constants are within half a step

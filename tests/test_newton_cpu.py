@@ -51,9 +51,9 @@ def test_nothing_to_orthogonalize():
 
 
 def test_workspaces():
-    # X twice and the two inner matrices, 4 bytes an element
-    assert z.zsmr_orthogonalize_workspace(4096, 4096) >= 4 * 4 * 4096 ** 2
-    assert z.zsmr_orthogonalize_workspace(4096, 4096) < 4.1 * 4 * 4096 ** 2
+    # X twice and two inner matrices, 4 bytes an element; three more inner matrices where steps go in groups
+    assert 0 <= z.zsmr_orthogonalize_workspace(4096, 4096) - 4 * 4 * 4096 ** 2 < 1e5
+    assert 0 <= z.zsmr_orthogonalize_workspace(4096, 8192) - (4 + 5) * 4 * 4096 ** 2 < 1e5
     assert z.zsmr_orthogonalize_workspace(300, 150, 7) == z.zsmr_orthogonalize_workspace(150, 300, 7) == z.zero_muon_workspace(150, 300, 7) > 0
     assert z.zsmr_orthogonalize_workspace(128, 128, 1000) == 0      # in a CU's LDS
     # a group's matrices at a time
@@ -171,26 +171,49 @@ PLAN = r"""
 #define CHECK(c) do { if (!(c)) { std::printf("CHECK failed line %d: %s\n", __LINE__, #c); std::exit(1); } } while (0)
 using namespace zsmr;
 
+static void grids(const NsShape& s, int64_t products) {
+    for (int kind : {N_INNER, N_UPDATE, N_LAST})
+        for (int64_t steps : {s.mp / 32, s.np / 32}) {
+            const NsGrid g = ns_grid(s, kind, products, steps);
+            CHECK((int64_t)g.p_tiles * 128 >= (kind == N_INNER ? s.m : s.n) && (int64_t)g.q_tiles * 128 >= s.m);
+            CHECK(g.tiles == (kind == N_INNER ? (int64_t)g.q_tiles * (g.q_tiles + 1) / 2 : (int64_t)g.p_tiles * g.q_tiles));
+            int64_t at = 0;
+            for (int i = 0; i < g.parts; ++i) {
+                const NsPart& p = g.part[i];
+                CHECK(p.first == at && p.count > 0 && p.form >= NS_WIDE && p.form <= NS_THIN);
+                CHECK(ns_groups(p) * 512 < (int64_t(1) << 32) && p.first + p.count <= INT32_MAX / 4);
+                at += p.count;
+            }
+            CHECK(g.parts >= 1 && g.parts <= 2 && at == (int64_t)g.tiles * products);
+        }
+}
+
 static void shape(int64_t rows, int64_t cols, int64_t count) {
-    const NsShape s = ns_shape(rows, cols, count);
-    CHECK(s.m <= s.n && s.m * s.n == rows * cols && s.tall == (rows > cols));
-    CHECK(s.mp >= s.m && s.mp % 32 == 0 && s.np >= s.n && s.np % 32 == 0);
-    CHECK(s.group >= 1 && s.group <= count && s.parts >= 1);
-    CHECK(s.group == 1 || s.group * s.m * s.n <= kNsGroupElems);
-    const NsSpace w = ns_space(s);
-    if (s.small) {      // a form that holds it
-        CHECK(s.m <= (s.small == 3 ? 128 : 64) && s.n <= (s.small == 1 ? 64 : s.small == 2 ? 256 : 128) && w.bytes == 0);
-        return;
+    for (int fp32 = 0; fp32 < 2; ++fp32) {
+        const NsShape s = ns_shape(rows, cols, count, fp32);
+        CHECK(s.m <= s.n && s.m * s.n == rows * cols && s.tall == (rows > cols));
+        CHECK(s.mp >= s.m && s.mp % 32 == 0 && s.np >= s.n && s.np % 32 == 0);
+        CHECK(s.group >= 1 && s.group <= count && s.parts >= 1);
+        CHECK(s.group == 1 || s.group * s.m * s.n <= kNsGroupElems);
+        const NsSpace w = ns_space(s);
+        if (s.small) {      // a form that holds it
+            CHECK(s.m <= (s.small == 3 ? 128 : 64) && s.n <= (s.small == 1 ? 64 : s.small == 2 ? 256 : 128) && w.bytes == 0);
+            continue;
+        }
+        int64_t end = 0;
+        for (int i = 0; i < kNsMatrices; ++i) {
+            const bool x = i == M_X0 || i == M_X1, used = x || i == M_A || i == M_Q0 || s.grouped;
+            CHECK(w.matrix[i] >= end && w.matrix[i] % 256 == 0);
+            end = w.matrix[i] + (used ? s.group * s.m * (x ? s.np : s.mp) * 4 : 0);
+        }
+        CHECK(w.partial >= end && w.partial % 256 == 0 && w.inverse >= w.partial + s.group * s.parts * 8 && w.bytes >= w.inverse + s.group * 8);
+        // work items of a launch, byte offsets within an operand's tile
+        CHECK(s.group * s.parts < (int64_t(1) << 24) && s.group * ((s.m + 63) / 64) * ((s.np + 63) / 64) * 256 < (int64_t(1) << 32));
+        CHECK(256 * s.np * 4 < (int64_t(1) << 31));
+        grids(s, 1);
+        grids(s, s.group);
+        grids(s, 2 * s.group);
     }
-    CHECK(w.x[1] - w.x[0] >= s.group * s.m * s.np * 4 && w.a - w.x[1] >= s.group * s.m * s.np * 4);
-    CHECK(w.x[1] - w.x[0] >= s.group * s.m * s.n * 4);      // the fp32 update
-    CHECK(w.b - w.a >= s.group * s.m * s.mp * 4 && w.partial - w.b >= s.group * s.m * s.mp * 4);
-    CHECK(w.bytes >= w.inverse + s.group * 8 && w.inverse - w.partial >= s.group * s.parts * 8);
-    for (int64_t at : {w.x[1], w.a, w.b, w.partial, w.inverse}) CHECK(at % 256 == 0);
-    // work items of a launch, byte offsets within an operand's tile
-    CHECK(s.group * s.parts < (int64_t(1) << 24) && s.group * ((s.m + 63) / 64) * ((s.np + 63) / 64) * 256 < (int64_t(1) << 32));
-    CHECK(s.group * ns_largest_grid(s) * kNsThreads < (int64_t(1) << 32));
-    CHECK(256 * s.np * 4 < (int64_t(1) << 31));
 }
 
 static void scores(int64_t tokens, int64_t vocab, int64_t top) {
@@ -229,6 +252,42 @@ static void scales(const double (*coef)[3], int steps) {
     }
 }
 
+// A list of products on one singular value: every matrix is a number.
+static void lists(const double (*coef)[3], int steps) {
+    NsPass pass[ZSMR_MAX_NS_STEPS];
+    double first = 0;
+    CHECK(ns_passes(coef, steps, pass, &first));
+    for (int grouped = 0; grouped < 2; ++grouped) {
+        NsOp ops[kNsMaxOps + 1];
+        const int n = ns_ops(coef, steps, grouped, ops);
+        CHECK(n > 0 && n <= kNsMaxOps && (grouped || n == 3 * steps) && ops[n - 1].kind == N_LAST);
+        for (int k = 0; k <= 1000; ++k) {
+            const double s = k / 1000.0;
+            double v[kNsMatrices], want = s;
+            bool has[kNsMatrices] = {true};
+            v[M_X0] = s * first;
+            for (int i = 0; i < n; ++i) {
+                const NsOp& o = ops[i];
+                CHECK(has[o.p] && has[o.q] && (o.old < 0 || has[o.old]) && (o.old2 < 0 || has[o.old2]));
+                // nothing is written that the launch reads
+                CHECK(o.dst != o.p && o.dst != o.q && o.dst != o.old && o.dst != o.old2);
+                if (o.paired) {
+                    const NsOp& t = ops[i + 1];
+                    CHECK(!t.paired && t.kind == N_INNER && t.dst != o.dst && t.dst != o.p && t.dst != o.q && t.dst != o.old && t.dst != o.old2);
+                    CHECK(o.dst != t.p && o.dst != t.q && o.dst != t.old && o.dst != t.old2);
+                    CHECK((o.p == M_X0 || o.p == M_X1) == (t.p == M_X0 || t.p == M_X1));
+                }
+                const double r = o.mul * v[o.p] * v[o.q] + (o.old < 0 ? 0 : o.old_mul * v[o.old]) + (o.old2 < 0 ? 0 : o.old2_mul * v[o.old2]);
+                CHECK(std::fabs(r) <= 32900);
+                v[o.dst] = r;
+                has[o.dst] = true;
+            }
+            for (int i = 0; i < steps; ++i) want *= coef[i][0] + want * want * (coef[i][1] + want * want * coef[i][2]);
+            CHECK(std::fabs(v[ops[n - 1].dst] - want) <= 2e-4 * (1 + std::fabs(want)));
+        }
+    }
+}
+
 int main() {
     for (int64_t r : {1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 700, 767, 1003, 1024, 1600, 2048, 4096, 6400, 14336, 65536, 262144})
         for (int64_t c : {1, 5, 32, 64, 100, 128, 129, 192, 193, 320, 1000, 1600, 2049, 4096, 5000, 14336, 32768, 262144})
@@ -245,6 +304,20 @@ int main() {
     scales(line, 2);
     scales(none, 2);
     scales(odd, 4);
+    const double soft[16][3] = {{2, -1.5, 0.5}, {2, -1.5, 0.5}, {2, -1.5, 0.5}, {2, -1.5, 0.5}, {1.875, -1.25, 0.375}, {1.875, -1.25, 0.375}, {1.875, -1.25, 0.375},
+                                {1.5, -0.5, 0}, {1.5, -0.5, 0}, {1.5, -0.5, 0}, {1.5, -0.5, 0}, {1.5, -0.5, 0}, {1.5, -0.5, 0}, {1.5, -0.5, 0}, {1.5, -0.5, 0}, {1.5, -0.5, 0}};
+    const double steep[4][3] = {{20, -30, 12}, {15, -20, 6}, {3, -3, 1}, {2, -1.5, 0.5}};
+    lists(quintic, 5);
+    lists(cubic, 3);
+    lists(none, 2);
+    lists(odd, 4);
+    lists(soft, 16);
+    lists(steep, 1);
+    lists(steep + 2, 2);
+    for (int steps = 1; steps <= 5; ++steps) lists(quintic, steps);
+    NsOp ops[kNsMaxOps];
+    CHECK(ns_ops(quintic, 5, true, ops) == 18 && ns_group_steps(true, true, quintic, 5, 1.0) == 3 && ns_group_steps(true, false, quintic, 2, 1.2) == 2);
+    CHECK(ns_group_steps(true, true, steep, 4, 1.0) == 1 && ns_group_steps(false, true, quintic, 5, 1.0) == 1);
     std::printf("plans passed\n");
     return 0;
 }

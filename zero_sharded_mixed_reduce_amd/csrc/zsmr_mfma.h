@@ -36,6 +36,12 @@ __device__ __forceinline__ u32x2 read_transposed(const char* __restrict__ p) {
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p)));
 }
 
+// The same for 16 bytes as they lie there.
+template <typename = void>
+__device__ __forceinline__ u32x4 read_lds16(const char* __restrict__ p) {
+    return *reinterpret_cast<const u32x4*>(p);
+}
+
 // Spread a block's LDS reads and loads evenly among its matrix instructions.
 template <int READS, int LOADS, int MFMA>
 __device__ __forceinline__ void interleave() {

@@ -37,7 +37,6 @@ namespace zsmr {
 namespace {
 
 constexpr int kThreads = kNsThreads, kWaves = kThreads / 64;
-constexpr int T = kNsTile;
 
 // ---------------------------------------------------------------- split fp16 --
 struct Split8 {
@@ -91,12 +90,13 @@ struct Operand {
 
     __device__ __forceinline__ static int swizzle(int k) { return ((k & 3) | ((k >> 3 & 1) << 2)) << 1; }
 
-    // at: the tile's first row of the product; k0: first k, a multiple of 32
-    __device__ __forceinline__ void init(const Mat& m, int64_t at, int64_t k0) {
+    // at: the tile's first row of the product; k0: first k, a multiple of 32; every:
+    // steps of 32 k to its next one; thread: of the WAVES
+    __device__ __forceinline__ void init(const Mat& m, int64_t at, int64_t k0, int every, int thread) {
         const int64_t row_bytes = m.ld * 2;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int idx = i * (WAVES * 64) + (int)threadIdx.x;
+            const int idx = i * (WAVES * 64) + thread;
             if constexpr (OUTER) {
                 const int k = idx / (R / 4), chunk = idx % (R / 4) ^ swizzle(k);
                 off[i] = at * 4 + chunk * 16 < row_bytes ? (uint32_t)(k * row_bytes + chunk * 16) : 0x80000000u;
@@ -109,17 +109,17 @@ struct Operand {
         if constexpr (OUTER) {
             base = p + k0 * row_bytes + at * 4;
             left = (m.rows - k0) * row_bytes - at * 4;
-            step = kNsStep * row_bytes;
+            step = every * kNsStep * row_bytes;
         } else {
             base = p + at * row_bytes + k0 * 4;
             left = (m.rows - at) * row_bytes - k0 * 4;
-            step = kNsStep * 4;
+            step = every * kNsStep * 4;
         }
     }
     // Start the loads of one step into `to` and move on; `on` false: the same
     // instructions, which read nothing and write zeros.
     __device__ __forceinline__ void load(char* to, bool on) {
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64) % WAVES;
         const int bound = !on || left < 0 ? 0 : left > 0x7fffffff ? 0x7fffffff : (int)left;
         const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, bound, 0x00027000);
 #pragma unroll
@@ -145,23 +145,27 @@ struct Operand {
             return r;
         } else {
             const int row = at + lane % 16;
-            return *reinterpret_cast<const u32x4*>(t + row * 128 + ((part * 4 + lane / 16) ^ (row & 7)) * 16);
+            return read_lds16(t + row * 128 + ((part * 4 + lane / 16) ^ (row & 7)) * 16);
         }
     }
 };
 
 // ------------------------------------------------------------------- product --
-enum : int { N_GRAM, N_SQUARE, N_UPDATE, N_LAST };
-
-// D[p, q] = sum_k P[p, k] Q[q, k] for each matrix of the group; a result's row is q.
-struct NsProduct {
-    Mat p, q;                       // of the first matrix
-    int64_t p_batch, q_batch;       // 16-bit values from matrix to matrix
-    int32_t steps, p_tiles, q_tiles, tiles, count;
-    float old_mul, mul;             // result = old_mul * old + mul * D
-    const uint16_t* old;            // of the result's shape and layout
+// One of the products of a launch: D[p, q] = sum_k P[p, k] Q[q, k] for each matrix of
+// the group; a result's row is q.
+struct NsSide {
+    const uint16_t *p, *q, *old, *old2;     // of the first matrix; old of the result's shape and layout
     uint16_t* dst;
-    int64_t ld, batch, rows, cols;  // of the result: ld of old and dst in 16-bit values
+    float mul, old_mul, old2_mul;
+};
+struct NsProduct {
+    NsSide side[2];
+    int32_t p_tiles, q_tiles, tiles;    // of 128 x 128, of a product and a matrix
+    int32_t first_tile, quarters;   // of the launch; a workgroup takes a quarter of a tile
+    int32_t count, steps;           // matrices; steps of 32 k
+    int64_t p_rows, p_ld, p_batch;  // rows; 16-bit values from row to row, from matrix to matrix
+    int64_t q_rows, q_ld, q_batch;
+    int64_t rows, cols, ld, batch;  // of the result and the old matrices
     // N_LAST
     int64_t first;                  // the group's first matrix
     int32_t tall, apply, dtype;     // dtype: of out, or of p16
@@ -221,63 +225,122 @@ __device__ __forceinline__ int triangle_row(int i) {
     return r;
 }
 
-template <int EPI>
-__global__ __launch_bounds__(kThreads, 2) void ns_product_kernel(NsProduct p) {
-#if defined(__HIP_DEVICE_COMPILE__)     // the scheduling hints have no host form
-    constexpr bool kSymmetric = EPI == N_GRAM || EPI == N_SQUARE, kOuter = !kSymmetric;
-    constexpr int WP = 2, TP = T / WP / 16, TQ = T / (kWaves / WP) / 16, STAGES = 2;
-    typedef Operand<T, kOuter, kWaves> P;
-    typedef Operand<T, false, kWaves> Q;
-    constexpr int kStage = P::kBytes + Q::kBytes;
-    __shared__ __attribute__((aligned(1024))) char smem[STAGES * kStage];
-    static_assert(STAGES * kStage >= T * T * 4, "the results leave through the same LDS");
-
-    // Consecutive workgroups go to the eight XCDs in turn; each XCD takes a
-    // contiguous run of tiles, in groups of 8 rows of tiles, so that the tiles it
-    // works on at a time share operands in its L2.
-    const int all = p.tiles * p.count, xcd = blockIdx.x % 8, each = all / 8, rem = all % 8;
-    int tile = xcd * each + min(xcd, rem) + (int)blockIdx.x / 8;
-    const int matrix = tile / p.tiles;
-    tile -= matrix * p.tiles;
+// A workgroup's tile of a launch, in tiles of its own size.
+struct Unit {
+    int side, matrix, tp, tq;
+};
+// Consecutive workgroups go to the eight XCDs in turn; each XCD takes a contiguous
+// run of tiles, in groups of 8 rows of tiles, so that the tiles it works on at a time
+// share operands in its L2.
+template <bool SYMMETRIC>
+__device__ __forceinline__ Unit unit_of(const NsProduct& p) {
+    const int all = gridDim.x, xcd = blockIdx.x % 8, each = all / 8, rem = all % 8;
+    const int at = xcd * each + min(xcd, rem) + (int)blockIdx.x / 8;
+    int tile = p.first_tile + (p.quarters ? at / 4 : at);
+    Unit u;
+    u.side = tile >= p.tiles * p.count;
+    tile -= u.side * p.tiles * p.count;
+    u.matrix = tile / p.tiles;
+    tile -= u.matrix * p.tiles;
     constexpr int kGroup = 8;
-    int tp, tq;
-    if constexpr (kSymmetric) {
+    if constexpr (SYMMETRIC) {
         // rows tp of tiles, tq <= tp
         const int first = triangle_row(tile) / kGroup * kGroup, height = min(kGroup, p.p_tiles - first);
         tile -= first * (first + 1) / 2;
         if (tile < first * height) {
-            tp = first + tile % height;
-            tq = tile / height;
+            u.tp = first + tile % height;
+            u.tq = tile / height;
         } else {
             tile -= first * height;
             int column = 0;
             while (tile >= height - column) tile -= height - column++;
-            tq = first + column;
-            tp = tq + tile;
+            u.tq = first + column;
+            u.tp = u.tq + tile;
         }
     } else {
-        const int group = tile / (kGroup * p.q_tiles), in_group = tile - group * kGroup * p.q_tiles;
-        const int height = min(kGroup, p.p_tiles - group * kGroup);
-        tp = group * kGroup + in_group % height;
-        tq = in_group / height;
+        const int band = tile / (kGroup * p.q_tiles), in_band = tile - band * kGroup * p.q_tiles;
+        const int height = min(kGroup, p.p_tiles - band * kGroup);
+        u.tp = band * kGroup + in_band % height;
+        u.tq = in_band / height;
     }
+    if (p.quarters) {
+        u.tp = u.tp * 2 + (at & 1);
+        u.tq = u.tq * 2 + (at >> 1 & 1);
+    }
+    return u;
+}
 
+// The results' other terms at eight elements: old_mul * old + old2_mul * old2.
+struct OldTerms {
+    u16x8 h[4];
+    __device__ __forceinline__ void load(const NsSide& side, int64_t at) {
+        if (side.old) {
+            h[0] = *reinterpret_cast<const u16x8*>(side.old + at);
+            h[1] = *reinterpret_cast<const u16x8*>(side.old + at + 32);
+        }
+        if (side.old2) {
+            h[2] = *reinterpret_cast<const u16x8*>(side.old2 + at);
+            h[3] = *reinterpret_cast<const u16x8*>(side.old2 + at + 32);
+        }
+    }
+    __device__ __forceinline__ f32x8 added(const NsSide& side, f32x8 d) const {
+        d *= side.mul;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (side.old) d[i] = (widen16<ZSMR_FP16>(h[0][i]) + widen16<ZSMR_FP16>(h[1][i])) * side.old_mul + d[i];
+            if (side.old2) d[i] = (widen16<ZSMR_FP16>(h[2][i]) + widen16<ZSMR_FP16>(h[3][i])) * side.old2_mul + d[i];
+        }
+        return d;
+    }
+};
+
+// A tile of T x T by GROUPS of four waves, each with STAGES of LDS, which take the
+// steps in turn and add up their sums in the end.
+template <int KIND, int T, int GROUPS, int STAGES>
+__global__ __launch_bounds__(kThreads * GROUPS, GROUPS == 1 ? 2 : GROUPS) void ns_product_kernel(NsProduct p) {
+#if defined(__HIP_DEVICE_COMPILE__)     // the scheduling hints have no host form
+    constexpr bool kSymmetric = KIND == N_INNER, kOuter = !kSymmetric;
+    constexpr int WP = 2, TP = T / WP / 16, TQ = T / (kWaves / WP) / 16;
+    typedef Operand<T, kOuter, kWaves> P;
+    typedef Operand<T, false, kWaves> Q;
+    constexpr int kStage = P::kBytes + Q::kBytes;
+    // The only LDS variable: beside another one the compiler waits for every load
+    // that writes LDS before each read of it.
+    __shared__ __attribute__((aligned(1024))) char smem[GROUPS * STAGES * kStage];
+    static_assert(STAGES * kStage >= T * T * 4, "the results leave through the same LDS");
+
+    const Unit unit = unit_of<kSymmetric>(p);
+    const NsSide& side = p.side[unit.side];
+    const int matrix = unit.matrix, tp = unit.tp, tq = unit.tq;
+    // quarters past the matrix or above the diagonal
+    if (T == 64 && ((int64_t)tp * T >= p.cols || (int64_t)tq * T >= p.rows || (kSymmetric && tq > tp))) return;
+
+    const int thread = threadIdx.x % kThreads, group = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
+    // steps of this group, and of all: one past the group's last multiplies zeros
+    const int own_steps = (p.steps - group + GROUPS - 1) / GROUPS, steps = (p.steps + GROUPS - 1) / GROUPS;
+    char* const lds = smem + group * (STAGES * kStage);
     P op;
     Q oq;
-    op.init(Mat{p.p.p + matrix * p.p_batch, p.p.ld, p.p.rows, p.p.cols}, (int64_t)tp * T, 0);
-    oq.init(Mat{p.q.p + matrix * p.q_batch, p.q.ld, p.q.rows, p.q.cols}, (int64_t)tq * T, 0);
+    op.init(Mat{side.p + matrix * p.p_batch, p.p_ld, p.p_rows, p.p_ld}, (int64_t)tp * T, group * kNsStep, GROUPS, thread);
+    oq.init(Mat{side.q + matrix * p.q_batch, p.q_ld, p.q_rows, p.q_ld}, (int64_t)tq * T, group * kNsStep, GROUPS, thread);
 
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, wp = wave % WP, wq = wave / WP;
+    const int lane = threadIdx.x % 64, wave = thread / 64, wp = wave % WP, wq = wave / WP;
     f32x4 acc[TP][TQ];
 #pragma unroll
     for (int i = 0; i < TP; ++i)
 #pragma unroll
         for (int j = 0; j < TQ; ++j) acc[i][j] = 0.f;
 
-    // Two stages of LDS.  A step multiplies hi hi while it reads the lo parts, then
-    // waits for the next stage and lets this one be filled again, and multiplies
-    // lo hi and hi lo while it reads the next stage's hi parts into the other set
-    // of registers.
+    const int64_t p0 = (int64_t)tp * T, q0 = (int64_t)tq * T, padded = p.ld / 2;
+    // where a thread has one group of eight results, what is added to them comes early
+    constexpr bool kEarly = T * T / 8 == kThreads * GROUPS;
+    OldTerms old;
+    if (kEarly && q0 + (int)threadIdx.x / (T / 8) < p.rows && p0 + (int)threadIdx.x % (T / 8) * 8 < padded)
+        old.load(side, matrix * p.batch + split_at(q0 + threadIdx.x / (T / 8), p0 + threadIdx.x % (T / 8) * 8, p.ld));
+
+    // A step multiplies hi hi while it reads the lo parts, then waits for the next
+    // stage and lets this one be filled again, and multiplies lo hi and hi lo while it
+    // reads the next stage's hi parts into the other set of registers.
     constexpr int kReads = TP * (kOuter ? 2 : 1) + TQ, kMfma = TP * TQ, kLoads = P::kLoads + Q::kLoads;
     u32x4 ph[2][TP], qh[2][TQ], pl[TP], ql[TQ];
     auto read = [&](u32x4* a, u32x4* b, const char* stage, int part) {
@@ -292,62 +355,82 @@ __global__ __launch_bounds__(kThreads, 2) void ns_product_kernel(NsProduct p) {
 #pragma unroll
             for (int j = 0; j < TQ; ++j) acc[i][j] = mfma<ZSMR_FP16>(a[i], b[j], acc[i][j]);
     };
-    char* const stage0 = smem;
-    char* const stage1 = smem + kStage;
-    op.load(stage0, true);
-    oq.load(stage0 + P::kBytes, true);
-    op.load(stage1, p.steps > 1);
-    oq.load(stage1 + P::kBytes, p.steps > 1);
-    ZSMR_WAIT(kLoads);
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) {
+        op.load(lds + i * kStage, i < own_steps);
+        oq.load(lds + i * kStage + P::kBytes, i < own_steps);
+    }
+    ZSMR_WAIT((STAGES - 1) * kLoads);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    read(ph[0], qh[0], stage0, 0);
+    read(ph[0], qh[0], lds, 0);
     auto step = [&](int s, char* cur, const char* next, u32x4* p0, u32x4* q0, u32x4* p1, u32x4* q1) {
         read(pl, ql, cur, 1);
         multiply(p0, q0);
         interleave<kReads, 0, kMfma>();
-        ZSMR_WAIT(0);
+        ZSMR_WAIT((STAGES - 2) * kLoads);
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        op.load(cur, s + STAGES < p.steps);
-        oq.load(cur + P::kBytes, s + STAGES < p.steps);
+        op.load(cur, s + STAGES < own_steps);
+        oq.load(cur + P::kBytes, s + STAGES < own_steps);
         read(p1, q1, next, 0);
         multiply(pl, q0);
         multiply(p0, ql);
-        interleave<kReads, kLoads, 2 * kMfma>();
+        // the reads first: the next step begins with them
+        interleave<kReads, 0, kMfma>();
+        interleave<0, kLoads, kMfma>();
+        asm volatile("" ::: "memory");      // the reads do not move on to the next step
     };
-    for (int s = 0; s < p.steps; s += 2) {
-        step(s, stage0, stage1, ph[0], qh[0], ph[1], qh[1]);
-        if (s + 1 == p.steps) break;
-        step(s + 1, stage1, stage0, ph[1], qh[1], ph[0], qh[0]);
+    static_assert(STAGES % 2 == 0, "the sets of registers alternate");
+    for (int s = 0; s < steps; s += STAGES) {
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i) {
+            step(s + i, lds + i * kStage, lds + (i + 1) % STAGES * kStage, ph[i % 2], qh[i % 2], ph[1 - i % 2], qh[1 - i % 2]);
+            if (s + i + 1 == steps) break;
+        }
     }
     ZSMR_WAIT(0);           // no load may still be on its way to this LDS
     __syncthreads();
 
+    if constexpr (GROUPS > 1) {
+        f32x4* const from = reinterpret_cast<f32x4*>(smem) + thread;
+        if (group > 0) {
+#pragma unroll
+            for (int i = 0; i < TP; ++i)
+#pragma unroll
+                for (int j = 0; j < TQ; ++j) from[((group - 1) * TP * TQ + i * TQ + j) * kThreads] = acc[i][j];
+        }
+        __syncthreads();
+        if (group == 0) {
+#pragma unroll
+            for (int g = 0; g < GROUPS - 1; ++g)
+#pragma unroll
+                for (int i = 0; i < TP; ++i)
+#pragma unroll
+                    for (int j = 0; j < TQ; ++j) acc[i][j] += from[(g * TP * TQ + i * TQ + j) * kThreads];
+        }
+        __syncthreads();
+    }
     // acc[i][j][r] is D at p = 16 i + 4 (lane / 16) + r, q = 16 j + lane % 16 of the
     // wave's part.  Results leave through LDS as [q][p] in fp32, the 16-byte chunk c
     // of row q in slot c ^ f(q): rows are then read along p, columns along q, each
     // with few bank conflicts.
     float* const out = reinterpret_cast<float*>(smem);
-    auto at = [&](int q, int c) { return q * T + (c ^ ((q ^ q >> 3) & 31)) * 4; };
+    auto at = [&](int q, int c) { return q * T + (c ^ ((q ^ q >> 3) & (T / 4 - 1) & 31)) * 4; };
 #pragma unroll
     for (int j = 0; j < TQ; ++j)
 #pragma unroll
         for (int i = 0; i < TP; ++i)
-            *reinterpret_cast<f32x4*>(out + at((wq * TQ + j) * 16 + lane % 16, (wp * TP + i) * 4 + lane / 16)) = acc[i][j];
+            if (group == 0) *reinterpret_cast<f32x4*>(out + at((wq * TQ + j) * 16 + lane % 16, (wp * TP + i) * 4 + lane / 16)) = acc[i][j];
     __syncthreads();
-    const int64_t p0 = (int64_t)tp * T, q0 = (int64_t)tq * T;
-    const uint16_t* old = p.old + matrix * p.batch;
-    uint16_t* dst = p.dst + matrix * p.batch;
-    const int64_t padded = p.ld / 2;
-    auto finish = [&](int64_t row, int64_t col, f32x8 d) {
-        if constexpr (EPI == N_GRAM) return d * p.mul;
-        else return load_split(old, split_at(row, col, p.ld)) * p.old_mul + d * p.mul;
-    };
-    // rows q of the result
-    for (int k = threadIdx.x; k < T * T / 8; k += kThreads) {
+    uint16_t* const dst = side.dst + matrix * p.batch;
+    // the other side of a symmetric result, or a tall matrix, is written along q
+    const bool turned = kSymmetric ? tp != tq : KIND == N_LAST && p.tall;
+    for (int k = threadIdx.x; k < T * T / 8; k += kThreads * GROUPS) {
         const int q = k / (T / 8), c = k % (T / 8);
         if (q0 + q >= p.rows || p0 + c * 8 >= padded) continue;
+        const int64_t e = split_at(q0 + q, p0 + c * 8, p.ld);
+        if (!kEarly) old.load(side, matrix * p.batch + e);
         f32x4* const lo = reinterpret_cast<f32x4*>(out + at(q, 2 * c));
         f32x4* const hi = reinterpret_cast<f32x4*>(out + at(q, 2 * c + 1));
         f32x8 d;
@@ -356,31 +439,31 @@ __global__ __launch_bounds__(kThreads, 2) void ns_product_kernel(NsProduct p) {
             d[i] = (*lo)[i];
             d[4 + i] = (*hi)[i];
         }
-        d = finish(q0 + q, p0 + c * 8, d);
-        if constexpr (EPI != N_LAST) {
-            store_split(dst, split_at(q0 + q, p0 + c * 8, p.ld), d);
-        } else if (p.tall) {
+        d = old.added(side, d);
+        if constexpr (KIND != N_LAST) store_split(dst, e, d);
+        else if (!p.tall) put_result(p, p.first + matrix, q0 + q, p0 + c * 8, (int)min((int64_t)8, p.cols - p0 - c * 8), d);
+        if (turned) {
+            f32x4 a, b;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                (*lo)[i] = d[i];
-                (*hi)[i] = d[4 + i];
+                a[i] = d[i];
+                b[i] = d[4 + i];
             }
-        } else {
-            put_result(p, p.first + matrix, q0 + q, p0 + c * 8, (int)min((int64_t)8, p.cols - p0 - c * 8), d);
+            *lo = a;
+            *hi = b;
         }
     }
-    // rows p: the other side of a symmetric result, or a tall matrix
-    if (kSymmetric ? tp == tq : EPI != N_LAST || !p.tall) return;
+    if (!turned) return;
     __syncthreads();
-    for (int k = threadIdx.x; k < T * T / 8; k += kThreads) {
+    for (int k = threadIdx.x; k < T * T / 8; k += kThreads * GROUPS) {
         const int row = k / (T / 8), q = k % (T / 8) * 8;
         const int64_t limit = kSymmetric ? p.rows : p.cols;
         if (p0 + row >= limit || q0 + q >= (kSymmetric ? padded : p.rows)) continue;
         f32x8 d;
 #pragma unroll
         for (int i = 0; i < 8; ++i) d[i] = out[at(q + i, row / 4) + row % 4];
-        if constexpr (EPI == N_LAST) put_result(p, p.first + matrix, p0 + row, q0 + q, (int)min((int64_t)8, p.rows - q0 - q), d);
-        else store_split(dst, split_at(p0 + row, q0 + q, p.ld), finish(p0 + row, q0 + q, d));
+        if constexpr (KIND == N_LAST) put_result(p, p.first + matrix, p0 + row, q0 + q, (int)min((int64_t)8, p.rows - q0 - q), d);
+        else store_split(dst, split_at(p0 + row, q0 + q, p.ld), d);
     }
 #endif
 }
@@ -892,19 +975,33 @@ hipError_t launch_small(const NewtonArgs& a, hipStream_t stream) {
 }
 
 struct Space {
-    uint16_t *x[2], *a, *b;
+    uint16_t* matrix[kNsMatrices];
     double *partial, *inverse;
 };
 Space space_of(const NsShape& s, void* ws) {
     const NsSpace w = ns_space(s);
     char* p = static_cast<char*>(ws);
     Space r;
-    for (int i = 0; i < 2; ++i) r.x[i] = reinterpret_cast<uint16_t*>(p + w.x[i]);
-    r.a = reinterpret_cast<uint16_t*>(p + w.a);
-    r.b = reinterpret_cast<uint16_t*>(p + w.b);
+    for (int i = 0; i < kNsMatrices; ++i) r.matrix[i] = reinterpret_cast<uint16_t*>(p + w.matrix[i]);
     r.partial = reinterpret_cast<double*>(p + w.partial);
     r.inverse = reinterpret_cast<double*>(p + w.inverse);
     return r;
+}
+
+template <int KIND>
+void launch_product(NsProduct& p, const NsGrid& grid, hipStream_t stream) {
+    p.p_tiles = grid.p_tiles;
+    p.q_tiles = grid.q_tiles;
+    p.tiles = grid.tiles;
+    for (int i = 0; i < grid.parts; ++i) {
+        const NsPart& part = grid.part[i];
+        const unsigned groups = (unsigned)ns_groups(part);
+        p.first_tile = (int32_t)part.first;
+        p.quarters = part.form == NS_THIN;
+        if (part.form == NS_WIDE) ns_product_kernel<KIND, 128, 1, 2><<<groups, kThreads, 0, stream>>>(p);
+        else if (part.form == NS_DEEP) ns_product_kernel<KIND, 128, 2, 2><<<groups, kThreads * 2, 0, stream>>>(p);
+        else ns_product_kernel<KIND, 64, 2, 4><<<groups, kThreads * 2, 0, stream>>>(p);
+    }
 }
 
 template <typename F>
@@ -915,8 +1012,8 @@ void of_dtype(int32_t dtype, F each) {
 }
 
 // From the partial sums on, for `count` matrices from the `first` one on.
-void passes(const NewtonArgs& a, const Space& w, const void* x, int32_t dtype, int64_t stride, int64_t batch, int64_t first, int count,
-            hipStream_t stream) {
+void products(const NewtonArgs& a, const NsOp* ops, int n_ops, const Space& w, const void* x, int32_t dtype, int64_t stride, int64_t batch,
+              int64_t first, int count, hipStream_t stream) {
     const NsShape& s = a.shape;
     ns_norm_kernel<<<count, 64, 0, stream>>>(w.partial, s.parts, a.eps, a.first, w.inverse);
     PackArgs pack{};
@@ -927,7 +1024,7 @@ void passes(const NewtonArgs& a, const Space& w, const void* x, int32_t dtype, i
     pack.n = s.n;
     pack.np = s.np;
     pack.inverse = w.inverse;
-    pack.dst = w.x[0];
+    pack.dst = w.matrix[M_X0];
     pack.tiles_n = (int32_t)((s.np + 63) / 64);
     pack.tiles = (int32_t)((s.m + 63) / 64) * pack.tiles_n;
     pack.tall = s.tall;
@@ -945,53 +1042,42 @@ void passes(const NewtonArgs& a, const Space& w, const void* x, int32_t dtype, i
     p.master = a.step.master;
     p.decay = a.decay;
     p.rate = a.rate;
-    const int64_t xb = s.m * s.np * 2, ab = s.m * s.mp * 2;
-    for (int i = 0; i < a.steps; ++i) {
-        const NsPass& pass = a.pass[i];
-        uint16_t *from = w.x[i % 2], *to = w.x[1 - i % 2];
-        const Mat mx{from, s.np * 2, s.m, s.np * 2}, ma{w.a, s.mp * 2, s.m, s.mp * 2}, mb{w.b, s.mp * 2, s.m, s.mp * 2};
-        p.p_tiles = p.q_tiles = (int32_t)s.m_tiles;
-        p.tiles = (int32_t)(s.m_tiles * (s.m_tiles + 1) / 2);
-        p.rows = p.cols = s.m;
-        p.ld = s.mp * 2;
-        p.batch = ab;
-        // A
-        p.p = p.q = mx;
-        p.p_batch = p.q_batch = xb;
-        p.steps = (int32_t)(s.np / kNsStep);
-        p.dst = w.a;
-        p.mul = pass.a_mul;
-        ns_product_kernel<N_GRAM><<<p.tiles * count, kThreads, 0, stream>>>(p);
-        // B
-        p.p = p.q = ma;
-        p.p_batch = p.q_batch = ab;
-        p.steps = (int32_t)(s.mp / kNsStep);
-        p.old = w.a;
-        p.dst = w.b;
-        p.old_mul = pass.b_old;
-        p.mul = pass.b_mul;
-        ns_product_kernel<N_SQUARE><<<p.tiles * count, kThreads, 0, stream>>>(p);
-        // X': columns of X are the product's p, rows of B its q
-        p.p = mx;
-        p.p_batch = xb;
-        p.q = mb;
-        p.p_tiles = (int32_t)s.n_tiles;
-        p.tiles = (int32_t)(s.n_tiles * s.m_tiles);
-        p.cols = s.n;
-        p.ld = s.np * 2;
-        p.batch = xb;
-        p.old = from;
-        p.dst = to;
-        p.old_mul = pass.x_old;
-        p.mul = pass.x_mul;
-        if (i + 1 < a.steps) ns_product_kernel<N_UPDATE><<<p.tiles * count, kThreads, 0, stream>>>(p);
-        else ns_product_kernel<N_LAST><<<p.tiles * count, kThreads, 0, stream>>>(p);
+    for (int i = 0; i < n_ops; ++i) {
+        int sides = 0;
+        const NsOp& o = ops[i];
+        for (;; ++i) {
+            const NsOp& op = ops[i];
+            NsSide& side = p.side[sides++];
+            side.p = w.matrix[op.p];
+            side.q = w.matrix[op.q];
+            side.old = op.old < 0 ? nullptr : w.matrix[op.old];
+            side.old2 = op.old2 < 0 ? nullptr : w.matrix[op.old2];
+            side.dst = w.matrix[op.dst];
+            side.mul = op.mul;
+            side.old_mul = op.old_mul;
+            side.old2_mul = op.old2_mul;
+            if (!op.paired) break;
+        }
+        const bool from_x = o.p == M_X0 || o.p == M_X1, gram = from_x && o.kind == N_INNER;
+        p.p_rows = p.q_rows = p.rows = s.m;
+        p.p_ld = (from_x ? s.np : s.mp) * 2;
+        p.q_ld = (gram ? s.np : s.mp) * 2;
+        p.cols = o.kind == N_INNER ? s.m : s.n;
+        p.ld = (o.kind == N_INNER ? s.mp : s.np) * 2;
+        p.p_batch = s.m * p.p_ld;
+        p.q_batch = s.m * p.q_ld;
+        p.batch = s.m * p.ld;
+        p.steps = (int32_t)((gram ? s.np : s.mp) / kNsStep);
+        const NsGrid grid = ns_grid(s, o.kind, (int64_t)sides * count, p.steps);
+        if (o.kind == N_INNER) launch_product<N_INNER>(p, grid, stream);
+        else if (o.kind == N_UPDATE) launch_product<N_UPDATE>(p, grid, stream);
+        else launch_product<N_LAST>(p, grid, stream);
     }
 }
 
 }  // namespace
 
-hipError_t launch_orthogonalize(const NewtonArgs& a, void* ws, hipStream_t stream) {
+hipError_t launch_orthogonalize(const NewtonArgs& a, const NsOp* ops, int n_ops, void* ws, hipStream_t stream) {
     const NsShape& s = a.shape;
     if (s.small) return launch_small(a, stream);
     const Space w = space_of(s, ws);
@@ -1005,17 +1091,17 @@ hipError_t launch_orthogonalize(const NewtonArgs& a, void* ws, hipStream_t strea
             ns_sumsq_kernel<decltype(dt)::value><<<dim3(s.parts, count), kThreads, 0, stream>>>(x, a.x_stride, a.x_batch, rows, cols,
                                                                                                row_threads, w.partial);
         });
-        passes(a, w, x, a.x_dtype, a.x_stride, a.x_batch, first, count, stream);
+        products(a, ops, n_ops, w, x, a.x_dtype, a.x_stride, a.x_batch, first, count, stream);
     }
     return hipGetLastError();
 }
 
-hipError_t launch_muon(const NewtonArgs& a, void* ws, hipStream_t stream) {
+hipError_t launch_muon(const NewtonArgs& a, const NsOp* ops, int n_ops, void* ws, hipStream_t stream) {
     const NsShape& s = a.shape;
     if (s.small) return launch_small(a, stream);
     const Space w = space_of(s, ws);
     const int64_t each = s.m * s.n, cols = s.tall ? s.m : s.n;
-    float* const u = reinterpret_cast<float*>(w.x[1]);
+    float* const u = reinterpret_cast<float*>(w.matrix[M_X1]);
     for (int64_t first = 0; first < s.count; first += s.group) {
         const int count = (int)std::min(s.group, s.count - first);
         MomentumArgs m{};
@@ -1029,7 +1115,7 @@ hipError_t launch_muon(const NewtonArgs& a, void* ws, hipStream_t stream) {
         m.partial = w.partial;
         if (a.grad_dtype == ZSMR_BF16) ns_momentum_kernel<ZSMR_BF16><<<dim3(s.parts, count), kThreads, 0, stream>>>(m);
         else ns_momentum_kernel<ZSMR_FP16><<<dim3(s.parts, count), kThreads, 0, stream>>>(m);
-        passes(a, w, u, ZSMR_FP32, cols, each, first, count, stream);
+        products(a, ops, n_ops, w, u, ZSMR_FP32, cols, each, first, count, stream);
     }
     return hipGetLastError();
 }

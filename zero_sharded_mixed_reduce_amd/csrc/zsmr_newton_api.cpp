@@ -2,6 +2,7 @@
 // include/zsmr_ops.h: every argument is checked here, then the launches of
 // zsmr_newton_launch.h go to the caller's stream.  No device memory is allocated
 // and nothing is kept between calls.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -46,7 +47,9 @@ extern "C" {
 
 int64_t zsmr_orthogonalize_workspace(int64_t rows, int64_t cols, int64_t count) {
     if (check_matrices(rows, cols, count)) return -1;
-    return count ? ns_space(ns_shape(rows, cols, count)).bytes : 0;
+    if (count == 0) return 0;
+    // of any result's format
+    return std::max(ns_space(ns_shape(rows, cols, count, false)).bytes, ns_space(ns_shape(rows, cols, count, true)).bytes);
 }
 
 int32_t zsmr_orthogonalize(const void* x, int32_t x_dtype, int64_t x_stride, int64_t x_batch, void* out, int32_t out_dtype,
@@ -58,7 +61,7 @@ int32_t zsmr_orthogonalize(const void* x, int32_t x_dtype, int64_t x_stride, int
     if (count == 0) return ZSMR_OK;
     if ((st = check_strided(x, x_dtype, x_stride, x_batch, rows, cols, count, false))) return st;
     if ((st = check_strided(out, out_dtype, out_stride, out_batch, rows, cols, count, true))) return st;
-    a.shape = ns_shape(rows, cols, count);
+    a.shape = ns_shape(rows, cols, count, out_dtype == ZSMR_FP32);
     if ((st = check_space(ws, ws_bytes, ns_space(a.shape).bytes))) return st;
     a.x = x;
     a.x_stride = x_stride;
@@ -68,7 +71,8 @@ int32_t zsmr_orthogonalize(const void* x, int32_t x_dtype, int64_t x_stride, int
     a.out_stride = out_stride;
     a.out_batch = out_batch;
     a.out_dtype = out_dtype;
-    return done(launch_orthogonalize(a, ws, stream));
+    NsOp ops[kNsMaxOps];
+    return done(launch_orthogonalize(a, ops, ns_ops(ns->coef, ns->steps, a.shape.grouped, ops), ws, stream));
 }
 
 int32_t zero_muon_step(zsmr_ctx* c, int32_t rank, int32_t unit, int64_t begin, int64_t rows, int64_t cols, int64_t count,
@@ -90,7 +94,7 @@ int32_t zero_muon_step(zsmr_ctx* c, int32_t rank, int32_t unit, int64_t begin, i
     if ((st = check_grads(c, grads, row_stride, base, len))) return st;
     if (!master || !momentum || !p16_dst) return ZSMR_ERR_ARG;
     if (!al(master, 4) || !al(momentum, 4) || !al(p16_dst, 2)) return ZSMR_ERR_ALIGN;
-    a.shape = ns_shape(rows, cols, count);
+    a.shape = ns_shape(rows, cols, count, false);
     if ((st = check_space(ws, ws_bytes, ns_space(a.shape).bytes))) return st;
     a.step.grads = static_cast<const uint16_t*>(grads) + base + begin;
     a.step.row_stride = row_stride;
@@ -105,7 +109,8 @@ int32_t zero_muon_step(zsmr_ctx* c, int32_t rank, int32_t unit, int64_t begin, i
     a.beta = (float)hp->beta;
     a.decay = (float)(1.0 - hp->lr * hp->weight_decay);
     a.rate = (float)(hp->lr * hp->scale);
-    const hipError_t e = launch_muon(a, ws, stream);
+    NsOp ops[kNsMaxOps];
+    const hipError_t e = launch_muon(a, ops, ns_ops(ns->coef, ns->steps, a.shape.grouped, ops), ws, stream);
     if (e != hipSuccess) return hip_fail(e);
     count_reduce(c, rank, total);
     count_cast(c, rank, total);

@@ -11,7 +11,7 @@ namespace zsmr {
 
 struct NewtonArgs {
     NsShape shape;
-    NsPass pass[ZSMR_MAX_NS_STEPS];
+    NsPass pass[ZSMR_MAX_NS_STEPS];     // of a matrix that stays in LDS
     int32_t steps;
     double eps, first;                  // first: the power of two of the first X
     // the matrices, in their own orientation (orthogonalise)
@@ -26,7 +26,8 @@ struct NewtonArgs {
     int32_t grad_dtype, param_dtype, nesterov;
     float beta, decay, rate;            // decay: 1 - lr * weight_decay; rate: lr * scale
 };
-hipError_t launch_orthogonalize(const NewtonArgs& a, void* ws, hipStream_t stream);
-hipError_t launch_muon(const NewtonArgs& a, void* ws, hipStream_t stream);
+// ops: the products, of matrices that do not
+hipError_t launch_orthogonalize(const NewtonArgs& a, const NsOp* ops, int n_ops, void* ws, hipStream_t stream);
+hipError_t launch_muon(const NewtonArgs& a, const NsOp* ops, int n_ops, void* ws, hipStream_t stream);
 
 }  // namespace zsmr
