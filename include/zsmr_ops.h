@@ -240,12 +240,12 @@ int32_t zero_muon_step(zsmr_ctx* ctx, int32_t rank, int32_t unit, int64_t begin,
  * ZSMR_FP32, stride elements apart.  With z = scale * logit, in fp32,
  *   lse = log sum_v exp z_v,  logprob = z_id - lse,  p_v = exp(z_v - lse),
  *   entropy = -sum_v p_v log p_v.
- * Logits of -infinity are masked: p = 0.  So are values of z below -3.0e38, which
+ * Logits of -infinity are masked: p = 0.  So are values of z below -2.3e38, which
  * the lowest values of bf16 and fp32 are.  A row with nothing else has lse
  * -infinity, entropy 0, logprob -infinity and a gradient of zeros.  A NaN makes a
  * row's lse, logprob, entropy and gradient NaN.  An id outside [0, vocab) is
  * padding: logprob 0, which has no gradient; entropy and alternatives are the
- * row's.  scale: finite, > 0. */
+ * row's.  scale: 2^-100 .. 2^100. */
 #define ZSMR_MAX_TOP 64
 
 /* Bytes of workspace, or -1 for sizes the call refuses. */

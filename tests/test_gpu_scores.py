@@ -29,7 +29,7 @@ def reference(x, ids, scale):
     """In 64 bits: values, and the probabilities."""
     s = torch.tensor(scale, dtype=F32).double().item()
     v = x.double() * s
-    v = torch.where(v < -3.0e38, -INF, v)
+    v = torch.where(v < -2.3e38, -INF, v)
     top = v.amax(1, keepdim=True)
     none = top[:, 0] == -INF
     e = torch.where(none[:, None], 0.0, (v - top).exp())
@@ -48,7 +48,7 @@ def reference(x, ids, scale):
 def bound(x, scale):
     """Of lse, logprob and entropy of each row."""
     v = x.double() * scale
-    top = torch.where(torch.isfinite(v) & (v > -3.0e38), v, 0.0).abs().amax(1)
+    top = torch.where(torch.isfinite(v) & (v > -2.3e38), v, 0.0).abs().amax(1)
     return 2.0 ** -24 * (x.shape[1] / 256 + 2 * (4 * top + 100) + 30)
 
 

@@ -99,7 +99,7 @@ LOGPROBS = dict(logits=A, stride=100, dtype=F32, ids=B, id_bytes=8, n=5, vocab=1
 GRAD = dict(logits=A, stride=100, dtype=F32, ids=B, id_bytes=8, n=5, vocab=100, scale=1.0, lse=C, entropy=C, g=C, h=C, dlogits=D, ds=100, stream=None)
 COMMON = [(dict(logits=None), ARG), (dict(stride=99), ARG), (dict(stride=(1 << 21) + 1), ARG), (dict(dtype=0), DTYPE), (dict(dtype=4), DTYPE),
           (dict(ids=None), ARG), (dict(id_bytes=2), ARG), (dict(n=-1), ARG), (dict(n=(1 << 24) + 1), ARG), (dict(vocab=0), ARG),
-          (dict(vocab=(1 << 21) + 1), ARG), (dict(scale=0.0), ARG), (dict(scale=-1.0), ARG), (dict(scale=NAN), ARG), (dict(scale=INF), ARG),
+          (dict(vocab=(1 << 21) + 1), ARG), (dict(scale=0.0), ARG), (dict(scale=-1.0), ARG), (dict(scale=NAN), ARG), (dict(scale=INF), ARG), (dict(scale=1e31), ARG), (dict(scale=1e-31), ARG),
           (dict(logits=A + 2), ALIGN), (dict(ids=B + 4), ALIGN), (dict(lse=C + 2), ALIGN), (dict(entropy=C + 1), ALIGN)]
 
 

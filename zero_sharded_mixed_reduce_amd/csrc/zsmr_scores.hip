@@ -22,22 +22,25 @@
 namespace zsmr {
 namespace {
 
-constexpr int kWaves = kScoreWaves, kThreads = kWaves * 64;
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.69314718f;
-constexpr float kFloor = -3.0e38f;
+constexpr float kEdge = 2.3e38f * kLog2e;
 
 // ---------------------------------------------------------------- statistics --
-// A part of a softmax: sums of e = exp(z - ref) and of e * log2 e; ref is finite.
+// Logits are taken times scale * log2 e, so that e^z is a power of two of one fused
+// multiply-add: d = x c - ref.  A part of a softmax is its reference (finite), the sum
+// of 2^d and the sum of 2^d d.  A reference follows the largest logit only when a lane's
+// eight powers pass 2^10: their sizes cost no accuracy, and no maximum has to be taken.
 struct Stats {
     float ref, sum, mean;
 };
-__device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d); }
-// A part relative to another reference, not below its own by much.
+__device__ __forceinline__ float power_of(float d) { return __builtin_amdgcn_exp2f(d); }
+__device__ __forceinline__ float log2_of(float x) { return __builtin_amdgcn_logf(x); }
+__device__ __forceinline__ float fused(float a, float b, float c) { return __builtin_fmaf(a, b, c); }
 __device__ __forceinline__ Stats moved(Stats a, float ref) {
     // a part without a sum (no logit above -infinity) has any reference
     if (a.sum == 0.f) return Stats{ref, 0.f, 0.f};
-    const float d = (a.ref - ref) * kLog2e, f = exp_of(d);
-    return Stats{ref, a.sum * f, f == 0.f ? 0.f : f * (a.mean + d * a.sum)};
+    const float d = a.ref - ref, f = power_of(d);
+    return Stats{ref, a.sum * f, f == 0.f ? 0.f : f * fused(d, a.sum, a.mean)};
 }
 __device__ __forceinline__ Stats join_stats(Stats a, Stats b) {
     const float ref = a.sum == 0.f ? b.ref : b.sum == 0.f ? a.ref : fmaxf(a.ref, b.ref);
@@ -45,8 +48,37 @@ __device__ __forceinline__ Stats join_stats(Stats a, Stats b) {
     b = moved(b, ref);
     return Stats{ref, a.sum + b.sum, a.mean + b.mean};
 }
-__device__ __forceinline__ Stats shuffled(Stats a, int d) {
-    return Stats{__shfl_xor(a.ref, d), __shfl_xor(a.sum, d), __shfl_xor(a.mean, d)};
+// Eight logits of a lane.
+__device__ __forceinline__ void add_powers(const f32x8& x, float c, float ref, float* sum, float* mean) {
+    float s = 0.f, m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float d = fused(x[i], c, -ref), e = power_of(d);
+        s += e;
+        m = fused(e, fmaxf(d, -200.f), m);      // 0 times -infinity is 0
+    }
+    *sum = s;
+    *mean = m;
+}
+__device__ __forceinline__ float largest(const f32x8& x) {
+    float top = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i]);
+    return top;
+}
+__device__ __forceinline__ float reference(float top, float c) { return __builtin_amdgcn_fmed3f(top * c, -kEdge, kEdge); }
+__device__ __forceinline__ void add_logits(Stats& s, const f32x8& x, float c) {
+    float sum, mean;
+    add_powers(x, c, s.ref, &sum, &mean);
+    if (sum > 1024.f) {
+        const float ref = reference(largest(x), c);
+        if (ref > s.ref) {
+            s = moved(s, ref);
+            add_powers(x, c, s.ref, &sum, &mean);
+        }
+    }
+    s.sum += sum;
+    s.mean += mean;
 }
 
 // ----------------------------------------------------------- top alternatives --
@@ -60,11 +92,40 @@ __device__ __forceinline__ float value_of(uint32_t o) {
     return __uint_as_float(o ^ (o >> 31 ? 0x80000000u : 0xffffffffu));
 }
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t index) { return (uint64_t)order_of(x) << 32 | (0xffffffffu - index); }
-__device__ __forceinline__ uint64_t shuffled(uint64_t k, int d) {
-    return (uint64_t)(uint32_t)__shfl_xor((int)(k >> 32), d) << 32 | (uint32_t)__shfl_xor((int)k, d);
+// The value of the lane whose number differs in bits D, by moves between lanes.
+template <int D>
+__device__ __forceinline__ uint32_t across(uint32_t x) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const int lane = threadIdx.x % 64;
+    if constexpr (D == 1) return __builtin_amdgcn_update_dpp(x, x, 0xb1, 0xf, 0xf, true);          // quad_perm 1 0 3 2
+    if constexpr (D == 2) return __builtin_amdgcn_update_dpp(x, x, 0x4e, 0xf, 0xf, true);          // quad_perm 2 3 0 1
+    if constexpr (D == 3) return __builtin_amdgcn_update_dpp(x, x, 0x1b, 0xf, 0xf, true);          // quad_perm 3 2 1 0
+    if constexpr (D == 7) return __builtin_amdgcn_update_dpp(x, x, 0x141, 0xf, 0xf, true);         // row_half_mirror
+    if constexpr (D == 4) return across<3>(across<7>(x));
+    if constexpr (D == 8) return __builtin_amdgcn_update_dpp(x, x, 0x128, 0xf, 0xf, true);         // row_ror 8
+    if constexpr (D == 15) return __builtin_amdgcn_update_dpp(x, x, 0x140, 0xf, 0xf, true);        // row_mirror
+    if constexpr (D == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+        return lane & 16 ? r[0] : r[1];
+    }
+    if constexpr (D == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        return lane & 32 ? r[0] : r[1];
+    }
+    if constexpr (D == 63) return across<32>(across<16>(across<15>(x)));
+#endif
+    return x;
+}
+template <int D>
+__device__ __forceinline__ uint64_t across(uint64_t k) {
+    return (uint64_t)across<D>((uint32_t)(k >> 32)) << 32 | across<D>((uint32_t)k);
+}
+template <int D>
+__device__ __forceinline__ float across(float x) {
+    return __uint_as_float(across<D>(__float_as_uint(x)));
 }
 __device__ __forceinline__ uint64_t lane_key(uint64_t k, int lane) {
-    return (uint64_t)(uint32_t)__shfl((int)(k >> 32), lane) << 32 | (uint32_t)__shfl((int)k, lane);
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(k >> 32), lane) << 32 | (uint32_t)__builtin_amdgcn_readlane((int)k, lane);
 }
 // LDS that the lanes of one wave exchange: its operations are in order, the
 // compiler has to keep them so.
@@ -72,178 +133,292 @@ __device__ __forceinline__ void wave_order() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
 }
-// One key a lane, largest first.
-__device__ __forceinline__ uint64_t merge_step(uint64_t k, int d, bool larger) {
-    const uint64_t o = shuffled(k, d);
-    return (k > o) == larger ? k : o;
-}
-__device__ __forceinline__ uint64_t sort64(uint64_t k) {
+// One key a lane, largest first: bitonic.
+template <int N, int D, typename K>
+__device__ __forceinline__ K sort_steps(K k) {
     const int lane = threadIdx.x % 64;
-#pragma unroll
-    for (int n = 2; n <= 64; n *= 2)
-#pragma unroll
-        for (int d = n / 2; d > 0; d /= 2) k = merge_step(k, d, ((lane & d) == 0) == ((lane & n) == 0));
-    return k;
+    const K o = across<D>(k);
+    k = (k > o) == (((lane & D) == 0) == ((lane & N) == 0)) ? k : o;
+    if constexpr (D > 1) return sort_steps<N, D / 2>(k);
+    else return k;
+}
+template <typename K>
+__device__ __forceinline__ K sort64(K k) {
+    k = sort_steps<2, 1>(k);
+    k = sort_steps<4, 2>(k);
+    k = sort_steps<8, 4>(k);
+    k = sort_steps<16, 8>(k);
+    k = sort_steps<32, 16>(k);
+    return sort_steps<64, 32>(k);
 }
 // The 64 largest of two sorted lists, sorted.
 __device__ __forceinline__ uint64_t merge64(uint64_t a, uint64_t b) {
-    const int lane = threadIdx.x % 64;
-    b = lane_key(b, 63 - lane);
-    uint64_t k = a > b ? a : b;
-#pragma unroll
-    for (int d = 32; d > 0; d /= 2) k = merge_step(k, d, (lane & d) == 0);
-    return k;
+    b = across<63>(b);
+    return sort_steps<64, 32>(a > b ? a : b);
+}
+// The largest of a group of `lanes` (a power of two up to 8) lanes.
+template <int D = 1>
+__device__ __forceinline__ float largest_of(float x, int lanes) {
+    if (D < lanes) x = fmaxf(x, across<D>(x));
+    if constexpr (D < 4) return largest_of<D * 2>(x, lanes);
+    else return x;
+}
+template <int D>
+__device__ __forceinline__ Stats joined(Stats s) {
+    s = join_stats(s, Stats{across<D>(s.ref), across<D>(s.sum), across<D>(s.mean)});
+    if constexpr (D < 32) return joined<D * 2>(s);
+    else return s;
 }
 
 // ------------------------------------------------------------------- forward --
 struct ForwardArgs {
     ScoreArgs a;
+    float c;                    // scale * log2 e
     int64_t segment;
     int32_t splits;
     float4* stats;              // [token][split], or NULL: the results themselves
     uint64_t* keys;             // [token][split][top]
 };
 
-__device__ __forceinline__ void put_token(const ScoreArgs& a, int64_t t, Stats s) {
-    const float log_sum = __builtin_amdgcn_logf(s.sum) * kLn2;
+__device__ __forceinline__ void put_token(const ForwardArgs& f, int64_t t, Stats s) {
+    const ScoreArgs& a = f.a;
+    const float log_sum = log2_of(s.sum);
     const bool none = s.sum == 0.f;
-    if (a.lse) a.lse[t] = none ? -INFINITY : s.ref + log_sum;
-    if (a.entropy) a.entropy[t] = none ? 0.f : log_sum - s.mean / s.sum * kLn2;
+    if (a.lse) a.lse[t] = none ? -INFINITY : (s.ref + log_sum) * kLn2;
+    if (a.entropy) a.entropy[t] = none ? 0.f : (log_sum - s.mean / s.sum) * kLn2;
     if (a.logprob) {
         const int32_t id = token_at(a.ids, a.id_bytes, t, a.vocab);
         float r = 0.f;
         if (id >= 0) {
             const int64_t e = t * a.stride + id;
             const float x = a.dtype == ZSMR_BF16 ? load1<ZSMR_BF16>(a.logits, e) : a.dtype == ZSMR_FP16 ? load1<ZSMR_FP16>(a.logits, e) : load1<ZSMR_FP32>(a.logits, e);
-            r = none ? -INFINITY : x * a.scale - s.ref - log_sum;
+            r = none ? -INFINITY : (fused(x, f.c, -s.ref) - log_sum) * kLn2;
         }
         a.logprob[t] = r;
     }
 }
-__device__ __forceinline__ void put_top(const ScoreArgs& a, int64_t t, Stats s, uint64_t key) {
+__device__ __forceinline__ void put_top(const ForwardArgs& f, int64_t t, Stats s, uint64_t key) {
+    const ScoreArgs& a = f.a;
     const int lane = threadIdx.x % 64;
     if (lane >= a.top) return;
     const int64_t e = t * a.top + lane;
-    const float log_sum = __builtin_amdgcn_logf(s.sum) * kLn2;
     const int32_t id = key ? (int32_t)(0xffffffffu - (uint32_t)key) : -1;
     if (a.top_ids) {
         if (a.top_bytes == 8) static_cast<int64_t*>(a.top_ids)[e] = id;
         else static_cast<int32_t*>(a.top_ids)[e] = id;
     }
-    if (a.top_logprobs) a.top_logprobs[e] = key ? value_of((uint32_t)(key >> 32)) * a.scale - s.ref - log_sum : -INFINITY;
+    if (a.top_logprobs)
+        a.top_logprobs[e] = key ? (fused(value_of((uint32_t)(key >> 32)), f.c, -s.ref) - log2_of(s.sum)) * kLn2 : -INFINITY;
 }
 
-template <int DT, bool TOP>
-__global__ __launch_bounds__(kThreads) void scores_kernel(ForwardArgs f) {
+// A wave's block of 512 logits, eight a lane: 16 bytes a lane and load, which covers a
+// contiguous KB.
+template <int DT>
+struct Block {
+    u32x4 raw[DT == ZSMR_FP32 ? 2 : 1];
+    __device__ __forceinline__ static int index(int i) {        // of the lane's i-th, in the block
+        const int lane = threadIdx.x % 64;
+        return DT == ZSMR_FP32 ? i / 4 * 256 + lane * 4 + i % 4 : lane * 8 + i;
+    }
+    __device__ __forceinline__ void load(const void* p, int64_t e) {
+        const int lane = threadIdx.x % 64;
+        if constexpr (DT == ZSMR_FP32) {
+            const float* q = static_cast<const float*>(p) + e + lane * 4;
+            raw[0] = __builtin_bit_cast(u32x4, *reinterpret_cast<const f32x4_any*>(q));
+            raw[1] = __builtin_bit_cast(u32x4, *reinterpret_cast<const f32x4_any*>(q + 256));
+        } else {
+            raw[0] = __builtin_bit_cast(u32x4, *reinterpret_cast<const u16x8_any*>(static_cast<const uint16_t*>(p) + e + lane * 8));
+        }
+    }
+    __device__ __forceinline__ f32x8 values() const {
+        f32x8 x;
+        if constexpr (DT == ZSMR_FP32) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(raw[i / 4][i % 4]);
+        } else {
+            const u16x8 h = __builtin_bit_cast(u16x8, raw[0]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = widen16<DT>(h[i]);
+        }
+        return x;
+    }
+};
+
+template <int DT, bool TOP, int kWaves>
+__global__ __launch_bounds__(kWaves * 64, 8) void scores_kernel(ForwardArgs f) {
     const ScoreArgs& a = f.a;
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int64_t t = blockIdx.x / f.splits;
     const int split = blockIdx.x % f.splits;
     const int64_t first = split * f.segment, end = first + f.segment < a.vocab ? first + f.segment : a.vocab;
+    // Top alternatives.  A wave stages the logits above a bound, sorts them into its best
+    // when enough have come, and shares the bound that follows with the other waves of
+    // the row: what is below the top-th best of any of them is none of the row's.  The
+    // order in which bounds arrive decides what is staged in vain, not what is found.
     constexpr int kStaged = TOP ? 64 + kScoreBlock : 1;
     __shared__ uint64_t staged[kWaves][kStaged];
-    __shared__ uint64_t best[kWaves][64];
+    __shared__ uint32_t shared_bound, counts[kWaves];
+    __shared__ uint32_t groups[64];
     __shared__ Stats part[kWaves];
 
-    Stats s{kFloor, 0.f, 0.f};
-    bool begun = false;
-    uint64_t keys = 0;
+    Stats s{-kEdge, 0.f, 0.f};
+    bool sorted = false;
+    uint64_t keys = 0;                  // the wave's best, sorted
     float above = -INFINITY;            // a logit has to be above it to be among the best
     int count = 0;
+    const int enough = a.top > 32 ? 64 : a.top > 8 ? 2 * a.top : 16;
+    // the value below which a logit is not above one of order o: the next one below it, and
+    // below +0 one that is not -0, which equals it
+    auto below = [](uint32_t o) { return o - (o == 0x80000000u ? 2 : 1); };
+    auto share = [&](uint32_t o) {
+        if (lane == 0) atomicMax(&shared_bound, o);
+    };
     auto flush = [&]() {
         wave_order();
-        const uint64_t k = lane < count ? staged[wave][lane] : 0;
-        keys = merge64(keys, sort64(k));
+        uint64_t k = sort64(lane < count ? staged[wave][lane] : 0);
+        keys = sorted ? merge64(keys, k) : k;
+        sorted = true;
         const int rest = count - 64;
         for (int i = lane; i < rest; i += 64) {         // move the rest up, 64 at a time
-            const uint64_t m = staged[wave][64 + i];
+            k = staged[wave][64 + i];
             wave_order();
-            staged[wave][i] = m;
+            staged[wave][i] = k;
         }
         wave_order();
         count = rest > 0 ? rest : 0;
         const uint64_t last = lane_key(keys, a.top - 1);
-        if (last) above = value_of((uint32_t)(last >> 32));
+        if (last) {
+            // later logits of this wave have larger indices: an equal one is not among the best
+            above = fmaxf(above, value_of((uint32_t)(last >> 32)));
+            share(below((uint32_t)(last >> 32)));
+        }
     };
-    for (int64_t c0 = first + wave * kScoreBlock; c0 < end; c0 += kWaves * kScoreBlock) {
-        const int64_t c = c0 + lane * 8;
-        f32x8 x;
-        if (c + 8 <= end) {
-            x = load8<DT>(a.logits, t * a.stride + c);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = c + i < end ? load1<DT>(a.logits, t * a.stride + c + i) : -INFINITY;
-        }
-        float top = x[0];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i]);
-        if constexpr (TOP) {
-            if (!begun) {
-                // the top-th largest of the lanes' largest is a bound to begin with
-                const uint64_t k = sort64(key_of(top == top ? top : -INFINITY, 0));
-                const uint32_t o = (uint32_t)(lane_key(k, a.top - 1) >> 32);
-                // the next value below it; below +0 that is not -0, which equals it
-                if (o > order_of(-INFINITY)) above = value_of(o - (o == 0x80000000u ? 2 : 1));
-            }
-            if (__any(top > above)) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const bool in = x[i] > above;
-                    const uint64_t mask = __ballot(in);
-                    if (in) staged[wave][count + __popcll(mask & ((1ull << lane) - 1))] = key_of(x[i], (uint32_t)(c + i));
-                    count += __popcll(mask);
-                }
-                while (count >= 64) flush();
-            }
-        }
-        begun = true;
-        // the reference follows the largest logit only when it is far behind: sums
-        // of e up to e^8 lose nothing
-        top *= a.scale;
-        if (s.sum == 0.f ? top > kFloor : top > s.ref + 8.f) {
-            s = moved(s, fminf(top, -kFloor));
-        }
+    auto offer = [&](const f32x8& x, int64_t c0) {
+        const float top = largest(x);
+        if (!__any(top > above)) return;
+        // the row's bound is asked for only where the wave's own is passed
+        wave_order();
+        above = fmaxf(above, value_of(*(volatile uint32_t*)&shared_bound));
+        if (!__any(top > above)) return;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float d = (x[i] * a.scale - s.ref) * kLog2e, e = exp_of(d);
-            s.sum += e;
-            s.mean += e * fmaxf(d, -200.f);
+            const bool in = x[i] > above;
+            const uint64_t mask = __ballot(in);
+            if (mask == 0) continue;
+            if (in) staged[wave][count + __popcll(mask & ((1ull << lane) - 1))] = key_of(x[i], (uint32_t)(c0 + Block<DT>::index(i)));
+            count += __popcll(mask);
         }
+        while (count >= enough) flush();
+    };
+    // whole blocks, the next two on their way
+    const int64_t row = t * a.stride, step = kWaves * kScoreBlock;
+    int64_t c0 = first + wave * kScoreBlock;
+    const bool whole = c0 + kScoreBlock <= end;
+    Block<DT> now, next, after;
+    float top = -INFINITY;
+    if (whole) {
+        now.load(a.logits, row + c0);
+        if (c0 + step + kScoreBlock <= end) next.load(a.logits, row + c0 + step);
+        if (c0 + 2 * step + kScoreBlock <= end) after.load(a.logits, row + c0 + 2 * step);
+        top = largest(now.values());
+        s.ref = reference(top, f.c);
     }
     if constexpr (TOP) {
-        if (count) flush();
-        best[wave][lane] = keys;
+        // A bound to begin with: the top-th largest of the largest of 64 groups of logits,
+        // taken from the waves' first blocks (from all eight waves, where they have one,
+        // groups of 64: for 5 alternatives about 5 of their 4,096 logits are above it, for
+        // 20 24).
+        const int64_t blocks = (end - first) / kScoreBlock;
+        int waves = kWaves;
+        while (waves > 1 && waves > blocks) waves /= 2;
+        const float group = largest_of(top == top ? top : -INFINITY, waves);
+        if (wave < waves && lane % waves == 0) groups[wave * (64 / waves) + lane / waves] = order_of(group);
+        if (threadIdx.x == 0) shared_bound = order_of(-INFINITY);
+        __syncthreads();
+        const uint32_t o = __builtin_amdgcn_readlane(sort64(groups[lane]), a.top - 1);
+        if (o > order_of(-INFINITY)) {
+            above = value_of(below(o));
+            if (wave == 0) share(below(o));
+        }
     }
+    if (whole)
+        for (; c0 + kScoreBlock <= end; c0 += step) {
+            const f32x8 x = now.values();
+            now = next;
+            next = after;
+            if (c0 + 3 * step + kScoreBlock <= end) after.load(a.logits, row + c0 + 3 * step);
+            if constexpr (TOP) offer(x, c0);
+            add_logits(s, x, f.c);
+        }
+    if (c0 < end) {             // the row's last, shorter one
+        f32x8 x;
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) s = join_stats(s, shuffled(s, d));
+        for (int i = 0; i < 8; ++i) {
+            const int64_t c = c0 + Block<DT>::index(i);
+            x[i] = c < end ? load1<DT>(a.logits, row + c) : -INFINITY;
+        }
+        if (!whole) s.ref = reference(largest(x), f.c);
+        if constexpr (TOP) offer(x, c0);
+        add_logits(s, x, f.c);
+    }
+    s = joined<1>(s);
     if (lane == 0) part[wave] = s;
     __syncthreads();
+    if constexpr (TOP) {
+        // what is above the last bound, of the staged and of the best, to the front
+        const uint32_t bound = shared_bound;
+        wave_order();
+        const uint64_t k = lane < count ? staged[wave][lane] : 0;
+        wave_order();
+        count = 0;
+        for (const uint64_t m : {k, keys}) {
+            const bool in = (uint32_t)(m >> 32) > bound;
+            const uint64_t mask = __ballot(in);
+            if (in) staged[wave][count + __popcll(mask & ((1ull << lane) - 1))] = m;
+            count += __popcll(mask);
+        }
+        if (lane == 0) counts[wave] = count;
+        __syncthreads();
+        if (wave) return;
+        // the first wave sorts what all have
+        int all = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) all += counts[w];
+        for (int at = 0; at < all; at += 64) {
+            int w = 0, i = at + lane;
+#pragma unroll
+            for (int n = 0; n < kWaves - 1; ++n)
+                if (w == n && i >= (int)counts[n]) {
+                    i -= (int)counts[n];
+                    ++w;
+                }
+            const uint64_t m = sort64(at + lane < all ? staged[w][i] : 0);
+            keys = at ? merge64(keys, m) : m;
+        }
+        if (!all) keys = 0;
+    }
     if (wave) return;
     s = part[0];
 #pragma unroll
     for (int i = 1; i < kWaves; ++i) s = join_stats(s, part[i]);
-    if constexpr (TOP) {
-#pragma unroll
-        for (int i = 1; i < kWaves; ++i) keys = merge64(keys, best[i][lane]);
-    }
     if (f.stats) {
         if (lane == 0) f.stats[blockIdx.x] = make_float4(s.ref, s.sum, s.mean, 0.f);
         if (TOP && lane < a.top) f.keys[(int64_t)blockIdx.x * a.top + lane] = keys;
     } else {
-        if (lane == 0) put_token(a, t, s);
-        if (TOP) put_top(a, t, s, keys);
+        if (lane == 0) put_token(f, t, s);
+        if (TOP) put_top(f, t, s, keys);
     }
 }
 
-// The segments of a row: each wave joins a share of them, then the waves' parts.
+// The segments of a row: each wave joins a share of them, then pairs of waves.
 constexpr int kJoinWaves = 8;
 template <bool TOP>
 __global__ __launch_bounds__(kJoinWaves * 64) void scores_join_kernel(ForwardArgs f) {
     __shared__ uint64_t best[kJoinWaves][64];
     __shared__ Stats part[kJoinWaves];
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int64_t t = blockIdx.x;
-    Stats s{kFloor, 0.f, 0.f};
+    Stats s{-kEdge, 0.f, 0.f};
     uint64_t keys = 0;
     for (int i = wave; i < f.splits; i += kJoinWaves) {
         const float4 v = f.stats[t * f.splits + i];
@@ -251,49 +426,92 @@ __global__ __launch_bounds__(kJoinWaves * 64) void scores_join_kernel(ForwardArg
         if (TOP) keys = merge64(keys, lane < f.a.top ? f.keys[(t * f.splits + i) * f.a.top + lane] : 0);
     }
     if (lane == 0) part[wave] = s;
-    best[wave][lane] = keys;
-    __syncthreads();
-    if (wave) return;
-    for (int i = 1; i < kJoinWaves; ++i) {
-        s = join_stats(s, part[i]);
-        if (TOP) keys = merge64(keys, best[i][lane]);
+    if (TOP) best[wave][lane] = keys;
+#pragma unroll
+    for (int n = 1; n < kJoinWaves; n *= 2) {
+        __syncthreads();
+        if (TOP && wave % (2 * n) == 0) best[wave][lane] = keys = merge64(keys, best[wave + n][lane]);
     }
-    if (lane == 0) put_token(f.a, t, s);
-    if (TOP) put_top(f.a, t, s, keys);
+    if (wave) return;
+    s = part[0];
+#pragma unroll
+    for (int i = 1; i < kJoinWaves; ++i) s = join_stats(s, part[i]);
+    if (lane == 0) put_token(f, t, s);
+    if (TOP) put_top(f, t, s, keys);
 }
 
 // ------------------------------------------------------------------ gradient --
-constexpr int kGradBlock = 256 * 8;
-template <int DT>
-__global__ __launch_bounds__(256) void scores_grad_kernel(ScoreArgs a, int64_t first_row, int32_t blocks) {
-    const int64_t t = first_row + blockIdx.x / blocks;
-    const int64_t c = (int64_t)(blockIdx.x % blocks) * kGradBlock + threadIdx.x * 8;
-    if (c >= a.vocab) return;
+// A workgroup takes kGradBlock elements of a row; what is the row's own is read once.
+// ds = g' [v = id] - p (g' + h' (log p + H)) with g' = scale g and h' = scale h, log p in
+// the base 2 that the power needs.
+constexpr int kGradThreads = 256, kGradTurns = 4, kGradBlock = kGradThreads * kGradTurns * 8;
+struct GradArgs {
+    ScoreArgs a;
+    float c;                        // scale * log2 e
+    int64_t last_row;               // rows go from the last one up: the forward pass read them last
+    int32_t blocks;                 // of a row
+};
+template <int DT, bool STREAM>
+__global__ __launch_bounds__(kGradThreads) void scores_grad_kernel(GradArgs f) {
+    const ScoreArgs& a = f.a;
+    const int64_t t = f.last_row - blockIdx.x / f.blocks, c0 = (int64_t)(blockIdx.x % f.blocks) * kGradBlock;
     const int32_t id = a.ids && a.dlogprob ? token_at(a.ids, a.id_bytes, t, a.vocab) : -1;
-    const float g = id >= 0 ? a.dlogprob[t] : 0.f, h = a.dentropy ? a.dentropy[t] : 0.f;
-    const float lse = a.lse[t], base = a.dentropy ? g + h * a.entropy[t] : g;
+    const float g = id >= 0 ? a.dlogprob[t] * a.scale : 0.f, h = a.dentropy ? a.dentropy[t] * a.scale : 0.f;
+    const float lse = a.lse[t], ref = lse * kLog2e, slope = h * kLn2, base = a.dentropy ? g + h * a.entropy[t] : g;
     const bool none = lse < -1e30f;     // a row whose logits are all masked
-    auto one = [&](float x, int64_t v) {
-        const float logp = x * a.scale - lse, p = exp_of(logp * kLog2e);
-        float d = p * (base + h * fmaxf(logp, -200.f));
-        d = (v == id ? g : 0.f) - d;
-        return none ? 0.f : d * a.scale;
+    auto one = [&](float x) {
+        // 16-bit logits: the error of lse log2 e, 1.2e-6 of p for an lse of 20, is below their
+        // result's; fp32 ones take the difference first
+        const float d = DT == ZSMR_FP32 ? (x * a.scale - lse) * kLog2e : fused(x, f.c, -ref), p = power_of(d);
+        return -p * fused(slope, fmaxf(d, -200.f), base);
     };
-    const int64_t e = t * a.stride + c, o = t * a.dstride + c;
-    if (c + 8 <= a.vocab) {
-        f32x8 x = load8<DT>(a.logits, e);
+    const int64_t e0 = t * a.stride + c0, o0 = t * a.dstride + c0;
+    const int64_t left = a.vocab - c0;
+    f32x8 x[kGradTurns];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = one(x[i], c + i);
-        store8<DT>(a.dlogits, o, x);
-    } else {
-        for (int64_t i = 0; i < a.vocab - c; ++i) store1<DT>(a.dlogits, o + i, one(load1<DT>(a.logits, e + i), c + i));
+    for (int k = 0; k < kGradTurns; ++k) {
+        const int64_t c = (k * kGradThreads + threadIdx.x) * 8;
+        if (c + 8 <= left) x[k] = load8<DT>(a.logits, e0 + c);
+    }
+#pragma unroll
+    for (int k = 0; k < kGradTurns; ++k) {
+        const int64_t c = (k * kGradThreads + threadIdx.x) * 8;
+        if (c >= left) break;
+        if (c + 8 <= left) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[k][i] = none ? 0.f : one(x[k][i]);
+            const int64_t at = id - c0 - c;
+            if (at >= 0 && at < 8 && !none) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i == at) x[k][i] += g;
+            }
+            if constexpr (STREAM) stream8<DT>(a.dlogits, o0 + c, x[k]);
+            else store8<DT>(a.dlogits, o0 + c, x[k]);
+        } else {
+            for (int64_t i = c; i < left; ++i) {
+                const float d = none ? 0.f : one(load1<DT>(a.logits, e0 + i)) + (c0 + i == id ? g : 0.f);
+                store1<DT>(a.dlogits, o0 + i, d);
+            }
+        }
     }
 }
 
-template <int DT>
+template <int DT, int WAVES>
 void forward(const ForwardArgs& f, int64_t groups, hipStream_t stream) {
-    if (f.a.top) scores_kernel<DT, true><<<(unsigned)groups, kThreads, 0, stream>>>(f);
-    else scores_kernel<DT, false><<<(unsigned)groups, kThreads, 0, stream>>>(f);
+    if (f.a.top) scores_kernel<DT, true, WAVES><<<(unsigned)groups, WAVES * 64, 0, stream>>>(f);
+    else scores_kernel<DT, false, WAVES><<<(unsigned)groups, WAVES * 64, 0, stream>>>(f);
+}
+template <int DT>
+void forward(const ForwardArgs& f, int64_t groups, int waves, hipStream_t stream) {
+    if (waves == 2) forward<DT, 2>(f, groups, stream);
+    else forward<DT, 8>(f, groups, stream);
+}
+
+template <int DT>
+void gradient(const GradArgs& f, unsigned grid, bool stream_out, hipStream_t stream) {
+    if (stream_out) scores_grad_kernel<DT, true><<<grid, kGradThreads, 0, stream>>>(f);
+    else scores_grad_kernel<DT, false><<<grid, kGradThreads, 0, stream>>>(f);
 }
 
 }  // namespace
@@ -304,6 +522,7 @@ hipError_t launch_logprobs(const ScoreArgs& a, void* ws, hipStream_t stream) {
     launch_groups(a.tokens * s.splits, [&](int64_t first, int64_t count) {
         ForwardArgs f{};
         f.a = a;
+        f.c = a.scale * kLog2e;
         f.segment = s.segment;
         f.splits = s.splits;
         if (s.splits > 1) {
@@ -319,9 +538,9 @@ hipError_t launch_logprobs(const ScoreArgs& a, void* ws, hipStream_t stream) {
             if (a.top_ids) f.a.top_ids = static_cast<char*>(a.top_ids) + first * a.top * a.top_bytes;
             if (a.top_logprobs) f.a.top_logprobs += first * a.top;
         }
-        if (a.dtype == ZSMR_BF16) forward<ZSMR_BF16>(f, count, stream);
-        else if (a.dtype == ZSMR_FP16) forward<ZSMR_FP16>(f, count, stream);
-        else forward<ZSMR_FP32>(f, count, stream);
+        if (a.dtype == ZSMR_BF16) forward<ZSMR_BF16>(f, count, s.waves, stream);
+        else if (a.dtype == ZSMR_FP16) forward<ZSMR_FP16>(f, count, s.waves, stream);
+        else forward<ZSMR_FP32>(f, count, s.waves, stream);
         if (s.splits > 1) {
             if (a.top) scores_join_kernel<true><<<(unsigned)a.tokens, kJoinWaves * 64, 0, stream>>>(f);
             else scores_join_kernel<false><<<(unsigned)a.tokens, kJoinWaves * 64, 0, stream>>>(f);
@@ -331,12 +550,18 @@ hipError_t launch_logprobs(const ScoreArgs& a, void* ws, hipStream_t stream) {
 }
 
 hipError_t launch_logprobs_grad(const ScoreArgs& a, hipStream_t stream) {
-    const int64_t blocks = (a.vocab + kGradBlock - 1) / kGradBlock;
-    launch_rows(a.tokens, blocks * 256, [&](int64_t first, int64_t count) {
-        const unsigned grid = (unsigned)(count * blocks);
-        if (a.dtype == ZSMR_BF16) scores_grad_kernel<ZSMR_BF16><<<grid, 256, 0, stream>>>(a, first, (int32_t)blocks);
-        else if (a.dtype == ZSMR_FP16) scores_grad_kernel<ZSMR_FP16><<<grid, 256, 0, stream>>>(a, first, (int32_t)blocks);
-        else scores_grad_kernel<ZSMR_FP32><<<grid, 256, 0, stream>>>(a, first, (int32_t)blocks);
+    GradArgs f{};
+    f.a = a;
+    f.c = a.scale * kLog2e;
+    f.blocks = (int32_t)((a.vocab + kGradBlock - 1) / kGradBlock);
+    // results that the 256 MB Infinity Cache cannot hold beside the logits go past it
+    const bool stream_out = a.tokens * a.vocab * (a.dtype == ZSMR_FP32 ? 8 : 4) > (int64_t(200) << 20);
+    launch_rows(a.tokens, (int64_t)f.blocks * kGradThreads, [&](int64_t first, int64_t count) {
+        const unsigned grid = (unsigned)(count * f.blocks);
+        f.last_row = a.tokens - 1 - first;
+        if (a.dtype == ZSMR_BF16) gradient<ZSMR_BF16>(f, grid, stream_out, stream);
+        else if (a.dtype == ZSMR_FP16) gradient<ZSMR_FP16>(f, grid, stream_out, stream);
+        else gradient<ZSMR_FP32>(f, grid, stream_out, stream);
     });
     return hipGetLastError();
 }

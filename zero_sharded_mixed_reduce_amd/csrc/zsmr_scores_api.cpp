@@ -1,7 +1,6 @@
 // Host side of the scores of logits, declared in include/zsmr_ops.h: every argument
 // is checked here, then the launches of zsmr_scores_launch.h go to the caller's
 // stream.  No device memory is allocated and nothing is kept between calls.
-#include <cmath>
 #include <cstdint>
 
 #include "zsmr_ops_check.h"
@@ -20,7 +19,7 @@ int32_t check_logits(const void* p, int64_t stride, int32_t dtype, int64_t token
     return al(p, dtype == ZSMR_FP32 ? 4 : 2) ? ZSMR_OK : ZSMR_ERR_ALIGN;
 }
 
-bool scale_ok(float scale) { return std::isfinite(scale) && scale > 0; }
+bool scale_ok(float scale) { return scale >= 0x1p-100f && scale <= 0x1p100f; }
 
 bool top_ok(int64_t vocab, int32_t top) { return top >= 0 && top <= ZSMR_MAX_TOP && top <= vocab; }
 
