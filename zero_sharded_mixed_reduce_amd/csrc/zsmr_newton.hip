@@ -723,6 +723,24 @@ __device__ __forceinline__ void store4(void* p, int64_t e, int64_t step, int cou
     for (int i = 0; i < 4; ++i)
         if (i < count) store1<DT>(p, e + i * step, f[i]);
 }
+// Eight contiguous elements, or (not WHOLE) as many as lie before `end` and repeats of
+// the last.  Either way nothing is loaded under a branch, at whose end it would be waited for.
+template <int DT, bool WHOLE>
+__device__ __forceinline__ f32x8 load_row(const void* p, int64_t e, int64_t end) {
+    if constexpr (WHOLE) return load8<DT>(p, e);
+    f32x8 f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = load1<DT>(p, min(e + i, end - 1));
+    return f;
+}
+// The first `count` of eight contiguous elements.
+template <int DT>
+__device__ __forceinline__ void store_some(void* p, int64_t e, int count, f32x8 f) {
+    if (count >= 8) return store8<DT>(p, e, f);
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (i < count) store1<DT>(p, e + i, f[i]);
+}
 template <typename F>
 __device__ __forceinline__ void by_dtype(int32_t dtype, F each) {
     if (dtype == ZSMR_BF16) each(std::integral_constant<int, ZSMR_BF16>());
@@ -730,8 +748,14 @@ __device__ __forceinline__ void by_dtype(int32_t dtype, F each) {
     else each(std::integral_constant<int, ZSMR_FP32>());
 }
 
-// A matrix of at most MP x NP.
-template <int MP, int NP, int WAVES, int FP, int FQ>
+// A matrix of at most MP x NP.  The plain call reads and writes each register's four
+// elements where they lie.  The shard's step (STEP) has nrows + 2 arrays of the matrix's
+// shape to read and three to write, so it takes memory in its own order, eight elements of
+// a row a thread, and the matrix changes hands in LDS, as fp32 rows a little longer than
+// the matrix's: 4 of 128 x 128 with 5 steps take 60.9 us at 4 rows and 64.5 at 16 (61.7
+// and 82 where the elements lie), 4 of 64 x 64 17.3 (19.4), while the plain call for 4 of
+// 128 x 128 would take 52.0 us for 49.1.
+template <int MP, int NP, int WAVES, int FP, int FQ, bool STEP>
 __global__ __launch_bounds__(WAVES * 64) void ns_small_kernel(SmallArgs s) {
 #if defined(__HIP_DEVICE_COMPILE__)
     __shared__ __attribute__((aligned(1024))) char smem[MP * NP * 4 + MP * MP * 4];
@@ -754,83 +778,114 @@ __global__ __launch_bounds__(WAVES * 64) void ns_small_kernel(SmallArgs s) {
     auto place = [&](int id, int i, int j) {
         return Place{id % mb * kRows + j * 16 + lane % 16, id / mb * kCols + i * 16 + lane / 16 * 4};
     };
-    auto tiles = [&](int parts, int limit, auto each) {
+    auto every = [&](auto each) {
 #pragma unroll
-        for (int t = 0; t < PARTS; ++t) {
-            const int id = wave + t * WAVES;
-            if (t >= parts || id >= limit) continue;
+        for (int t = 0; t < PARTS; ++t)
 #pragma unroll
             for (int i = 0; i < FP; ++i)
 #pragma unroll
-                for (int j = 0; j < FQ; ++j) each(t, i, j, place(id, i, j));
-        }
+                for (int j = 0; j < FQ; ++j) each(t, i, j, place(wave + t * WAVES, i, j));
     };
-    // Element (row, col) of the wide orientation, and the step to the next column.
-    const int64_t step = tall ? (a.step.master ? m : a.x_stride) : 1, out_step = tall ? (a.step.master ? m : a.out_stride) : 1;
-    auto at = [&](Place p, int64_t stride, int64_t batch) {
+    // How many of a register's elements, from p on along its row, the matrix has.
+    auto inside = [&](int t, Place p) { return wave + t * WAVES < mb * nb && p.row < m ? n - p.col : 0; };
+    auto element = [&](Place p, int64_t stride, int64_t batch) {
         return matrix * batch + (tall ? p.col * stride + p.row : p.row * stride + p.col);
     };
-    const int64_t own = tall ? m : n, each_matrix = shape.m * shape.n;     // of matrices behind each other
+    constexpr int kChunks = MP * NP / 8 / (WAVES * 64);
+    static_assert(kChunks * 8 * WAVES * 64 == MP * NP, "chunks for every thread");
+    static_assert(sizeof(smem) >= (MP * (NP + 4) > NP * (MP + 4) ? MP * (NP + 4) : NP * (MP + 4)) * 4, "room for the matrix");
+    const int rows = tall ? n : m, cols = tall ? m : n, of_row = (cols + 7) / 8, pitch = (cols + 3) / 4 * 4 + 4;
+    const int64_t each = shape.m * shape.n, at = matrix * each;      // of matrices one behind the other
+    float* const flat = reinterpret_cast<float*>(smem);
+    struct Chunk {
+        int row, col, count, at;        // at: in the matrix, and where count is 0, in it too
+    };
+    auto chunk = [&](int k) {
+        const int id = k * (WAVES * 64) + (int)threadIdx.x, row = id / of_row, col = id % of_row * 8;
+        return Chunk{row, col, row < rows ? min(8, cols - col) : 0, row < rows ? row * cols + col : 0};
+    };
+    auto put_flat = [&](Chunk c, f32x8 f) {
+        // whole groups of four: the row's end has room for them
+        float* const to = flat + c.row * pitch + c.col;
+        if (c.count > 0) *reinterpret_cast<f32x4*>(to) = f32x4{f[0], f[1], f[2], f[3]};
+        if (c.count > 4) *reinterpret_cast<f32x4*>(to + 4) = f32x4{f[4], f[5], f[6], f[7]};
+    };
 
     f32x4 x[PARTS][FP][FQ];
     double sum = 0;
+    if constexpr (STEP) {
+        f32x8 w[kChunks], g[kChunks];
+        auto load = [&](auto dt, auto whole) {
+            constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll
-    for (int t = 0; t < PARTS; ++t)
-#pragma unroll
-        for (int i = 0; i < FP; ++i)
-#pragma unroll
-            for (int j = 0; j < FQ; ++j) x[t][i][j] = 0.f;
-    if (a.step.master) {
-        tiles(PARTS, mb * nb, [&](int t, int i, int j, Place p) {
-            const int count = p.row < m ? n - p.col : 0;
-            if (count <= 0) return;
-            const int64_t e = at(p, own, each_matrix);
-            f32x4 g = -0.0f, w = load4<ZSMR_FP32>(a.step.m, e, step, count);         // -0 + x is x for every x
-            by_dtype(a.grad_dtype, [&](auto dt) {
-#pragma unroll 4
-                for (int r = 0; r < a.step.nrows; ++r) g += load4<decltype(dt)::value>(a.step.grads + r * a.step.row_stride, e, step, count);
-            });
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float next = w[r];
-                const float u = momentum(a.step, a.beta, a.nesterov, g[r], &next);
-                w[r] = next;
-                if (r < count) x[t][i][j][r] = u;
+            for (int k = 0; k < kChunks; ++k) {
+                w[k] = load_row<ZSMR_FP32, kWhole>(a.step.m, at + chunk(k).at, at + each);
+                g[k] = -0.0f;               // -0 + x is x for every x
             }
-            store4<ZSMR_FP32>(a.step.m, e, step, count, w);
+#pragma unroll 2
+            for (int r = 0; r < a.step.nrows; ++r) {
+                f32x8 h[kChunks];
+#pragma unroll
+                for (int k = 0; k < kChunks; ++k)
+                    h[k] = load_row<decltype(dt)::value, kWhole>(a.step.grads + r * a.step.row_stride, at + chunk(k).at, at + each);
+#pragma unroll
+                for (int k = 0; k < kChunks; ++k) g[k] += h[k];
+            }
+        };
+        by_dtype(a.grad_dtype, [&](auto dt) {
+            if (cols % 8 == 0) load(dt, std::true_type());
+            else load(dt, std::false_type());
         });
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
+            const Chunk c = chunk(k);
+            f32x8 u;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float next = w[k][i];
+                u[i] = momentum(a.step, a.beta, a.nesterov, g[k][i], &next);
+                w[k][i] = next;
+                if (i < c.count) sum = __builtin_fma((double)u[i], (double)u[i], sum);
+            }
+            store_some<ZSMR_FP32>(a.step.m, at + c.at, c.count, w[k]);
+            put_flat(c, u);
+        }
     } else {
+        const int64_t step = tall ? a.x_stride : 1;
         by_dtype(a.x_dtype, [&](auto dt) {
-            tiles(PARTS, mb * nb, [&](int t, int i, int j, Place p) {
-                if (p.row < m) x[t][i][j] = load4<decltype(dt)::value>(a.x, at(p, a.x_stride, a.x_batch), step, n - p.col);
+            every([&](int t, int i, int j, Place p) {
+                x[t][i][j] = load4<decltype(dt)::value>(a.x, element(p, a.x_stride, a.x_batch), step, inside(t, p));
             });
+        });
+        every([&](int t, int i, int j, Place) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sum = __builtin_fma((double)x[t][i][j][r], (double)x[t][i][j][r], sum);
         });
     }
-#pragma unroll
-    for (int t = 0; t < PARTS; ++t)
-#pragma unroll
-        for (int i = 0; i < FP; ++i)
-#pragma unroll
-            for (int j = 0; j < FQ; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) sum = __builtin_fma((double)x[t][i][j][r], (double)x[t][i][j][r], sum);
     sum = block_sum<WAVES * 64>(sum);
     if (threadIdx.x == 0) norm = inverse_norm(sum, a.eps, a.first);
     __syncthreads();
     const double inverse = norm;
     auto store_x = [&]() {
-        tiles(PARTS, mb * nb, [&](int t, int i, int j, Place p) {
-            if (p.col < (int)shape.np) small_store<XLD>(xs, p.row, p.col, x[t][i][j]);
+        every([&](int t, int i, int j, Place p) {
+            if (wave + t * WAVES < mb * nb && p.col < (int)shape.np) small_store<XLD>(xs, p.row, p.col, x[t][i][j]);
         });
     };
+    every([&](int t, int i, int j, Place p) {
+        if constexpr (STEP) {
+            const int count = inside(t, p);
+            x[t][i][j] = 0.f;
+            if (!tall && count > 0) x[t][i][j] = *reinterpret_cast<const f32x4*>(flat + p.row * pitch + p.col);
 #pragma unroll
-    for (int t = 0; t < PARTS; ++t)
+            for (int r = 0; r < 4; ++r) {
+                if (tall && r < count) x[t][i][j][r] = flat[(p.col + r) * pitch + p.row];
+                if (r >= count) x[t][i][j][r] = 0.f;
+            }
+        }
 #pragma unroll
-        for (int i = 0; i < FP; ++i)
-#pragma unroll
-            for (int j = 0; j < FQ; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) x[t][i][j][r] = (float)((double)x[t][i][j][r] * inverse);
+        for (int r = 0; r < 4; ++r) x[t][i][j][r] = (float)((double)x[t][i][j][r] * inverse);
+    });
+    if (STEP) __syncthreads();
     store_x();
     __syncthreads();
 
@@ -945,31 +1000,62 @@ __global__ __launch_bounds__(WAVES * 64) void ns_small_kernel(SmallArgs s) {
         store_x();
         __syncthreads();
     }
-    tiles(PARTS, mb * nb, [&](int t, int i, int j, Place p) {
-        const int count = p.row < m ? n - p.col : 0;
-        if (count <= 0) return;
-        if (a.step.master) {
-            const int64_t e = at(p, own, each_matrix);
-            f32x4 w = load4<ZSMR_FP32>(a.step.master, e, step, count);
-            w = w * a.decay - a.rate * x[t][i][j];
-            store4<ZSMR_FP32>(a.step.master, e, step, count, w);
-            by_dtype(a.param_dtype, [&](auto dt) { store4<decltype(dt)::value>(a.step.p16, e, step, count, w); });
-        } else {
-            by_dtype(a.out_dtype, [&](auto dt) { store4<decltype(dt)::value>(a.out, at(p, a.out_stride, a.out_batch), out_step, count, x[t][i][j]); });
+    if constexpr (STEP) {
+        __syncthreads();
+        every([&](int t, int i, int j, Place p) {
+            const int count = inside(t, p);
+            if (!tall && count > 0) *reinterpret_cast<f32x4*>(flat + p.row * pitch + p.col) = x[t][i][j];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (tall && r < count) flat[(p.col + r) * pitch + p.row] = x[t][i][j][r];
+        });
+        __syncthreads();
+        f32x8 w[kChunks];
+        auto load = [&](auto whole) {
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k) w[k] = load_row<ZSMR_FP32, decltype(whole)::value>(a.step.master, at + chunk(k).at, at + each);
+        };
+        if (cols % 8 == 0) load(std::true_type());
+        else load(std::false_type());
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
+            const Chunk c = chunk(k);
+            if (c.count <= 0) continue;
+            const float* const from = flat + c.row * pitch + c.col;
+            f32x8 f = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < c.count) f[i] = from[i];
+            const int64_t e = at + c.at;
+            f = w[k] * a.decay - a.rate * f;
+            store_some<ZSMR_FP32>(a.step.master, e, c.count, f);
+            by_dtype(a.param_dtype, [&](auto dt) { store_some<decltype(dt)::value>(a.step.p16, e, c.count, f); });
         }
-    });
+    } else {
+        const int64_t step = tall ? a.out_stride : 1;
+        by_dtype(a.out_dtype, [&](auto dt) {
+            every([&](int t, int i, int j, Place p) {
+                store4<decltype(dt)::value>(a.out, element(p, a.out_stride, a.out_batch), step, inside(t, p), x[t][i][j]);
+            });
+        });
+    }
 #endif
 }
 
 // ------------------------------------------------------------------ launches --
+template <bool STEP>
+void small_of(const SmallArgs& s, unsigned count, hipStream_t stream) {
+    if (s.a.shape.small == 1) ns_small_kernel<64, 64, 8, 2, 1, STEP><<<count, 512, 0, stream>>>(s);
+    else if (s.a.shape.small == 2) ns_small_kernel<64, 256, 8, 4, 2, STEP><<<count, 512, 0, stream>>>(s);
+    else ns_small_kernel<128, 128, 8, 4, 2, STEP><<<count, 512, 0, stream>>>(s);
+}
 hipError_t launch_small(const NewtonArgs& a, hipStream_t stream) {
     SmallArgs s{};
     s.a = a;
     launch_rows(a.shape.count, 512, [&](int64_t first, int64_t count) {
         s.first = first;
-        if (a.shape.small == 1) ns_small_kernel<64, 64, 8, 2, 1><<<(unsigned)count, 512, 0, stream>>>(s);
-        else if (a.shape.small == 2) ns_small_kernel<64, 256, 8, 4, 2><<<(unsigned)count, 512, 0, stream>>>(s);
-        else ns_small_kernel<128, 128, 8, 4, 2><<<(unsigned)count, 512, 0, stream>>>(s);
+        if (a.step.master) small_of<true>(s, (unsigned)count, stream);
+        else small_of<false>(s, (unsigned)count, stream);
     });
     return hipGetLastError();
 }
