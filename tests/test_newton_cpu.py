@@ -318,6 +318,11 @@ int main() {
     NsOp ops[kNsMaxOps];
     CHECK(ns_ops(quintic, 5, true, ops) == 18 && ns_group_steps(true, true, quintic, 5, 1.0) == 3 && ns_group_steps(true, false, quintic, 2, 1.2) == 2);
     CHECK(ns_group_steps(true, true, steep, 4, 1.0) == 1 && ns_group_steps(false, true, quintic, 5, 1.0) == 1);
+    // groups where they are sooner, never for fp32 results
+    auto chosen = [&](int64_t m, int64_t n, int64_t count, bool fp32 = false) { return ns_choose(quintic, 5, ns_shape(m, n, count, fp32), ops); };
+    CHECK(chosen(767, 1003, 1) == 15 && chosen(1003, 767, 1) == 15 && chosen(1600, 6400, 1) == 18 && chosen(140, 2000, 1) == 18);
+    CHECK(chosen(1600, 6400, 1, true) == 15 && chosen(4096, 4096, 1) == 15 && chosen(513, 2050, 1) == 18 && chosen(2300, 200, 1) == 18);
+    CHECK(chosen(130, 2100, 2) == 18 && chosen(1000, 513, 20) == 18);
     std::printf("plans passed\n");
     return 0;
 }

@@ -1128,12 +1128,12 @@ void products(const NewtonArgs& a, const NsOp* ops, int n_ops, const Space& w, c
     p.master = a.step.master;
     p.decay = a.decay;
     p.rate = a.rate;
-    for (int i = 0; i < n_ops; ++i) {
-        int sides = 0;
+    for (int i = 0; i < n_ops;) {
         const NsOp& o = ops[i];
-        for (;; ++i) {
-            const NsOp& op = ops[i];
-            NsSide& side = p.side[sides++];
+        const int sides = ns_sides(&o);
+        for (int k = 0; k < sides; ++k) {
+            const NsOp& op = ops[i + k];
+            NsSide& side = p.side[k];
             side.p = w.matrix[op.p];
             side.q = w.matrix[op.q];
             side.old = op.old < 0 ? nullptr : w.matrix[op.old];
@@ -1142,9 +1142,9 @@ void products(const NewtonArgs& a, const NsOp* ops, int n_ops, const Space& w, c
             side.mul = op.mul;
             side.old_mul = op.old_mul;
             side.old2_mul = op.old2_mul;
-            if (!op.paired) break;
         }
-        const bool from_x = o.p == M_X0 || o.p == M_X1, gram = from_x && o.kind == N_INNER;
+        i += sides;
+        const bool from_x = ns_from_x(o), gram = from_x && o.kind == N_INNER;
         p.p_rows = p.q_rows = p.rows = s.m;
         p.p_ld = (from_x ? s.np : s.mp) * 2;
         p.q_ld = (gram ? s.np : s.mp) * 2;
@@ -1153,7 +1153,7 @@ void products(const NewtonArgs& a, const NsOp* ops, int n_ops, const Space& w, c
         p.p_batch = s.m * p.p_ld;
         p.q_batch = s.m * p.q_ld;
         p.batch = s.m * p.ld;
-        p.steps = (int32_t)((gram ? s.np : s.mp) / kNsStep);
+        p.steps = (int32_t)ns_steps_of(s, o);
         const NsGrid grid = ns_grid(s, o.kind, (int64_t)sides * count, p.steps);
         if (o.kind == N_INNER) launch_product<N_INNER>(p, grid, stream);
         else if (o.kind == N_UPDATE) launch_product<N_UPDATE>(p, grid, stream);

@@ -72,7 +72,7 @@ int32_t zsmr_orthogonalize(const void* x, int32_t x_dtype, int64_t x_stride, int
     a.out_batch = out_batch;
     a.out_dtype = out_dtype;
     NsOp ops[kNsMaxOps];
-    return done(launch_orthogonalize(a, ops, ns_ops(ns->coef, ns->steps, a.shape.grouped, ops), ws, stream));
+    return done(launch_orthogonalize(a, ops, ns_choose(ns->coef, ns->steps, a.shape, ops), ws, stream));
 }
 
 int32_t zero_muon_step(zsmr_ctx* c, int32_t rank, int32_t unit, int64_t begin, int64_t rows, int64_t cols, int64_t count,
@@ -110,7 +110,7 @@ int32_t zero_muon_step(zsmr_ctx* c, int32_t rank, int32_t unit, int64_t begin, i
     a.decay = (float)(1.0 - hp->lr * hp->weight_decay);
     a.rate = (float)(hp->lr * hp->scale);
     NsOp ops[kNsMaxOps];
-    const hipError_t e = launch_muon(a, ops, ns_ops(ns->coef, ns->steps, a.shape.grouped, ops), ws, stream);
+    const hipError_t e = launch_muon(a, ops, ns_choose(ns->coef, ns->steps, a.shape, ops), ws, stream);
     if (e != hipSuccess) return hip_fail(e);
     count_reduce(c, rank, total);
     count_cast(c, rank, total);

@@ -24,7 +24,7 @@ struct NsShape {
     bool tall;                          // the wide orientation is the transposed one
     int64_t count, group;               // matrices; of a group, whose launches they share
     int parts;                          // partial sums of squares of a matrix
-    bool grouped;                       // steps in groups
+    bool grouped;                       // steps may be taken in groups
     int small;                          // the form of a matrix that stays in LDS, or 0
 };
 
@@ -78,6 +78,7 @@ struct NsGrid {
     int32_t p_tiles, q_tiles, tiles;    // of one matrix of one product
     int parts;                          // launches: one, or a second one for the last tiles
     NsPart part[2];
+    double us;                          // ns_cost() of them
 };
 inline int64_t ns_groups(const NsPart& p) { return p.form == NS_THIN ? p.count * 4 : p.count; }
 // What a launch takes, in microseconds.  Measured on MI355X, products of m x m, from 10
@@ -125,8 +126,11 @@ inline NsGrid ns_grid(const NsShape& s, int kind, int64_t products, int64_t step
             g.parts = 2;
             g.part[0] = NsPart{NS_WIDE, 0, whole};
             g.part[1] = rest;
+        } else {
+            least = one;
         }
     }
+    g.us = least;
     return g;
 }
 
@@ -296,6 +300,31 @@ inline int ns_ops(const double (*coef)[3], int steps, bool grouped, NsOp* ops) {
         x = next;
     }
     return n;
+}
+
+// Products behind each other that share a launch, and their steps of k.
+inline int ns_sides(const NsOp* op) {
+    int n = 1;
+    while (op[n - 1].paired) ++n;
+    return n;
+}
+inline bool ns_from_x(const NsOp& op) { return op.p == M_X0 || op.p == M_X1; }
+inline int64_t ns_steps_of(const NsShape& s, const NsOp& op) {
+    return (op.kind == N_INNER && ns_from_x(op) ? s.np : s.mp) / kNsStep;
+}
+// Groups where they end sooner.  Their products are fewer but one behind the other, so a
+// matrix of 767 x 1,003, whose launches all last 9 to 12 us, takes single steps.
+inline int ns_choose(const double (*coef)[3], int steps, const NsShape& s, NsOp* ops) {
+    auto us = [&](int n) {
+        double sum = 0;
+        for (int i = 0; i < n; i += ns_sides(ops + i)) sum += ns_grid(s, ops[i].kind, ns_sides(ops + i) * s.group, ns_steps_of(s, ops[i])).us;
+        return sum;
+    };
+    int n = ns_ops(coef, steps, false, ops);
+    if (!s.grouped) return n;
+    const double single = us(n);
+    n = ns_ops(coef, steps, true, ops);
+    return us(n) < single ? n : ns_ops(coef, steps, false, ops);
 }
 
 }  // namespace zsmr
