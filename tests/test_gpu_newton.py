@@ -144,7 +144,8 @@ def test_more_matrices_than_a_group_holds():
 
 
 @pytest.mark.parametrize("rows,cols,count", [(200, 240, 1), (130, 700, 3), (700, 130, 2), (513, 1100, 1), (1100, 513, 1), (1290, 1290, 1), (640, 640, 7),
-                                             (2100, 300, 1), (65, 6000, 1), (130, 2100, 2), (2300, 200, 1), (513, 2050, 1), (1000, 513, 20)])
+                                             (2100, 300, 1), (65, 6000, 1), (130, 2100, 2), (2300, 200, 1), (513, 2050, 1), (1000, 513, 20),
+                                             (1500, 6100, 1), (9000, 2048, 1), (333, 5001, 3)])
 def test_steps_in_groups_and_split_products(rows, cols, count):
     for rank in (None, 20):
         x = matrices(rows + cols, count, rows, cols, rank=rank)

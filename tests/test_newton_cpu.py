@@ -174,17 +174,23 @@ using namespace zsmr;
 static void grids(const NsShape& s, int64_t products) {
     for (int kind : {N_INNER, N_UPDATE, N_LAST})
         for (int64_t steps : {s.mp / 32, s.np / 32}) {
-            const NsGrid g = ns_grid(s, kind, products, steps);
-            CHECK((int64_t)g.p_tiles * 128 >= (kind == N_INNER ? s.m : s.n) && (int64_t)g.q_tiles * 128 >= s.m);
-            CHECK(g.tiles == (kind == N_INNER ? (int64_t)g.q_tiles * (g.q_tiles + 1) / 2 : (int64_t)g.p_tiles * g.q_tiles));
-            int64_t at = 0;
-            for (int i = 0; i < g.parts; ++i) {
-                const NsPart& p = g.part[i];
-                CHECK(p.first == at && p.count > 0 && p.form >= NS_WIDE && p.form <= NS_THIN);
-                CHECK(ns_groups(p) * 512 < (int64_t(1) << 32) && p.first + p.count <= INT32_MAX / 4);
-                at += p.count;
+            for (int gram = 0; gram < (kind == N_INNER && steps == s.np / 32 ? 2 : 1); ++gram) {
+                const NsGrid g = ns_grid(s, kind, products, steps, gram);
+                CHECK((int64_t)g.p_tiles * 128 >= (kind == N_INNER ? s.m : s.n) && (int64_t)g.q_tiles * 128 >= s.m);
+                CHECK(g.tiles == (kind == N_INNER ? (int64_t)g.q_tiles * (g.q_tiles + 1) / 2 : (int64_t)g.p_tiles * g.q_tiles));
+                int64_t at = 0;
+                for (int i = 0; i < g.parts; ++i) {
+                    const NsPart& p = g.part[i];
+                    CHECK(p.first == at && p.count > 0 && p.form >= NS_WIDE && p.form <= NS_PAIR);
+                    CHECK(ns_groups(p) * 512 < (int64_t(1) << 32) && p.first + p.count <= INT32_MAX / 4);
+                    at += p.count;
+                }
+                CHECK(g.parts >= 1 && g.parts <= 2 && at == (int64_t)g.tiles * products && g.us > 0);
+                // split steps: one launch, every part has some, and the sums fit X's other copy
+                CHECK(g.split == 1 ? g.split_steps == steps : gram && g.parts == 1 && g.split <= kNsMaxSplit);
+                CHECK((int64_t)g.split * g.split_steps >= steps && (int64_t)(g.split - 1) * g.split_steps < steps);
+                CHECK(g.split == 1 || at * g.split * kNsTileBytes <= products * s.m * s.np * 4);
             }
-            CHECK(g.parts >= 1 && g.parts <= 2 && at == (int64_t)g.tiles * products);
         }
 }
 

@@ -163,6 +163,8 @@ struct NsProduct {
     int32_t p_tiles, q_tiles, tiles;    // of 128 x 128, of a product and a matrix
     int32_t first_tile, quarters;   // of the launch; a workgroup takes a quarter of a tile
     int32_t count, steps;           // matrices; steps of 32 k
+    int32_t split_steps;            // N_PARTIAL: of a part, which blockIdx.y counts
+    float* partial;                 // tiles in quarters of 64 x 64, [part][tile][quarter][q][p]
     int64_t p_rows, p_ld, p_batch;  // rows; 16-bit values from row to row, from matrix to matrix
     int64_t q_rows, q_ld, q_batch;
     int64_t rows, cols, ld, batch;  // of the result and the old matrices
@@ -225,9 +227,10 @@ __device__ __forceinline__ int triangle_row(int i) {
     return r;
 }
 
-// A workgroup's tile of a launch, in tiles of its own size.
+// A workgroup's tile of a launch, in tiles of its own size; index: in all tiles of 128
+// or their quarters.
 struct Unit {
-    int side, matrix, tp, tq;
+    int side, matrix, tp, tq, index;
 };
 // Consecutive workgroups go to the eight XCDs in turn; each XCD takes a contiguous
 // run of tiles, in groups of 8 rows of tiles, so that the tiles it works on at a time
@@ -238,6 +241,7 @@ __device__ __forceinline__ Unit unit_of(const NsProduct& p) {
     const int at = xcd * each + min(xcd, rem) + (int)blockIdx.x / 8;
     int tile = p.first_tile + (p.quarters ? at / 4 : at);
     Unit u;
+    u.index = p.quarters ? p.first_tile * 4 + at : p.first_tile + at;
     u.side = tile >= p.tiles * p.count;
     tile -= u.side * p.tiles * p.count;
     u.matrix = tile / p.tiles;
@@ -295,11 +299,13 @@ struct OldTerms {
 };
 
 // A tile of T x T by GROUPS of four waves, each with STAGES of LDS, which take the
-// steps in turn and add up their sums in the end.
+// steps in turn and add up their sums in the end.  N_PARTIAL: some of the steps of an
+// N_INNER product, whose sums go to memory as they are.
+constexpr int N_PARTIAL = 100;
 template <int KIND, int T, int GROUPS, int STAGES>
-__global__ __launch_bounds__(kThreads * GROUPS, GROUPS == 1 ? 2 : GROUPS) void ns_product_kernel(NsProduct p) {
+__global__ __launch_bounds__(kThreads * GROUPS, T == 64 && STAGES == 2 ? 4 : 2) void ns_product_kernel(NsProduct p) {
 #if defined(__HIP_DEVICE_COMPILE__)     // the scheduling hints have no host form
-    constexpr bool kSymmetric = KIND == N_INNER, kOuter = !kSymmetric;
+    constexpr bool kPartial = KIND == N_PARTIAL, kSymmetric = KIND == N_INNER || kPartial, kOuter = !kSymmetric;
     constexpr int WP = 2, TP = T / WP / 16, TQ = T / (kWaves / WP) / 16;
     typedef Operand<T, kOuter, kWaves> P;
     typedef Operand<T, false, kWaves> Q;
@@ -316,13 +322,14 @@ __global__ __launch_bounds__(kThreads * GROUPS, GROUPS == 1 ? 2 : GROUPS) void n
     if (T == 64 && ((int64_t)tp * T >= p.cols || (int64_t)tq * T >= p.rows || (kSymmetric && tq > tp))) return;
 
     const int thread = threadIdx.x % kThreads, group = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
+    const int first_step = kPartial ? blockIdx.y * p.split_steps : 0, all_steps = kPartial ? min(p.split_steps, p.steps - first_step) : p.steps;
     // steps of this group, and of all: one past the group's last multiplies zeros
-    const int own_steps = (p.steps - group + GROUPS - 1) / GROUPS, steps = (p.steps + GROUPS - 1) / GROUPS;
+    const int own_steps = (all_steps - group + GROUPS - 1) / GROUPS, steps = (all_steps + GROUPS - 1) / GROUPS;
     char* const lds = smem + group * (STAGES * kStage);
     P op;
     Q oq;
-    op.init(Mat{side.p + matrix * p.p_batch, p.p_ld, p.p_rows, p.p_ld}, (int64_t)tp * T, group * kNsStep, GROUPS, thread);
-    oq.init(Mat{side.q + matrix * p.q_batch, p.q_ld, p.q_rows, p.q_ld}, (int64_t)tq * T, group * kNsStep, GROUPS, thread);
+    op.init(Mat{side.p + matrix * p.p_batch, p.p_ld, p.p_rows, p.p_ld}, (int64_t)tp * T, (int64_t)(first_step + group) * kNsStep, GROUPS, thread);
+    oq.init(Mat{side.q + matrix * p.q_batch, p.q_ld, p.q_rows, p.q_ld}, (int64_t)tq * T, (int64_t)(first_step + group) * kNsStep, GROUPS, thread);
 
     const int lane = threadIdx.x % 64, wave = thread / 64, wp = wave % WP, wq = wave / WP;
     f32x4 acc[TP][TQ];
@@ -335,7 +342,7 @@ __global__ __launch_bounds__(kThreads * GROUPS, GROUPS == 1 ? 2 : GROUPS) void n
     // where a thread has one group of eight results, what is added to them comes early
     constexpr bool kEarly = T * T / 8 == kThreads * GROUPS;
     OldTerms old;
-    if (kEarly && q0 + (int)threadIdx.x / (T / 8) < p.rows && p0 + (int)threadIdx.x % (T / 8) * 8 < padded)
+    if (kEarly && !kPartial && q0 + (int)threadIdx.x / (T / 8) < p.rows && p0 + (int)threadIdx.x % (T / 8) * 8 < padded)
         old.load(side, matrix * p.batch + split_at(q0 + threadIdx.x / (T / 8), p0 + threadIdx.x % (T / 8) * 8, p.ld));
 
     // A step multiplies hi hi while it reads the lo parts, then waits for the next
@@ -411,6 +418,19 @@ __global__ __launch_bounds__(kThreads * GROUPS, GROUPS == 1 ? 2 : GROUPS) void n
         }
         __syncthreads();
     }
+    if constexpr (kPartial) {
+        if (group > 0) return;
+#pragma unroll
+        for (int j = 0; j < TQ; ++j)
+#pragma unroll
+            for (int i = 0; i < TP; ++i) {
+                const int q = (wq * TQ + j) * 16 + lane % 16, c = (wp * TP + i) * 16 + lane / 16 * 4;
+                const int64_t quarter = T == 64 ? unit.index : unit.index * (int64_t)4 + q / 64 * 2 + c / 64;
+                const int64_t all = (int64_t)p.tiles * p.count * 4;
+                *reinterpret_cast<f32x4*>(p.partial + ((blockIdx.y * all + quarter) * 64 + q % 64) * 64 + c % 64) = acc[i][j];
+            }
+        return;
+    }
     // acc[i][j][r] is D at p = 16 i + 4 (lane / 16) + r, q = 16 j + lane % 16 of the
     // wave's part.  Results leave through LDS as [q][p] in fp32, the 16-byte chunk c
     // of row q in slot c ^ f(q): rows are then read along p, columns along q, each
@@ -464,6 +484,47 @@ __global__ __launch_bounds__(kThreads * GROUPS, GROUPS == 1 ? 2 : GROUPS) void n
         for (int i = 0; i < 8; ++i) d[i] = out[at(q + i, row / 4) + row % 4];
         if constexpr (KIND == N_LAST) put_result(p, p.first + matrix, p0 + row, q0 + q, (int)min((int64_t)8, p.rows - q0 - q), d);
         else store_split(dst, split_at(p0 + row, q0 + q, p.ld), d);
+    }
+#endif
+}
+
+// What the parts of an N_PARTIAL product add up to, a quarter of a tile a workgroup.
+__global__ __launch_bounds__(kThreads) void ns_join_kernel(NsProduct p, int split) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int kPitch = 68;      // rows are read along p and along q
+    __shared__ __attribute__((aligned(16))) float out[64 * kPitch];
+    const Unit unit = unit_of<true>(p);
+    const NsSide& side = p.side[0];
+    const int64_t p0 = (int64_t)unit.tp * 64, q0 = (int64_t)unit.tq * 64, padded = p.ld / 2;
+    if (p0 >= p.cols || q0 >= p.rows || unit.tq > unit.tp) return;
+    uint16_t* const dst = side.dst + unit.matrix * p.batch;
+    const int64_t part = (int64_t)p.tiles * p.count * 4 * 64 * 64;
+    const float* const from = p.partial + (int64_t)unit.index * 64 * 64;
+    f32x8 sum[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) sum[i] = load8<ZSMR_FP32>(from, (i * kThreads + threadIdx.x) * 8);
+#pragma unroll 4
+    for (int s = 1; s < split; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) sum[i] += load8<ZSMR_FP32>(from + s * part, (i * kThreads + threadIdx.x) * 8);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int k = i * kThreads + threadIdx.x, q = k / 8, c = k % 8 * 8;
+        const f32x8 d = sum[i] * side.mul;
+        if (q0 + q < p.rows && p0 + c < padded) store_split(dst, split_at(q0 + q, p0 + c, p.ld), d);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) out[q * kPitch + c + r] = d[r];
+    }
+    if (unit.tp == unit.tq) return;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int k = i * kThreads + threadIdx.x, row = k % 64, q = k / 64 * 8;
+        if (p0 + row >= p.rows || q0 + q >= padded) continue;
+        f32x8 d;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) d[r] = out[(q + r) * kPitch + row];
+        store_split(dst, split_at(p0 + row, q0 + q, p.ld), d);
     }
 #endif
 }
@@ -1076,17 +1137,19 @@ Space space_of(const NsShape& s, void* ws) {
 
 template <int KIND>
 void launch_product(NsProduct& p, const NsGrid& grid, hipStream_t stream) {
+    p.split_steps = grid.split_steps;
     p.p_tiles = grid.p_tiles;
     p.q_tiles = grid.q_tiles;
     p.tiles = grid.tiles;
     for (int i = 0; i < grid.parts; ++i) {
         const NsPart& part = grid.part[i];
-        const unsigned groups = (unsigned)ns_groups(part);
+        const dim3 groups((unsigned)ns_groups(part), grid.split);
         p.first_tile = (int32_t)part.first;
-        p.quarters = part.form == NS_THIN;
+        p.quarters = ns_quarters(part.form);
         if (part.form == NS_WIDE) ns_product_kernel<KIND, 128, 1, 2><<<groups, kThreads, 0, stream>>>(p);
         else if (part.form == NS_DEEP) ns_product_kernel<KIND, 128, 2, 2><<<groups, kThreads * 2, 0, stream>>>(p);
-        else ns_product_kernel<KIND, 64, 2, 4><<<groups, kThreads * 2, 0, stream>>>(p);
+        else if (part.form == NS_THIN) ns_product_kernel<KIND, 64, 2, 4><<<groups, kThreads * 2, 0, stream>>>(p);
+        else ns_product_kernel<KIND, 64, 2, 2><<<groups, kThreads * 2, 0, stream>>>(p);
     }
 }
 
@@ -1144,7 +1207,7 @@ void products(const NewtonArgs& a, const NsOp* ops, int n_ops, const Space& w, c
             side.old2_mul = op.old2_mul;
         }
         i += sides;
-        const bool from_x = ns_from_x(o), gram = from_x && o.kind == N_INNER;
+        const bool from_x = ns_from_x(o), gram = ns_gram(o);
         p.p_rows = p.q_rows = p.rows = s.m;
         p.p_ld = (from_x ? s.np : s.mp) * 2;
         p.q_ld = (gram ? s.np : s.mp) * 2;
@@ -1154,8 +1217,14 @@ void products(const NewtonArgs& a, const NsOp* ops, int n_ops, const Space& w, c
         p.q_batch = s.m * p.q_ld;
         p.batch = s.m * p.ld;
         p.steps = (int32_t)ns_steps_of(s, o);
-        const NsGrid grid = ns_grid(s, o.kind, (int64_t)sides * count, p.steps);
-        if (o.kind == N_INNER) launch_product<N_INNER>(p, grid, stream);
+        const NsGrid grid = ns_grid(s, o.kind, (int64_t)sides * count, p.steps, gram);
+        if (grid.split > 1) {
+            p.partial = reinterpret_cast<float*>(w.matrix[o.p == M_X0 ? M_X1 : M_X0]);
+            launch_product<N_PARTIAL>(p, grid, stream);
+            p.first_tile = 0;
+            p.quarters = 1;
+            ns_join_kernel<<<(unsigned)(grid.part[0].count * 4), kThreads, 0, stream>>>(p, grid.split);
+        } else if (o.kind == N_INNER) launch_product<N_INNER>(p, grid, stream);
         else if (o.kind == N_UPDATE) launch_product<N_UPDATE>(p, grid, stream);
         else launch_product<N_LAST>(p, grid, stream);
     }

@@ -68,8 +68,10 @@ struct NsOp {
 };
 // How the tiles of 128 x 128 of a product are computed: by four waves, two workgroups
 // a CU (NS_WIDE); by eight, one a CU, each four half of the steps (NS_DEEP); in
-// quarters of 64 x 64, by eight waves in the same way (NS_THIN).
-enum : int { NS_WIDE, NS_DEEP, NS_THIN };
+// quarters of 64 x 64, by eight waves in the same way, with four stages of LDS
+// (NS_THIN) or, two workgroups a CU, with two (NS_PAIR).
+enum : int { NS_WIDE, NS_DEEP, NS_THIN, NS_PAIR };
+inline bool ns_quarters(int form) { return form >= NS_THIN; }
 struct NsPart {
     int form;
     int64_t first, count;               // tiles
@@ -78,25 +80,39 @@ struct NsGrid {
     int32_t p_tiles, q_tiles, tiles;    // of one matrix of one product
     int parts;                          // launches: one, or a second one for the last tiles
     NsPart part[2];
-    double us;                          // ns_cost() of them
+    int32_t split;                      // the steps' parts, whose sums a launch of their own adds up; or 1
+    int32_t split_steps;                // of a part; the last one may have fewer
+    double us;                          // what it takes
 };
-inline int64_t ns_groups(const NsPart& p) { return p.form == NS_THIN ? p.count * 4 : p.count; }
+inline int64_t ns_groups(const NsPart& p) { return ns_quarters(p.form) ? p.count * 4 : p.count; }
 // What a launch takes, in microseconds.  Measured on MI355X, products of m x m, from 10
 // to 128 steps: a workgroup with a CU for itself 0.75, 0.58 and 0.21 us a step after
 // 7.5, 8 and 5.5 us; under full load (where the power decides) 1.22 us for two wide
-// tiles, 0.68 for a deep and 0.26 for a thin one.
+// tiles, 0.68 for a deep and 0.26 for a thin one, 0.4 for a pair.  364 quarters of 50
+// steps: thin 28.2 us, in pairs 24.6; 78 of 24: 9.6 and 12.3.
 inline double ns_cost(int form, int64_t tiles, int64_t steps) {
-    const int64_t groups = form == NS_THIN ? tiles * 4 : tiles, each = form == NS_WIDE ? 2 * kNsCus : kNsCus;
+    const int64_t groups = ns_quarters(form) ? tiles * 4 : tiles, each = form == NS_WIDE || form == NS_PAIR ? 2 * kNsCus : kNsCus;
     const int64_t full = groups / each, rest = groups % each;
     if (form == NS_WIDE) return 7.5 + steps * (full * 1.22 + (rest > kNsCus ? 1.22 : rest > 0 ? (full ? 0.6 : 0.75) : 0));
     if (form == NS_DEEP) return 8 + steps * (full * 0.68 + (rest > 0 ? full ? 0.62 : 0.58 : 0));
+    if (form == NS_PAIR) return 5.5 + steps * (full * 0.42 + (rest > kNsCus ? 0.4 : rest > 0 ? 0.28 : 0));
     return 5.5 + steps * (full + (rest > 0) > 1 ? (full + (rest > 0)) * 0.26 : 0.21);
 }
 // The form that ends soonest, for whole rounds over the CUs and, if that is sooner,
 // another for what is left of the last round.  A symmetric product of 4,096 has 528
 // tiles, 16 more than a round: all of them wide 225 us, the 16 in quarters 195.
-inline NsGrid ns_grid(const NsShape& s, int kind, int64_t products, int64_t steps) {
+//
+// X X^T of a long X has more steps than tiles.  Its steps may be split: every part's tiles
+// go to memory in fp32 (into X's other copy, free at that time), and ns_join_kernel adds
+// them up.  1,600 x 6,400: 55 us and 9 to join 5 parts,
+// 110 in one; 128 x 8,192: 9 and 7 for 16, 59 in one.
+constexpr int kNsMaxSplit = 16;
+constexpr int64_t kNsTileBytes = 128 * 128 * 4;
+inline double ns_join_cost(int64_t tiles, int split) { return 5.5 + (double)(tiles * kNsTileBytes * split) * 1.7e-7; }
+inline NsGrid ns_grid(const NsShape& s, int kind, int64_t products, int64_t steps, bool gram = false) {
     NsGrid g{};
+    g.split = 1;
+    g.split_steps = (int32_t)steps;
     g.p_tiles = (int32_t)ns_tiles(kind == N_INNER ? s.m : s.n, 128);
     g.q_tiles = (int32_t)ns_tiles(s.m, 128);
     g.tiles = kind == N_INNER ? g.q_tiles * (g.q_tiles + 1) / 2 : g.p_tiles * g.q_tiles;
@@ -105,7 +121,7 @@ inline NsGrid ns_grid(const NsShape& s, int kind, int64_t products, int64_t step
     auto best = [&](int64_t first, int64_t count) {
         NsPart p{NS_WIDE, first, count};
         double us = ns_cost(NS_WIDE, count, steps);
-        for (int form : {NS_DEEP, NS_THIN}) {
+        for (int form : {NS_DEEP, NS_THIN, NS_PAIR}) {
             const double t = ns_cost(form, count, steps);
             if (t < us) {
                 us = t;
@@ -128,6 +144,19 @@ inline NsGrid ns_grid(const NsShape& s, int kind, int64_t products, int64_t step
             g.part[1] = rest;
         } else {
             least = one;
+        }
+    }
+    for (int split = 2; gram && split <= kNsMaxSplit && all * split * kNsTileBytes <= products * s.m * s.np * 4; ++split) {
+        const int64_t each = ns_tiles(steps, split);
+        if (each < 8 || (split - 1) * each >= steps) continue;
+        for (int form : {NS_WIDE, NS_DEEP, NS_THIN, NS_PAIR}) {
+            const double us = ns_cost(form, all * split, each) + ns_join_cost(all, split);
+            if (us >= least) continue;
+            least = us;
+            g.parts = 1;
+            g.part[0] = NsPart{form, 0, all};
+            g.split = split;
+            g.split_steps = (int32_t)each;
         }
     }
     g.us = least;
@@ -309,15 +338,14 @@ inline int ns_sides(const NsOp* op) {
     return n;
 }
 inline bool ns_from_x(const NsOp& op) { return op.p == M_X0 || op.p == M_X1; }
-inline int64_t ns_steps_of(const NsShape& s, const NsOp& op) {
-    return (op.kind == N_INNER && ns_from_x(op) ? s.np : s.mp) / kNsStep;
-}
+inline bool ns_gram(const NsOp& op) { return op.kind == N_INNER && ns_from_x(op); }
+inline int64_t ns_steps_of(const NsShape& s, const NsOp& op) { return (ns_gram(op) ? s.np : s.mp) / kNsStep; }
 // Groups where they end sooner.  Their products are fewer but one behind the other, so a
 // matrix of 767 x 1,003, whose launches all last 9 to 12 us, takes single steps.
 inline int ns_choose(const double (*coef)[3], int steps, const NsShape& s, NsOp* ops) {
     auto us = [&](int n) {
         double sum = 0;
-        for (int i = 0; i < n; i += ns_sides(ops + i)) sum += ns_grid(s, ops[i].kind, ns_sides(ops + i) * s.group, ns_steps_of(s, ops[i])).us;
+        for (int i = 0; i < n; i += ns_sides(ops + i)) sum += ns_grid(s, ops[i].kind, ns_sides(ops + i) * s.group, ns_steps_of(s, ops[i]), ns_gram(ops[i])).us;
         return sum;
     };
     int n = ns_ops(coef, steps, false, ops);
