@@ -4,7 +4,8 @@ polynomial in 64 bits.
 Tolerances.  The kernels hold every matrix in 22 bits (an error of at most 2^-22 of
 each element, and of half of fp16's smallest step, 2^-25, over the power of two the
 matrix is held times, 2^14 at least for these polynomials: 2^-39), leave out products
-of 2^-22, and sum 3 k / 32 partial sums of a product in fp32.  ``rounded`` makes the 64-bit computation with errors of these sizes, drawn at
+of 2^-22, and sum 3 k / 32 partial sums of a product in fp32.  ``polynomial`` with
+``noise`` makes the 64-bit computation with errors of these sizes, drawn at
 random, at every place where the kernels have one; the distance of that from the
 exact result, the largest of eight drawings (a single drawing says little of a
 matrix of few elements), four times, is what a result may be off in the 2-norm, and
@@ -12,6 +13,8 @@ ten times its share of an element (a normal error passes five of its deviations
 once in two million) what an element may, besides half a step of the result's own
 format.
 """
+import math
+
 import pytest
 import torch
 
@@ -343,3 +346,82 @@ def test_steps_captured_into_a_graph():
         torch.cuda.synchronize()
         for k in ("master", "momentum", "p16"):
             assert torch.equal(a[k], b[k]), (i, k)
+
+
+# ------------------------------------------------------------- used together --
+@pytest.mark.parametrize("vocab,width,tokens,world", [(301, 72, 130, 3), (700, 140, 65, 2)])
+def test_policy_example(vocab, width, tokens, world):
+    """Scores, their gradient and the two kinds of step as a policy uses them: against
+    the formulas in 64 bits, each from the 16-bit values it was given."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "policy.py")
+    spec = importlib.util.spec_from_file_location("policy", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    torch.manual_seed(3)
+    policy = module.Policy(vocab, width, tokens, world, 3e-3, 0.02, 0.05)
+    g, u = gen(4), torch.finfo(BF16).eps / 2
+    x = torch.randint(vocab, (world, tokens), device="cuda", generator=g)
+    for r in range(world):
+        hidden, logits = policy.logits(x[r])
+        actions = torch.randint(vocab, (tokens,), device="cuda", generator=g)
+        advantage = torch.randn(tokens, device="cuda", generator=g)
+        policy.backward(r, x[r], hidden, logits, actions, advantage)
+        leaf = logits.double().requires_grad_()
+        p = torch.log_softmax(leaf, 1)
+        picked, entropy = p.gather(1, actions[:, None]).squeeze(1), -(p.exp() * p).sum(1)
+        # lse, its difference and the sums of V terms in fp32
+        near = 2.0 ** -20 * (8 + leaf.detach().abs().amax(1))
+        assert ((policy.logprob - picked).abs() <= near).all() and ((policy.entropy - entropy).abs() <= 4 * near).all()
+        best = p.detach().gather(1, policy.top_ids)
+        assert ((policy.top_logprobs - best).abs() <= near[:, None]).all()
+        assert torch.equal(logits.gather(1, policy.top_ids), logits.topk(4).values)
+        loss = -(advantage.double() * picked).mean() - 0.05 * entropy.mean()
+        exact, = torch.autograd.grad(loss, leaf)
+        # one bf16 rounding, and p's relative error times the terms it is in
+        terms = (advantage.abs().double()[:, None] + 0.05 * (p.abs() + entropy[:, None]).detach()) / tokens
+        assert ((policy.dlogits.double() - exact).abs() <= u * exact.abs() + 8 * near[:, None] * terms * p.exp().detach() + 2.0 ** -22 * terms).all()
+        # products of 16-bit values, of which each is rounded once: dhidden and dx on the way;
+        # sums of up to 700 terms in fp32: 701 roundings of 2^-24 are below 2^-14
+        d, h, e = policy.dlogits.double(), hidden.double(), policy.x.double()
+        w, head = policy.weights[1].double(), policy.weights[2].double()
+        dh = d @ head
+        for got, want, off in ((policy.weight_grads[2][r], d.t() @ h, d.abs().t() @ h.abs() * 2.0 ** -14),
+                               (policy.weight_grads[1][r], dh.t() @ e, (u * dh.abs() + d.abs() @ head.abs() * 2.0 ** -14).t() @ e.abs() * (1 + 2.0 ** -8))):
+            assert ((got.double() - want).abs() <= u * want.abs() + off * (1 + u) + 1e-30).all()
+        dx = dh @ w
+        dx_off = (u * dh.abs() + d.abs() @ head.abs() * 2.0 ** -14) @ w.abs() * (1 + 2.0 ** -8) + u * dx.abs()
+        add = lambda t: torch.zeros(vocab, width, device="cuda", dtype=torch.float64).index_add_(0, x[r], t)
+        want, off = add(dx), add(dx_off + 2.0 ** -14 * dx.abs())
+        assert ((policy.weight_grads[0][r].double() - want).abs() <= u * want.abs() + off * (1 + u) + 1e-30).all()
+    o, n = policy.at[1], width * width
+    rows, old = policy.grads[:, o:o + n], policy.master[o:o + n].double()
+    mean = rows[0].float()
+    for r in range(1, world):
+        mean = mean + rows[r].float()
+    mean = mean / torch.full_like(mean, world)
+    b = torch.tensor(0.95, device="cuda")
+    exact, each, _ = allowed((mean + b * mean).view(1, width, width), F16)
+    adam = [policy.master[s].clone() for s in (slice(0, o), slice(o + n, None))]
+    policy.update()
+    want = old - 0.02 * exact.reshape(-1)
+    tol = 0.02 * each.reshape(-1) + 2.0 ** -24 * (2 * old.abs() + 4 * exact.reshape(-1).abs() + want.abs()) + 1e-30
+    assert ((policy.master[o:o + n].double() - want).abs() <= tol).all()
+    assert torch.equal(policy.m[o:o + n], mean)
+    assert torch.equal(policy.params, policy.master.to(BF16))
+    # Adam's first step is lr or less an element
+    for before, s in zip(adam, (slice(0, o), slice(o + n, None))):
+        moved = (policy.master[s] - before).abs()
+        assert moved.max() <= 3e-3 * (1 + 1e-5) + 2.0 ** -23 * before.abs().max() and (moved > 0).any()
+
+
+def test_policy_example_runs():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "policy.py")
+    spec = importlib.util.spec_from_file_location("policy", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    rewards = module.train(vocab=100, width=64, tokens=256, world=2, steps=5, say=lambda *_: None)
+    assert len(rewards) == 5 and all(math.isfinite(r) and 0 <= r <= 1 for r in rewards)
