@@ -88,14 +88,15 @@ inline int64_t ns_groups(const NsPart& p) { return ns_quarters(p.form) ? p.count
 // What a launch takes, in microseconds.  Measured on MI355X, products of m x m, from 10
 // to 128 steps: a workgroup with a CU for itself 0.75, 0.58 and 0.21 us a step after
 // 7.5, 8 and 5.5 us; under full load (where the power decides) 1.22 us for two wide
-// tiles, 0.68 for a deep and 0.26 for a thin one, 0.4 for a pair.  364 quarters of 50
-// steps: thin 28.2 us, in pairs 24.6; 78 of 24: 9.6 and 12.3.
+// tiles, 0.68 for a deep and 0.26 for a thin one, 0.4 for a pair (0.52
+// in each of several rounds).  364 quarters of 50 steps: thin 28.2 us, in pairs 24.6; 78
+// of 24: 9.6 and 12.3; 1,456 of 50: in pairs 77.5, 364 wide tiles 68.
 inline double ns_cost(int form, int64_t tiles, int64_t steps) {
     const int64_t groups = ns_quarters(form) ? tiles * 4 : tiles, each = form == NS_WIDE || form == NS_PAIR ? 2 * kNsCus : kNsCus;
     const int64_t full = groups / each, rest = groups % each;
     if (form == NS_WIDE) return 7.5 + steps * (full * 1.22 + (rest > kNsCus ? 1.22 : rest > 0 ? (full ? 0.6 : 0.75) : 0));
     if (form == NS_DEEP) return 8 + steps * (full * 0.68 + (rest > 0 ? full ? 0.62 : 0.58 : 0));
-    if (form == NS_PAIR) return 5.5 + steps * (full * 0.42 + (rest > kNsCus ? 0.4 : rest > 0 ? 0.28 : 0));
+    if (form == NS_PAIR) return 5.5 + steps * (full * 0.52 + (rest > kNsCus ? 0.4 : rest > 0 ? 0.28 : 0));
     return 5.5 + steps * (full + (rest > 0) > 1 ? (full + (rest > 0)) * 0.26 : 0.21);
 }
 // The form that ends soonest, for whole rounds over the CUs and, if that is sooner,
