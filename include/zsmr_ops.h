@@ -204,9 +204,11 @@ typedef struct zsmr_newton {
 int64_t zsmr_orthogonalize_workspace(int64_t rows, int64_t cols, int64_t count);
 
 /* out[k] = the last X of x[k], rounded to out_dtype once, for `count` matrices of
- * rows x cols: row_stride elements from row to row (at least cols), batch elements from
- * matrix to matrix (any, as long as the matrices of out do not overlap).  Formats:
- * ZSMR_FP16, ZSMR_BF16 or ZSMR_FP32. */
+ * rows x cols: x_stride and out_stride elements from row to row (at least cols),
+ * x_batch and out_batch from matrix to matrix (any, as long as the matrices of out do
+ * not overlap).  out may be x, in the same format and layout, or memory apart from it.
+ * Formats: ZSMR_FP16, ZSMR_BF16 or ZSMR_FP32.  The bits of a matrix do not depend on
+ * what the others hold, but on how many a call has. */
 int32_t zsmr_orthogonalize(const void* x, int32_t x_dtype, int64_t x_stride, int64_t x_batch,
                            void* out, int32_t out_dtype, int64_t out_stride, int64_t out_batch,
                            int64_t rows, int64_t cols, int64_t count, const zsmr_newton* ns,
@@ -242,8 +244,10 @@ int32_t zero_muon_step(zsmr_ctx* ctx, int32_t rank, int32_t unit, int64_t begin,
  *   entropy = -sum_v p_v log p_v.
  * Logits of -infinity are masked: p = 0.  So are values of z below -2.3e38, which
  * the lowest values of bf16 and fp32 are.  A row with nothing else has lse
- * -infinity, entropy 0, logprob -infinity and a gradient of zeros.  A NaN makes a
- * row's lse, logprob, entropy and gradient NaN.  An id outside [0, vocab) is
+ * -infinity, entropy 0, log probabilities of -infinity and a gradient of zeros.  A
+ * NaN makes a row's lse, logprob, entropy and gradient NaN; +infinity, or a z above
+ * 2.3e38, makes its lse +infinity and leaves the rest of the row's results but the
+ * alternatives' indices unspecified.  An id outside [0, vocab) is
  * padding: logprob 0, which has no gradient; entropy and alternatives are the
  * row's.  scale: 2^-100 .. 2^100. */
 #define ZSMR_MAX_TOP 64

@@ -240,6 +240,39 @@ def test_the_same_bits_again_on_another_stream_and_captured():
     agrees(out, x)
 
 
+@pytest.mark.parametrize("count,rows,cols", [(30, 64, 48), (2, 100, 128), (3, 333, 200), (40, 1000, 1000)])
+def test_in_place(count, rows, cols):
+    x = matrices(11, count, rows, cols, dtype=BF16)
+    want = call(x, torch.empty_like(x))
+    call(x, x)
+    assert torch.equal(x, want)
+
+
+def test_calls_at_once_and_graphs_that_share_a_workspace():
+    x = [matrices(12 + k, 2, 150, 1700) for k in range(2)]
+    want = [call(t, torch.empty_like(t)) for t in x]
+    size = z.zsmr_orthogonalize_workspace(150, 1700, 2)
+    out, ws = [torch.zeros_like(t) for t in x], [torch.empty(size, device="cuda", dtype=torch.uint8) for _ in x]
+    streams = [torch.cuda.Stream() for _ in x]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for k, stream in enumerate(streams):
+            z.zsmr_orthogonalize(x[k], out[k], ws[k], stream=stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(out, want))
+    graphs = [torch.cuda.CUDAGraph() for _ in x]
+    for k, graph in enumerate(graphs):
+        with torch.cuda.graph(graph):
+            z.zsmr_orthogonalize(x[k], out[k], ws[0])
+    for turn in range(3):
+        for o in out:
+            o.zero_()
+        for graph in graphs if turn % 2 else graphs[::-1]:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(out, want))
+
+
 # ---------------------------------------------------------------- shard step --
 def muon(ctx, rank, unit, begin, rows, cols, count, s, **kw):
     size = z.zsmr_orthogonalize_workspace(rows, cols, count)

@@ -168,6 +168,38 @@ def test_masked_rows(dtype, many):
         assert (out["lse"] == -INF).all() and (out["entropy"] == 0).all() and (out["logprob"][:7] == -INF).all() and out["logprob"][7] == 0
 
 
+@pytest.mark.parametrize("v", [700, 90000])
+def test_alternatives_of_a_masked_row(v):
+    """Lowest values are alternatives (they are above -infinity) of no probability."""
+    x, _ = logits(17, 3, v, BF16)
+    x[1] = torch.finfo(BF16).min
+    x[2, 1:] = torch.finfo(BF16).min
+    out = score(x, None, 6)
+    assert torch.equal(out["top_ids"], best(x, 6))
+    assert (out["top_logprobs"][1] == -INF).all() and (out["top_logprobs"][2, 1:] == -INF).all()
+    # the reference is x log2 e rounded once, half a step of a number below 16
+    assert x[2, 0].abs() < 11 and out["top_logprobs"][2, 0].abs() <= 2.0 ** -24 * 16
+
+
+def test_calls_on_two_streams_at_once():
+    x, ids = logits(18, 40, 128256, BF16)
+    want = score(x, ids, 9)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    size = z.zsmr_logprobs_workspace(40, 128256, 9)
+    for stream in streams:
+        out = {k: torch.full_like(t, 5) for k, t in want.items()}
+        got.append((out, torch.empty(size, device="cuda", dtype=torch.uint8)))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for stream, (out, ws) in zip(streams, got):
+            z.zsmr_logprobs(x, ids, out["logprob"], out["lse"], out["entropy"], ws, top_ids=out["top_ids"], top_logprobs=out["top_logprobs"],
+                            stream=stream)
+    torch.cuda.synchronize()
+    for out, _ in got:
+        assert all(torch.equal(out[k], want[k]) for k in want)
+
+
 def test_nan_and_infinity():
     x, ids = logits(8, 6, 3000, F32)
     x[1, 2999] = float("nan")

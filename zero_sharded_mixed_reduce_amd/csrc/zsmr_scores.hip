@@ -208,7 +208,7 @@ __device__ __forceinline__ void put_top(const ForwardArgs& f, int64_t t, Stats s
         else static_cast<int32_t*>(a.top_ids)[e] = id;
     }
     if (a.top_logprobs)
-        a.top_logprobs[e] = key ? (fused(value_of((uint32_t)(key >> 32)), f.c, -s.ref) - log2_of(s.sum)) * kLn2 : -INFINITY;
+        a.top_logprobs[e] = key && s.sum != 0.f ? (fused(value_of((uint32_t)(key >> 32)), f.c, -s.ref) - log2_of(s.sum)) * kLn2 : -INFINITY;
 }
 
 // A wave's block of 512 logits, eight a lane: 16 bytes a lane and load, which covers a
