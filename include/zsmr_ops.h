@@ -181,8 +181,9 @@ int32_t zero_clipped_step(zsmr_ctx* ctx, int32_t rank, int32_t unit, const float
  * an odd polynomial that moves every singular value the way the triple says:
  * with a = 3.4445, b = -4.7750, c = 2.0315 five times, to about 1.  Every
  * product has fp32's accuracy (operands of 22 bits, fp32 sums), whatever the
- * formats of x and out.  A matrix of zeros gives zeros; one with a NaN or an
- * infinity gives NaN. */
+ * formats of x and out.  For 16-bit results steps may share their products with X,
+ * which costs about 1e-4 of the norm, less than the results' rounding.  A matrix of
+ * zeros gives zeros; one with a NaN or an infinity gives NaN. */
 #define ZSMR_MAX_NS_STEPS 16
 typedef struct zsmr_newton {
     double eps;                             /* finite, >= 0 */

@@ -6,7 +6,7 @@
 // towards 1.  X is the wide orientation, m <= n, so the inner matrices are m x m.
 // All of it is matrix products: A and A^2 are symmetric, of which only the tiles on
 // and below the diagonal are computed and written twice, so a pass does
-// m^2 n + m^3 + 2 m^2 n operations.
+// m^2 n + m^3 + 2 m^2 n operations, or fewer with steps in groups (zsmr_newton_plan.h).
 //
 // Precision.  The first passes raise small singular values by a factor of several
 // hundred, and a rounding of X with them: with operands of one 16-bit rounding the
@@ -301,6 +301,10 @@ struct OldTerms {
 // A tile of T x T by GROUPS of four waves, each with STAGES of LDS, which take the
 // steps in turn and add up their sums in the end.  N_PARTIAL: some of the steps of an
 // N_INNER product, whose sums go to memory as they are.
+// Bound by the power of the matrix units where the tiles fill the CUs: X' of 4,096 x
+// 14,336, wide tiles, takes 1.08 ms, 1.34 PFLOP/s of fp16 with the units busy in 0.76 of
+// the cycles at 1.76 GHz; the inner products of 4,096 run at 1.24.  Elsewhere by one
+// round's steps (zsmr_newton_plan.h has what each form takes).
 constexpr int N_PARTIAL = 100;
 template <int KIND, int T, int GROUPS, int STAGES>
 __global__ __launch_bounds__(kThreads * GROUPS, T == 64 && STAGES == 2 ? 4 : 2) void ns_product_kernel(NsProduct p) {
@@ -489,6 +493,8 @@ __global__ __launch_bounds__(kThreads * GROUPS, T == 64 && STAGES == 2 ? 4 : 2) 
 }
 
 // What the parts of an N_PARTIAL product add up to, a quarter of a tile a workgroup.
+// Reads the parts once: 9.4 us for 91 tiles of 5 parts, 50 for 528 of 6 (4.7 TB/s with
+// what it writes).
 __global__ __launch_bounds__(kThreads) void ns_join_kernel(NsProduct p, int split) {
 #if defined(__HIP_DEVICE_COMPILE__)
     constexpr int kPitch = 68;      // rows are read along p and along q
@@ -536,7 +542,8 @@ __device__ __forceinline__ void add_squares(f32x8 f, double* s) {
     for (int i = 0; i < 8; ++i) *s = __builtin_fma((double)f[i], (double)f[i], *s);
 }
 
-// Partial sums of squares of the group's matrices: parts of each.
+// Partial sums of squares of the group's matrices: parts of each.  4,096 x 4,096 bf16 take
+// 9 us, 3.6 TB/s.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void ns_sumsq_kernel(const void* x, int64_t stride, int64_t batch, int64_t rows, int64_t cols,
                                                             int32_t row_threads, double* partial) {
@@ -561,7 +568,8 @@ __global__ __launch_bounds__(kThreads) void ns_sumsq_kernel(const void* x, int64
 
 // The mean gradient over the ranks, the momentum, and the update u before it is
 // orthogonalised, with its partial sums of squares.  Rows are summed in rank
-// order, in fp32.
+// order, in fp32.  Bound by HBM: 28 bytes an element of 8 rows, 5.8 TB/s (283 us for
+// 14,336 x 4,096).
 struct MomentumArgs {
     StepArgs step;                  // from the group's first matrix on
     int64_t each;                   // elements of a matrix
@@ -638,7 +646,8 @@ __global__ __launch_bounds__(64) void ns_norm_kernel(const double* partial, int3
 }
 
 // X0 in two fp16 parts and in the wide orientation.  A workgroup takes 64 rows and
-// 64 columns of it; a tall matrix is turned in LDS.
+// 64 columns of it; a tall matrix is turned in LDS.  1,600 x 6,400 of fp32 take 14 us, 5.8
+// TB/s; turned, 14,336 x 4,096 119 us, 3.9 TB/s: half of its LDS cycles are conflicts.
 struct PackArgs {
     const void* x;
     int64_t stride, batch, m, n, np;
@@ -702,7 +711,8 @@ struct SmallArgs {
 };
 // The 16-byte chunk c of row r sits in slot c ^ f(r): 8 rows read at one chunk fall
 // into different banks, and so do the 32 bytes that a transposing read takes of each of
-// 4 rows.
+// 4 rows.  Half of the kernel's LDS cycles are conflicts still; an f of more bits, for 16
+// lanes at a time, needs more registers than there are and took a tenth longer.
 __device__ __forceinline__ int small_slot(int row, int chunk) { return chunk ^ ((row & 3) << 1 | (row >> 2 & 1)); }
 // Where a lane reads its operand registers of 16 rows (or, OUTER, columns) and k =
 // 8 (lane / 16) + 0..7 of the hi parts at the matrix's corner; LD: bytes of a row.  The
@@ -809,7 +819,9 @@ __device__ __forceinline__ void by_dtype(int32_t dtype, F each) {
     else each(std::integral_constant<int, ZSMR_FP32>());
 }
 
-// A matrix of at most MP x NP.  The plain call reads and writes each register's four
+// A matrix of at most MP x NP.  A product waits for the one before it, so a CU's matrix
+// units are busy 0.15 (64 x 64) to 0.29 (128 x 128) of the time; 24 of 64 x 64 take 16.1 us
+// where 15 launches of products would take 92.  The plain call reads and writes each register's four
 // elements where they lie.  The shard's step (STEP) has nrows + 2 arrays of the matrix's
 // shape to read and three to write, so it takes memory in its own order, eight elements of
 // a row a thread, and the matrix changes hands in LDS, as fp32 rows a little longer than
