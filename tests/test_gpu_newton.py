@@ -248,6 +248,22 @@ def test_in_place(count, rows, cols):
     assert torch.equal(x, want)
 
 
+@pytest.mark.parametrize("rows,cols", [(40, 72), (130, 150)])
+def test_matrices_past_32_bits(rows, cols):
+    far = (1 << 32) + 24
+    try:
+        big = torch.empty(far + rows * cols, device="cuda", dtype=BF16)
+    except torch.cuda.OutOfMemoryError:
+        pytest.skip("needs 9 GB")
+    x = matrices(13, 2, rows, cols, dtype=BF16)
+    apart = big.as_strided((2, rows, cols), (far, cols, 1))
+    apart.copy_(x)
+    want = call(x, torch.empty_like(x))
+    assert torch.equal(call(apart, torch.empty_like(x)), want)
+    call(x, apart)
+    assert torch.equal(apart, want)
+
+
 def test_calls_at_once_and_graphs_that_share_a_workspace():
     x = [matrices(12 + k, 2, 150, 1700) for k in range(2)]
     want = [call(t, torch.empty_like(t)) for t in x]

@@ -181,6 +181,25 @@ def test_alternatives_of_a_masked_row(v):
     assert x[2, 0].abs() < 11 and out["top_logprobs"][2, 0].abs() <= 2.0 ** -24 * 16
 
 
+def test_rows_past_32_bits():
+    """The last rows lie more than 2^32 elements from the first."""
+    n, v, stride = 2060, 1000, 1 << 21
+    try:
+        big = torch.empty(n * stride, device="cuda", dtype=BF16)
+    except torch.cuda.OutOfMemoryError:
+        pytest.skip("needs 9 GB")
+    x, ids = logits(19, n, v, BF16)
+    far = big.view(n, stride)[:, :v]
+    far.copy_(x)
+    got, want = score(far, ids, 5), score(x, ids, 5)
+    assert all(torch.equal(got[k], want[k]) for k in want)
+    g = torch.randn(n, device="cuda", generator=gen(20))
+    dx = torch.empty_like(x)
+    z.zsmr_logprobs_grad(x, ids, want["lse"], want["entropy"], dx, g, -g)
+    z.zsmr_logprobs_grad(far, ids, want["lse"], want["entropy"], far, g, -g)
+    assert torch.equal(far, dx)
+
+
 def test_calls_on_two_streams_at_once():
     x, ids = logits(18, 40, 128256, BF16)
     want = score(x, ids, 9)
