@@ -647,7 +647,8 @@ __global__ __launch_bounds__(64) void ns_norm_kernel(const double* partial, int3
 
 // X0 in two fp16 parts and in the wide orientation.  A workgroup takes 64 rows and
 // 64 columns of it; a tall matrix is turned in LDS.  1,600 x 6,400 of fp32 take 14 us, 5.8
-// TB/s; turned, 14,336 x 4,096 119 us, 3.9 TB/s: half of its LDS cycles are conflicts.
+// TB/s; turned, 14,336 x 4,096 105 us, 4.5 TB/s (rows of tiles along n 114, rows of 65 in
+// LDS 119).
 struct PackArgs {
     const void* x;
     int64_t stride, batch, m, n, np;
@@ -657,34 +658,49 @@ struct PackArgs {
 };
 template <int DT>
 __global__ __launch_bounds__(kThreads) void ns_pack_kernel(PackArgs a) {
-    __shared__ float turned[64][65];
+    // element (row, column) of the wide orientation's tile, in 16-byte chunks of a row
+    // that change places: the writes of a column and the reads of two rows use all banks
+    __shared__ __attribute__((aligned(16))) float turned[64 * 64];
+    auto chunk_at = [&](int row, int chunk) { return row * 64 + (chunk ^ (row >> 3) ^ (row & 1)) * 4; };
     const int64_t matrix = blockIdx.x / a.tiles;
     const int tile = blockIdx.x % a.tiles;
-    const int64_t m0 = tile / a.tiles_n * 64, n0 = (int64_t)(tile % a.tiles_n) * 64;
-    const double inverse = a.inverse[matrix];
+    int tm = tile / a.tiles_n, tn = tile % a.tiles_n;
+    if (a.tall) {
+        // 8 tiles along n, then the next ones along m: pages of both matrices are used whole
+        const int tiles_m = a.tiles / a.tiles_n, band = tile / (8 * tiles_m), width = min(8, a.tiles_n - band * 8), in_band = tile - band * 8 * tiles_m;
+        tm = in_band / width;
+        tn = band * 8 + in_band % width;
+    }
+    const int64_t m0 = (int64_t)tm * 64, n0 = (int64_t)tn * 64;
     const int64_t rows = a.tall ? a.n : a.m, cols = a.tall ? a.m : a.n, r0 = a.tall ? n0 : m0, c0 = a.tall ? m0 : n0;
     uint16_t* dst = a.dst + matrix * a.m * a.np * 2;
+    f32x8 f[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int r = k * 32 + threadIdx.x / 8, c = threadIdx.x % 8 * 8;
-        f32x8 f = 0.f;
+        f[k] = 0.f;
         if (r0 + r < rows) {
             const int64_t e = matrix * a.batch + (r0 + r) * a.stride + c0 + c;
             if (c0 + c + 8 <= cols) {
-                f = load8<DT>(a.x, e);
+                f[k] = load8<DT>(a.x, e);
             } else {
 #pragma unroll
                 for (int i = 0; i < 7; ++i)
-                    if (c0 + c + i < cols) f[i] = load1<DT>(a.x, e + i);
+                    if (c0 + c + i < cols) f[k][i] = load1<DT>(a.x, e + i);
             }
         }
+    }
+    const double inverse = a.inverse[matrix];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = (float)((double)f[i] * inverse);
+    for (int k = 0; k < 2; ++k) {
+        const int r = k * 32 + threadIdx.x / 8, c = threadIdx.x % 8 * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[k][i] = (float)((double)f[k][i] * inverse);
         if (!a.tall) {
-            if (r0 + r < rows && c0 + c < a.np) store_split(dst, split_at(r0 + r, c0 + c, a.np * 2), f);
+            if (r0 + r < rows && c0 + c < a.np) store_split(dst, split_at(r0 + r, c0 + c, a.np * 2), f[k]);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) turned[c + i][r] = f[i];
+            for (int i = 0; i < 8; ++i) turned[chunk_at(c + i, r / 4) + r % 4] = f[k][i];
         }
     }
     if (!a.tall) return;
@@ -693,10 +709,9 @@ __global__ __launch_bounds__(kThreads) void ns_pack_kernel(PackArgs a) {
     for (int k = 0; k < 2; ++k) {
         const int r = k * 32 + threadIdx.x / 8, c = threadIdx.x % 8 * 8;
         if (m0 + r >= a.m || n0 + c >= a.np) continue;
-        f32x8 f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = turned[r][c + i];
-        store_split(dst, split_at(m0 + r, n0 + c, a.np * 2), f);
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(turned + chunk_at(r, c / 4)), hi = *reinterpret_cast<const f32x4*>(turned + chunk_at(r, c / 4 + 1));
+        const f32x8 t = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        store_split(dst, split_at(m0 + r, n0 + c, a.np * 2), t);
     }
 }
 
