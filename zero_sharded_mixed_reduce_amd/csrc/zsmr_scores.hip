@@ -30,30 +30,51 @@ constexpr float kEdge = 2.3e38f * kLog2e;
 // multiply-add: d = x c - ref.  A part of a softmax is its reference (finite), the sum
 // of 2^d and the sum of 2^d d.  A reference follows the largest logit only when a lane's
 // eight powers pass 2^10: their sizes cost no accuracy, and no maximum has to be taken.
-struct Stats {
-    float ref, sum, mean;
+//
+// A reference is the product x c of a logit x, rounded to fp32: for x itself d is that
+// rounding and not 0.  References of the streaming pass stay within kNear, where it is a
+// 32nd at most; logits far below that add nothing there, logits far above an infinity.
+// What is left without a sum, or with a huge one, is a row (or a segment of one) far from
+// zero, and a second pass takes its largest logit with the product's other part, `low`:
+// d = x c - ref - low.  From 3e9 on the power of that part is infinite or zero.
+struct Ref {
+    float ref, low;
 };
+struct Stats {
+    float ref, low, sum, mean;
+};
+constexpr float kNear = 0x1p20f, kTinySum = 0x1p-64f, kHugeSum = 0x1p64f;
 __device__ __forceinline__ float power_of(float d) { return __builtin_amdgcn_exp2f(d); }
 __device__ __forceinline__ float log2_of(float x) { return __builtin_amdgcn_logf(x); }
 __device__ __forceinline__ float fused(float a, float b, float c) { return __builtin_fmaf(a, b, c); }
-__device__ __forceinline__ Stats moved(Stats a, float ref) {
+// FAR: references may have a low part.
+template <bool FAR>
+__device__ __forceinline__ Stats moved(Stats a, Ref to) {
     // a part without a sum (no logit above -infinity) has any reference
-    if (a.sum == 0.f) return Stats{ref, 0.f, 0.f};
-    const float d = a.ref - ref, f = power_of(d);
-    return Stats{ref, a.sum * f, f == 0.f ? 0.f : f * fused(d, a.sum, a.mean)};
+    if (a.sum == 0.f) return Stats{to.ref, to.low, 0.f, 0.f};
+    const float d = FAR ? a.ref - to.ref + (a.low - to.low) : a.ref - to.ref, f = power_of(d);
+    // an infinite sum, of logits past the range, stays one
+    const float sum = FAR && a.sum == INFINITY ? a.sum : a.sum * f;
+    return Stats{to.ref, to.low, sum, f == 0.f ? 0.f : f * fused(d, a.sum, a.mean)};
 }
+template <bool FAR>
 __device__ __forceinline__ Stats join_stats(Stats a, Stats b) {
-    const float ref = a.sum == 0.f ? b.ref : b.sum == 0.f ? a.ref : fmaxf(a.ref, b.ref);
-    a = moved(a, ref);
-    b = moved(b, ref);
-    return Stats{ref, a.sum + b.sum, a.mean + b.mean};
+    const bool larger = FAR ? b.ref > a.ref || (b.ref == a.ref && b.low > a.low) : b.ref > a.ref;
+    const bool to_b = a.sum == 0.f || (b.sum != 0.f && larger);
+    const Ref to{to_b ? b.ref : a.ref, FAR ? to_b ? b.low : a.low : 0.f};
+    a = moved<FAR>(a, to);
+    b = moved<FAR>(b, to);
+    return Stats{to.ref, to.low, a.sum + b.sum, a.mean + b.mean};
 }
 // Eight logits of a lane.
-__device__ __forceinline__ void add_powers(const f32x8& x, float c, float ref, float* sum, float* mean) {
+template <bool FAR>
+__device__ __forceinline__ void add_powers(const f32x8& x, float c, Ref to, float* sum, float* mean) {
     float s = 0.f, m = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float d = fused(x[i], c, -ref), e = power_of(d);
+        float d = fused(x[i], c, -to.ref);
+        if (FAR) d -= to.low;
+        const float e = power_of(d);
         s += e;
         m = fused(e, fmaxf(d, -200.f), m);      // 0 times -infinity is 0
     }
@@ -66,15 +87,19 @@ __device__ __forceinline__ float largest(const f32x8& x) {
     for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i]);
     return top;
 }
-__device__ __forceinline__ float reference(float top, float c) { return __builtin_amdgcn_fmed3f(top * c, -kEdge, kEdge); }
+__device__ __forceinline__ float reference(float top, float c) { return __builtin_amdgcn_fmed3f(top * c, -kNear, kNear); }
+__device__ __forceinline__ Ref far_reference(float top, float c) {
+    const float product = top * c;
+    return Ref{__builtin_amdgcn_fmed3f(product, -kEdge, kEdge), fabsf(product) <= kEdge ? fused(top, c, -product) : 0.f};
+}
 __device__ __forceinline__ void add_logits(Stats& s, const f32x8& x, float c) {
     float sum, mean;
-    add_powers(x, c, s.ref, &sum, &mean);
+    add_powers<false>(x, c, Ref{s.ref, 0.f}, &sum, &mean);
     if (sum > 1024.f) {
         const float ref = reference(largest(x), c);
         if (ref > s.ref) {
-            s = moved(s, ref);
-            add_powers(x, c, s.ref, &sum, &mean);
+            s = moved<false>(s, Ref{ref, 0.f});
+            add_powers<false>(x, c, Ref{ref, 0.f}, &sum, &mean);
         }
     }
     s.sum += sum;
@@ -165,9 +190,21 @@ __device__ __forceinline__ float largest_of(float x, int lanes) {
 }
 template <int D>
 __device__ __forceinline__ Stats joined(Stats s) {
-    s = join_stats(s, Stats{across<D>(s.ref), across<D>(s.sum), across<D>(s.mean)});
+    s = join_stats<false>(s, Stats{across<D>(s.ref), 0.f, across<D>(s.sum), across<D>(s.mean)});
     if constexpr (D < 32) return joined<D * 2>(s);
     else return s;
+}
+template <int D = 1>
+__device__ __forceinline__ float wave_largest(float x) {
+    x = fmaxf(x, across<D>(x));
+    if constexpr (D < 32) return wave_largest<D * 2>(x);
+    else return x;
+}
+template <int D = 1>
+__device__ __forceinline__ float wave_sum(float x) {
+    x += across<D>(x);
+    if constexpr (D < 32) return wave_sum<D * 2>(x);
+    else return x;
 }
 
 // ------------------------------------------------------------------- forward --
@@ -184,7 +221,7 @@ __device__ __forceinline__ void put_token(const ForwardArgs& f, int64_t t, Stats
     const ScoreArgs& a = f.a;
     const float log_sum = log2_of(s.sum);
     const bool none = s.sum == 0.f;
-    if (a.lse) a.lse[t] = none ? -INFINITY : (s.ref + log_sum) * kLn2;
+    if (a.lse) a.lse[t] = none ? -INFINITY : (s.ref + (s.low + log_sum)) * kLn2;
     if (a.entropy) a.entropy[t] = none ? 0.f : (log_sum - s.mean / s.sum) * kLn2;
     if (a.logprob) {
         const int32_t id = token_at(a.ids, a.id_bytes, t, a.vocab);
@@ -192,7 +229,7 @@ __device__ __forceinline__ void put_token(const ForwardArgs& f, int64_t t, Stats
         if (id >= 0) {
             const int64_t e = t * a.stride + id;
             const float x = a.dtype == ZSMR_BF16 ? load1<ZSMR_BF16>(a.logits, e) : a.dtype == ZSMR_FP16 ? load1<ZSMR_FP16>(a.logits, e) : load1<ZSMR_FP32>(a.logits, e);
-            r = none ? -INFINITY : (fused(x, f.c, -s.ref) - log_sum) * kLn2;
+            r = none ? -INFINITY : (fused(x, f.c, -s.ref) - s.low - log_sum) * kLn2;
         }
         a.logprob[t] = r;
     }
@@ -208,7 +245,7 @@ __device__ __forceinline__ void put_top(const ForwardArgs& f, int64_t t, Stats s
         else static_cast<int32_t*>(a.top_ids)[e] = id;
     }
     if (a.top_logprobs)
-        a.top_logprobs[e] = key && s.sum != 0.f ? (fused(value_of((uint32_t)(key >> 32)), f.c, -s.ref) - log2_of(s.sum)) * kLn2 : -INFINITY;
+        a.top_logprobs[e] = key && s.sum != 0.f ? (fused(value_of((uint32_t)(key >> 32)), f.c, -s.ref) - s.low - log2_of(s.sum)) * kLn2 : -INFINITY;
 }
 
 // A wave's block of 512 logits, eight a lane: 16 bytes a lane and load, which covers a
@@ -265,7 +302,7 @@ __global__ __launch_bounds__(kWaves * 64, 8) void scores_kernel(ForwardArgs f) {
     __shared__ uint32_t groups[64];
     __shared__ Stats part[kWaves];
 
-    Stats s{-kEdge, 0.f, 0.f};
+    Stats s{-kNear, 0.f, 0.f, 0.f};
     bool sorted = false;
     uint64_t keys = 0;                  // the wave's best, sorted
     float above = -INFINITY;            // a logit has to be above it to be among the best
@@ -368,6 +405,52 @@ __global__ __launch_bounds__(kWaves * 64, 8) void scores_kernel(ForwardArgs f) {
     s = joined<1>(s);
     if (lane == 0) part[wave] = s;
     __syncthreads();
+    bool tiny = true, huge = false;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        tiny = tiny && part[i].sum < kTinySum;
+        huge = huge || part[i].sum > kHugeSum;
+    }
+    if (tiny || huge) {         // far from zero, or masked: again, from the largest logit
+        auto blocks = [&](auto each) {
+            for (int64_t c = first + wave * kScoreBlock; c < end; c += step) {
+                f32x8 x;
+                if (c + kScoreBlock <= end) {
+                    now.load(a.logits, row + c);
+                    x = now.values();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int64_t e = c + Block<DT>::index(i);
+                        x[i] = e < end ? load1<DT>(a.logits, row + e) : -INFINITY;
+                    }
+                }
+                each(x);
+            }
+        };
+        float top = -INFINITY;
+        blocks([&](const f32x8& x) { top = fmaxf(top, largest(x)); });
+        top = wave_largest(top);
+        __syncthreads();        // every wave has read the sums
+        if (lane == 0) part[wave].ref = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) top = fmaxf(top, part[i].ref);
+        const Ref to = far_reference(top, f.c);
+        float sum = 0.f, mean = 0.f;
+        if (top * f.c >= -kEdge)        // else nothing but masks
+            blocks([&](const f32x8& x) {
+                float e, m;
+                add_powers<true>(x, f.c, to, &e, &m);
+                sum += e;
+                mean += m;
+            });
+        sum = wave_sum(sum);
+        mean = wave_sum(mean);
+        __syncthreads();        // every wave has read the largest
+        if (lane == 0) part[wave] = Stats{to.ref, to.low, sum, mean};
+        __syncthreads();
+    }
     if constexpr (TOP) {
         // what is above the last bound, of the staged and of the best, to the front
         const uint32_t bound = shared_bound;
@@ -403,10 +486,12 @@ __global__ __launch_bounds__(kWaves * 64, 8) void scores_kernel(ForwardArgs f) {
     }
     if (wave) return;
     s = part[0];
+    // references are one value, or have no low part
 #pragma unroll
-    for (int i = 1; i < kWaves; ++i) s = join_stats(s, part[i]);
+    for (int i = 1; i < kWaves; ++i) s = join_stats<false>(s, part[i]);
+    s.low = part[0].low;
     if (f.stats) {
-        if (lane == 0) f.stats[blockIdx.x] = make_float4(s.ref, s.sum, s.mean, 0.f);
+        if (lane == 0) f.stats[blockIdx.x] = make_float4(s.ref, s.low, s.sum, s.mean);
         if (TOP && lane < a.top) f.keys[(int64_t)blockIdx.x * a.top + lane] = keys;
     } else {
         if (lane == 0) put_token(f, t, s);
@@ -422,11 +507,11 @@ __global__ __launch_bounds__(kJoinWaves * 64) void scores_join_kernel(ForwardArg
     __shared__ Stats part[kJoinWaves];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int64_t t = blockIdx.x;
-    Stats s{-kEdge, 0.f, 0.f};
+    Stats s{-kEdge, 0.f, 0.f, 0.f};
     uint64_t keys = 0;
     for (int i = wave; i < f.splits; i += kJoinWaves) {
         const float4 v = f.stats[t * f.splits + i];
-        s = join_stats(s, Stats{v.x, v.y, v.z});
+        s = join_stats<true>(s, Stats{v.x, v.y, v.z, v.w});
         if (TOP) keys = merge64(keys, lane < f.a.top ? f.keys[(t * f.splits + i) * f.a.top + lane] : 0);
     }
     if (lane == 0) part[wave] = s;
@@ -439,7 +524,7 @@ __global__ __launch_bounds__(kJoinWaves * 64) void scores_join_kernel(ForwardArg
     if (wave) return;
     s = part[0];
 #pragma unroll
-    for (int i = 1; i < kJoinWaves; ++i) s = join_stats(s, part[i]);
+    for (int i = 1; i < kJoinWaves; ++i) s = join_stats<true>(s, part[i]);
     if (lane == 0) put_token(f, t, s);
     if (TOP) put_top(f, t, s, keys);
 }
