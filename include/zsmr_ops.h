@@ -272,7 +272,8 @@ int32_t zsmr_logprobs(const void* logits, int64_t stride, int32_t dtype, const v
  * gradient of sum (g * logprob + h * entropy), in the format of the logits, whose
  * memory it may share (the same address and stride).  g and h: n_tokens fp32 each, or
  * NULL for zeros; entropy may be NULL where h is, ids where g is.  lse and entropy
- * are what zsmr_logprobs left. */
+ * are what zsmr_logprobs left.  An lse in fp32 holds less of log p the larger it is: a row
+ * of |lse| above 512 (fp16), 4,096 (bf16) or 64 (fp32) is summed again from its logits. */
 int32_t zsmr_logprobs_grad(const void* logits, int64_t stride, int32_t dtype, const void* ids,
                            int32_t id_bytes, int64_t n_tokens, int64_t vocab, float scale,
                            const float* lse, const float* entropy, const float* g, const float* h,

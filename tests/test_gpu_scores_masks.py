@@ -1,5 +1,5 @@
-"""Scores of logits with finite masks and of rows far from zero, against
-64 bits.
+"""Scores of logits with finite masks and of rows far from zero, and their gradient,
+against 64 bits.
 
 Tolerances.  A term 2^d, d = (x - x_ref) scale log2 e, has the roundings of the
 constant, of d and of the power; terms of |z - z_ref| up to 40 count, so its relative
@@ -13,7 +13,8 @@ ln 2 itself; logprob has as many of its own.
 import pytest
 import torch
 
-from tests.test_gpu_scores import BF16, F16, F32, INF, best, gen, near, score
+import zero_sharded_mixed_reduce_amd as z
+from tests.test_gpu_scores import BF16, F16, F32, HALF_STEP, INF, best, gen, near, score
 
 pytestmark = pytest.mark.gpu
 
@@ -105,3 +106,56 @@ def test_rows_far_from_zero(dtype, at, v, many):
     x, ids = far_rows(dtype, v, many, at)
     for scale in (0.3, 1.0, 1.25):
         check(x, ids, 5, scale)
+
+
+def check_gradient(x, ids, scale, what="gh", into=None):
+    """The gradient where lse and entropy are what the forward pass left.
+
+    p has the relative error of log p: `sums`, half steps of 2^-24 of d and of its
+    product, and of lse (as in `check`) up to the size from which a row is summed again.  log p and H have those errors themselves; four roundings of the terms, the
+    results' own, and powers below 2^-126 are zero."""
+    out, ref, (n, v) = score(x, ids, 0, scale), reference(x, ids, scale), x.shape
+    g = torch.randn(n, generator=gen(11), device="cuda") if "g" in what else None
+    h = torch.randn(n, generator=gen(12), device="cuda") if "h" in what else None
+    raw = x.clone()
+    d = torch.empty_like(x) if into is None else into
+    z.zsmr_logprobs_grad(x, ids, out["lse"], out["entropy"], d, dlogprob=g, dentropy=h, scale=scale)
+    ok = (ids >= 0) & (ids < v)
+    gg = torch.where(ok, g.double(), 0.0)[:, None] if g is not None else torch.zeros(n, 1, device="cuda")
+    hh = h.double()[:, None] if h is not None else torch.zeros(n, 1, device="cuda")
+    hit = torch.zeros(n, v, device="cuda", dtype=torch.float64).scatter_(1, torch.where(ok, ids, 0)[:, None], 1.0)
+    p, entropy = ref["p"], ref["entropy"][:, None]
+    logp = torch.where(p > 0, ref["logp"], 0.0)
+    want = scale * (gg * hit - p * (gg + hh * (logp + entropy)))
+    want[ref["lse"] == -INF] = 0
+    tol = sums(n, v)
+    off = tol + 2.0 ** -24 * (5 * size(ref["lse"])[:, None].clamp(max={F32: 64, F16: 512, BF16: 4096}[x.dtype]) + 6 * logp.abs())
+    terms = gg.abs() + hh.abs() * (logp.abs() + entropy)
+    slack = scale * (p * (off * terms + hh.abs() * (off + tol * (1 + entropy))) + 2.0 ** -22 * (p * terms + gg.abs() * hit) + 2.0 ** -126 * (terms + 100 * hh.abs()))
+    slack = slack + want.abs() * HALF_STEP[x.dtype] + (2.0 ** -25 if x.dtype is F16 else 0.0)
+    bad = ~((d.double() - want).abs() <= slack)
+    assert not bad.any(), (bad.any(1).nonzero()[:5, 0], d[bad][:5], want[bad][:5])
+    return d, raw, out, g, h
+
+
+@pytest.mark.parametrize("v,many", SHAPES)
+@pytest.mark.parametrize("dtype,mask", MASKS)
+def test_gradient_of_finite_masks(dtype, mask, v, many):
+    x, ids = masked(dtype, v, many, mask)
+    for scale in (0.25, 0.5, 0.65, 1.0, 1.25):
+        check_gradient(x, ids, scale)
+
+
+@pytest.mark.parametrize("v,many", SHAPES)
+@pytest.mark.parametrize("dtype,at", FAR + [(t, a) for t in (F16, BF16, F32) for a in (40.0, -90.0, 300.0, -600.0, 1500.0, 6e3, -6e3)])
+def test_gradient_of_rows_far_from_zero(dtype, at, v, many):
+    x, ids = far_rows(dtype, v, many, at)
+    for scale, what in ((0.3, "gh"), (1.0, "g"), (1.25, "h")):
+        check_gradient(x, ids, scale, what)
+    # in place, and through a view with rows apart
+    d, raw, out, g, h = check_gradient(x, ids, 1.0)
+    z.zsmr_logprobs_grad(x, ids, out["lse"], out["entropy"], x, dlogprob=g, dentropy=h)
+    assert torch.equal(x, d)
+    wide = torch.full((len(x), v + 9), 4.0, device="cuda", dtype=dtype)
+    z.zsmr_logprobs_grad(raw, ids, out["lse"], out["entropy"], wide[:, 3:3 + v], dlogprob=g, dentropy=h)
+    assert torch.equal(wide[:, 3:3 + v], d) and (wide[:, :3] == 4).all() and (wide[:, 3 + v:] == 4).all()

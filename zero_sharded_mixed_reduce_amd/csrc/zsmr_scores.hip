@@ -534,6 +534,14 @@ __global__ __launch_bounds__(kJoinWaves * 64) void scores_join_kernel(ForwardArg
 // 8,192 rows of 128,256 bf16: 685 us, 6.1 TB/s.
 // ds = g' [v = id] - p (g' + h' (log p + H)) with g' = scale g and h' = scale h, log p in
 // the base 2 that the power needs.
+//
+// log p = scale s - lse has one rounding of its own, but lse, rounded to fp32, is off by up
+// to 4.3 * 2^-24 of its size (its constant, reference, sum and product with ln 2), and p
+// by as much: at 512 and 4,096 a quarter of what fp16's and bf16's results may be off, at 64
+// 1.6e-5.  A row further from zero than that gets the sum again from its largest logit, by
+// one workgroup that then writes all of it; at -1e9 lse holds no log p at all.
+template <int DT>
+constexpr float kFarLse = DT == ZSMR_FP32 ? 64.f : DT == ZSMR_FP16 ? 512.f : 4096.f;
 constexpr int kGradThreads = 256, kGradTurns = 4, kGradBlock = kGradThreads * kGradTurns * 8;
 struct GradArgs {
     ScoreArgs a;
@@ -541,20 +549,83 @@ struct GradArgs {
     int64_t last_row;               // rows go from the last one up: the forward pass read them last
     int32_t blocks;                 // of a row
 };
+// A whole row by one workgroup: the largest logit, the sum, then the results, which may
+// take the logits' place.  8,192 such rows of 128,256 bf16 take 1.58 ms (others 0.69), 16
+// of them 31 us (5).
+template <int DT, typename F>
+__device__ __forceinline__ void far_row(const ScoreArgs& a, float c, int64_t t, int32_t id, float g, F slope_at) {
+    __shared__ float part[2][kGradThreads / 64];
+    const int64_t row = t * a.stride, to = t * a.dstride;
+    auto every = [&](auto each) {
+        int64_t v = threadIdx.x * 8;
+        for (; v - threadIdx.x * 8 + kGradBlock <= a.vocab; v += kGradBlock) {
+            f32x8 x[kGradTurns];
+#pragma unroll
+            for (int k = 0; k < kGradTurns; ++k) x[k] = load8<DT>(a.logits, row + v + k * kGradThreads * 8);
+#pragma unroll
+            for (int k = 0; k < kGradTurns; ++k) each(v + k * kGradThreads * 8, 8, x[k]);
+        }
+        for (; v < a.vocab; v += kGradThreads * 8) {
+            const int count = (int)min((int64_t)8, a.vocab - v);
+            f32x8 x = -INFINITY;
+            if (count == 8) {
+                x = load8<DT>(a.logits, row + v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 7; ++i)
+                    if (i < count) x[i] = load1<DT>(a.logits, row + v + i);
+            }
+            each(v, count, x);
+        }
+    };
+    const int wave = threadIdx.x / 64;
+    float top = -INFINITY, sum = 0.f;
+    every([&](int64_t, int, const f32x8& x) { top = fmaxf(top, largest(x)); });
+    top = wave_largest(top);
+    if (threadIdx.x % 64 == 0) part[0][wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kGradThreads / 64; ++i) top = fmaxf(top, part[0][i]);
+    every([&](int64_t, int, const f32x8& x) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += power_of((x[i] - top) * c);
+    });
+    sum = wave_sum(sum);
+    if (threadIdx.x % 64 == 0) part[1][wave] = sum;
+    __syncthreads();
+    sum = part[1][0];
+#pragma unroll
+    for (int i = 1; i < kGradThreads / 64; ++i) sum += part[1][i];
+    const float log_sum = log2_of(sum);
+    every([&](int64_t v, int count, const f32x8& x) {
+        f32x8 d;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = slope_at((x[i] - top) * c - log_sum) + (v + i == id ? g : 0.f);
+        if (count == 8) {
+            store8<DT>(a.dlogits, to + v, d);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+                if (i < count) store1<DT>(a.dlogits, to + v + i, d[i]);
+        }
+    });
+}
+// Six waves a SIMD: with eight the same rows take 0.76 ms, with five 0.77.
 template <int DT, bool STREAM>
-__global__ __launch_bounds__(kGradThreads) void scores_grad_kernel(GradArgs f) {
+__global__ __launch_bounds__(kGradThreads, 6) void scores_grad_kernel(GradArgs f) {
     const ScoreArgs& a = f.a;
     const int64_t t = f.last_row - blockIdx.x / f.blocks, c0 = (int64_t)(blockIdx.x % f.blocks) * kGradBlock;
     const int32_t id = a.ids && a.dlogprob ? token_at(a.ids, a.id_bytes, t, a.vocab) : -1;
     const float g = id >= 0 ? a.dlogprob[t] * a.scale : 0.f, h = a.dentropy ? a.dentropy[t] * a.scale : 0.f;
-    const float lse = a.lse[t], ref = lse * kLog2e, slope = h * kLn2, base = a.dentropy ? g + h * a.entropy[t] : g;
-    const bool none = lse < -1e30f;     // a row whose logits are all masked
-    auto one = [&](float x) {
-        // 16-bit logits: the error of lse log2 e, 1.2e-6 of p for an lse of 20, is below their
-        // result's; fp32 ones take the difference first
-        const float d = DT == ZSMR_FP32 ? (x * a.scale - lse) * kLog2e : fused(x, f.c, -ref), p = power_of(d);
-        return -p * fused(slope, fmaxf(d, -200.f), base);
-    };
+    const float lse = a.lse[t], slope = h * kLn2, base = a.dentropy ? g + h * a.entropy[t] : g;
+    const bool none = lse == -INFINITY; // a row whose logits are all masked
+    auto slope_at = [&](float d) { return -power_of(d) * fused(slope, fmaxf(d, -200.f), base); };
+    if (fabsf(lse) > kFarLse<DT> && fabsf(lse) < INFINITY) {
+        // another block of every row: a row's first ones may all be on one XCD
+        if (blockIdx.x % f.blocks == t % f.blocks) far_row<DT>(a, f.c, t, id, g, slope_at);
+        return;
+    }
+    auto one = [&](float x) { return slope_at(fused(x, a.scale, -lse) * kLog2e); };
     const int64_t e0 = t * a.stride + c0, o0 = t * a.dstride + c0;
     const int64_t left = a.vocab - c0;
     f32x8 x[kGradTurns];
