@@ -17,6 +17,7 @@ void launch_rows(int64_t rows, int64_t items, F each) {
     const int64_t most = kMaxGroups * 256 / items;
     for (int64_t first = 0; first < rows; first += most) each(first, rows - first < most ? rows - first : most);
 }
+// Workgroups of 256.
 template <typename F>
 void launch_groups(int64_t groups, F each) {
     launch_rows(groups, 256, each);

@@ -7,6 +7,7 @@
 #include <algorithm>
 
 #include "zsmr_ops.h"
+#include "zsmr_ops_launch.h"
 
 namespace zsmr {
 
@@ -34,6 +35,11 @@ inline ScoreShape score_shape(int64_t tokens, int64_t vocab, int64_t top) {
     s.splits = (int)((vocab + s.segment - 1) / s.segment);
     if (s.splits > 1) s.bytes = tokens * s.splits * (16 + 8 * top);
     return s;
+}
+// The launches over all segments: each(first, count) workgroups.
+template <typename F>
+void score_launches(const ScoreShape& s, int64_t tokens, F each) {
+    launch_rows(tokens * s.splits, s.waves * 64, each);
 }
 
 }  // namespace zsmr
