@@ -31,7 +31,17 @@ static int launches(int64_t t, int64_t v) {
     return n;
 }
 
+// Rows in segments: one launch, whose workgroups one launch of the join follows.
+static void segments(int64_t t, int64_t v) {
+    const ScoreShape s = score_shape(t, v, 64);
+    CHECK(s.splits >= 1 && (s.splits == 1 || t * s.splits <= kScoreSplits));
+    CHECK(s.splits == 1 || launches(t, v) == 1);
+    CHECK((s.splits - 1) * s.segment < v && s.splits * s.segment >= v);
+}
+
 int main() {
+    for (int64_t t = 1; t <= 1100; ++t)
+        for (int64_t v : {1, 8191, 8192, 65536, 65537, 70000, 100000, 128256, 500000, 2097151, 2097152}) segments(t, v);
     for (int64_t t : {1, 2, 16, 255, 256, 257, 4096, 1 << 20, (1 << 23) - 1, 1 << 23, (1 << 23) + 1, 10000000, 1 << 24})
         for (int64_t v : {1, 500, 8191, 8192, 50257, 128256, 1 << 21}) launches(t, v);
     const int64_t t = 1 << 24, v = 8192;

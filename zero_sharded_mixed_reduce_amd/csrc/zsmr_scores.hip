@@ -679,7 +679,7 @@ void gradient(const GradArgs& f, unsigned grid, bool stream_out, hipStream_t str
 
 hipError_t launch_logprobs(const ScoreArgs& a, void* ws, hipStream_t stream) {
     const ScoreShape s = score_shape(a.tokens, a.vocab, a.top);
-    // with splits there are 1,024 workgroups at most
+    // with splits there are kScoreSplits workgroups at most, one launch
     score_launches(s, a.tokens, [&](int64_t first, int64_t count) {
         ForwardArgs f{};
         f.a = a;

@@ -13,6 +13,8 @@ namespace zsmr {
 
 // A wave reads blocks of 512 elements, 8 a lane.
 constexpr int kScoreBlock = 512;
+// Segments of all rows together, where rows are cut.
+constexpr int64_t kScoreSplits = 512;
 
 struct ScoreShape {
     int waves;                  // of a workgroup, 8 or 2
@@ -30,7 +32,7 @@ inline ScoreShape score_shape(int64_t tokens, int64_t vocab, int64_t top) {
     ScoreShape s{};
     s.waves = vocab < 16 * kScoreBlock && tokens > 256 ? 2 : 8;
     const int64_t most = std::max<int64_t>(1, vocab / (2 * kScoreBlock * s.waves));
-    const int64_t want = vocab <= 16 * kScoreBlock * s.waves ? 1 : std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(tokens, 1), most));
+    const int64_t want = vocab <= 16 * kScoreBlock * s.waves ? 1 : std::max<int64_t>(1, std::min<int64_t>(kScoreSplits / std::max<int64_t>(tokens, 1), most));
     s.segment = ((vocab + want - 1) / want + kScoreBlock - 1) / kScoreBlock * kScoreBlock;
     s.splits = (int)((vocab + s.segment - 1) / s.segment);
     if (s.splits > 1) s.bytes = tokens * s.splits * (16 + 8 * top);
