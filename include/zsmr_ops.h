@@ -199,9 +199,12 @@ typedef struct zsmr_newton {
 #define ZSMR_MAX_MATRIX   ((int64_t)1 << 33)
 #define ZSMR_MAX_MATRICES ((int64_t)1 << 20)
 
-/* Bytes of workspace of the two calls below, or -1 for sizes they refuse: 8
- * bytes an element and 8 an element of the inner matrices, for the matrices that
- * are worked on at a time (2^25 elements at most, or one matrix). */
+/* Bytes of workspace of the two calls below, or -1 for sizes they refuse.  For the
+ * matrices that are worked on at a time (2^25 elements at most, or one matrix) 8 bytes
+ * an element, and an element of the inner m x m matrix, m the shorter side, 8, or 20
+ * where the longer side is 1.2 m or more; rows count with a padding to 32.  Matrices of
+ * up to 2^25 elements need less than 1.0 GB, however many there are.  It serves every
+ * format of the result and every list of steps, so a call may leave some of it alone. */
 int64_t zsmr_orthogonalize_workspace(int64_t rows, int64_t cols, int64_t count);
 
 /* out[k] = the last X of x[k], rounded to out_dtype once, for `count` matrices of

@@ -29,7 +29,8 @@ struct NsShape {
 };
 
 // A group's matrices have 2^25 elements at most (or are one): enough to fill the
-// CUs many times over, while the workspace stays below 600 MB for any count.
+// CUs many times over, while the workspace stays below 1.0 GB for any count (104 x 129
+// needs the most an element: 29.8 bytes, with rows padded to 128 and 160).
 constexpr int64_t kNsGroupElems = int64_t(1) << 25;
 
 // A matrix that fits a CU's LDS with its inner matrix is one workgroup's: every pass
@@ -166,7 +167,9 @@ inline NsGrid ns_grid(const NsShape& s, int kind, int64_t products, int64_t step
 
 // The workspace: byte offsets of its parts, and its size.  X is there twice (a
 // product cannot write what its other tiles still read); the second copy holds the
-// fp32 update before the first product.
+// fp32 update before the first product.  Single steps have two inner matrices, steps in
+// groups five; the size is that of groups wherever they are allowed, since whether
+// they are taken depends on the steps' factors too.
 struct NsSpace {
     int64_t matrix[kNsMatrices], partial, inverse, bytes;
 };
