@@ -38,7 +38,8 @@ constexpr int64_t kNsGroupElems = int64_t(1) << 25;
 inline int ns_small(int64_t m, int64_t n) {
     return m <= 64 ? n <= 64 ? 1 : n <= 256 ? 2 : 0 : n <= 128 ? 3 : 0;
 }
-inline NsShape ns_shape(int64_t rows, int64_t cols, int64_t count, bool fp32_result) {
+// single: every step has its own product with X.
+inline NsShape ns_shape(int64_t rows, int64_t cols, int64_t count, bool single) {
     NsShape s{};
     s.tall = rows > cols;
     s.m = std::min(rows, cols);
@@ -47,8 +48,8 @@ inline NsShape ns_shape(int64_t rows, int64_t cols, int64_t count, bool fp32_res
     s.np = ns_ceil(s.n, kNsStep);
     s.count = count;
     s.small = ns_small(s.m, s.n);
-    // from n = 1.2 m on; fp32 results keep the accuracy of single steps
-    s.grouped = !s.small && !fp32_result && s.n * 5 >= s.m * 6;
+    // from n = 1.2 m on
+    s.grouped = !s.small && !single && s.n * 5 >= s.m * 6;
     s.group = std::max<int64_t>(1, std::min({count, kNsGroupElems / (s.m * s.n), int64_t(1) << 14}));
     // a workgroup of the sums takes 2,048 elements at a time
     s.parts = (int)std::min<int64_t>((s.m * s.n + 2047) / 2048, std::max<int64_t>(1, 1024 / s.group));
@@ -268,9 +269,13 @@ constexpr int kNsMaxOps = 4 * ZSMR_MAX_NS_STEPS + 4;
 // goes on among m x m matrices, all symmetric, and multiplies X once, by Q = S .. S:
 // 3 n / m + 4 g - 3 products of m^3 for g steps, where single steps have (3 n / m + 1) g.
 // What it costs is accuracy: an error of A grows by S^2 a step.  Small singular values
-// are still small at the start, where three steps in a group are as accurate as one by
-// one (S^2 twice is 141 for the quintic; relative to the result 1e-5 to 9e-5 in all,
-// single steps 4e-6 to 6e-5, the fp32 form of the plain products the same), later two are.
+// are still small at the start, where three steps may be in a group (S^2 twice is 141 for
+// the quintic), later two.  Measured in the 2-norm, relative to the result, for 140 x 2,000
+// to 1,600 x 6,400: white noise 2.6e-6 to 5.2e-6 in groups, 0.9e-6 to 2.0e-6 step by step,
+// 1.3e-6 to 4.2e-6 with the library's fp32 products; singular values of 1/k^3 1.6e-5 to
+// 6.4e-5, 1.4e-5 to 5.2e-5, 2.3e-5 to 8.3e-5; near rank one 5.1e-5 to 2.0e-4, 4.6e-5 to
+// 1.7e-4, 8.2e-5 to 2.7e-4.  So groups are about as accurate as products of fp32 operands,
+// and are taken wherever a call does not ask for its result in fp32.
 inline int ns_group_steps(bool grouped, bool at_start, const double (*coef)[3], int left, double top) {
     const int most = std::min(left, !grouped ? 1 : at_start ? 3 : 2);
     const double limit = at_start ? 256 : 16;
