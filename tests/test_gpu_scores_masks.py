@@ -159,3 +159,76 @@ def test_gradient_of_rows_far_from_zero(dtype, at, v, many):
     wide = torch.full((len(x), v + 9), 4.0, device="cuda", dtype=dtype)
     z.zsmr_logprobs_grad(raw, ids, out["lse"], out["entropy"], wide[:, 3:3 + v], dlogprob=g, dentropy=h)
     assert torch.equal(wide[:, 3:3 + v], d) and (wide[:, :3] == 4).all() and (wide[:, 3 + v:] == 4).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_the_smallest_and_largest_scales(dtype):
+    """At 2^-100 all log probabilities are equal, at 2^100 the largest logits are all."""
+    x = torch.randn(5, 6000, generator=gen(13), device="cuda").to(dtype)
+    x[1] = x[1].clamp(max=0.5)          # a tie of many
+    x[2] -= 50.0
+    x[3, ::2] = -INF
+    x[4] = torch.finfo(dtype).min
+    ids = torch.tensor([0, int(x[1].argmax()), 7, 1, -1], device="cuda")
+    for scale in (2.0 ** -100, 2.0 ** 100):
+        check(x, ids, 9, scale)
+        check_gradient(x, ids, scale)
+
+
+def test_nan_and_infinity_in_far_rows():
+    x = torch.full((6, 90000), -1e9, device="cuda")
+    x[0, 77] = float("nan")
+    x[1, 80000] = INF
+    x[2] = 1e9
+    x[2, 5] = float("nan")
+    x[3, 40000:] = -INF
+    x[4, 0] = float("nan")
+    x[4, 1:] = INF
+    out = score(x, torch.zeros(6, device="cuda", dtype=torch.int64), 3)
+    assert torch.isnan(out["lse"][[0, 2, 4]]).all() and torch.isnan(out["entropy"][[0, 2, 4]]).all() and torch.isnan(out["logprob"][[0, 2, 4]]).all()
+    assert out["lse"][1] == INF and torch.equal(out["top_ids"], best(x, 3))
+    good = [3, 5]
+    check(x[good], torch.tensor([5, 89999], device="cuda"), 3, 1.0)
+    d = torch.empty_like(x)
+    one = torch.ones(6, device="cuda")
+    z.zsmr_logprobs_grad(x, torch.zeros(6, device="cuda", dtype=torch.int64), out["lse"], out["entropy"], d, one, one)
+    assert torch.isnan(d[[0, 2, 4]]).all() and torch.isfinite(d[good]).all()
+
+
+def test_far_rows_captured():
+    """Rows move between ordinary, masked and far ones from replay to replay."""
+    x, ids = masked(BF16, 90000, 1, -1e9)
+    out = {k: torch.empty(8, device="cuda") for k in ("logprob", "lse", "entropy")}
+    d, g = torch.empty_like(x), torch.ones(8, device="cuda")
+    ws = torch.empty(z.zsmr_logprobs_workspace(8, 90000, 0), device="cuda", dtype=torch.uint8)
+
+    def run():
+        z.zsmr_logprobs(x, ids, out["logprob"], out["lse"], out["entropy"], ws)
+        z.zsmr_logprobs_grad(x, ids, out["lse"], out["entropy"], d, dlogprob=g, dentropy=g)
+
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for mask in (-1e30, -INF, torch.finfo(BF16).min, -1e9, 1e10):
+        x.copy_(masked(BF16, 90000, 1, mask)[0])
+        ws.fill_(0xff)
+        graph.replay()
+        got = [t.clone() for t in (*out.values(), d)]
+        torch.cuda.synchronize()
+        run()
+        assert all(torch.equal(a, b) for a, b in zip(got, (*out.values(), d)))
+        check(x, ids, 4, 1.0)
+        check_gradient(x, ids, 1.0)
+
+
+@pytest.mark.parametrize("v,many", SHAPES)
+def test_rows_about_the_last_near_reference(v, many):
+    """Products with log2 e of 2^20 and some powers more or fewer, of either sign."""
+    edge = 2.0 ** 20 / 1.4426950408889634
+    k = torch.tensor([-300.0, -100.0, -89.0, -60.0, -45.0, -44.0, -20.0, 0.0, 3.0, 20.0, 44.0, 45.0, 60.0, 89.0, 100.0, 300.0], device="cuda")
+    at = torch.cat([edge + k, -edge + k])
+    x = (at[:, None] + torch.randn(32, v, generator=gen(14), device="cuda") * 3).repeat(many, 1)
+    ids = (torch.arange(32 * many, device="cuda") * 37) % v
+    check(x, ids, 3, 1.0)
+    check_gradient(x, ids, 1.0)
