@@ -220,7 +220,8 @@ int32_t zsmr_orthogonalize(const void* x, int32_t x_dtype, int64_t x_stride, int
                            int64_t rows, int64_t cols, int64_t count, const zsmr_newton* ns,
                            void* ws, int64_t ws_bytes, hipStream_t stream);
 
-/* lr, weight_decay, scale: finite, >= 0; 0 <= beta < 1; nesterov 0 or 1. */
+/* lr, weight_decay, scale: finite, >= 0, and lr * weight_decay and lr * scale in fp32's
+ * range; 0 <= beta < 1; nesterov 0 or 1. */
 typedef struct zsmr_muon {
     double lr, beta, weight_decay, scale;
     int32_t nesterov, pad;

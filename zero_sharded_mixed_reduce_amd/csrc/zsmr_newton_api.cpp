@@ -3,6 +3,7 @@
 // zsmr_newton_launch.h go to the caller's stream.  No device memory is allocated
 // and nothing is kept between calls.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -84,6 +85,9 @@ int32_t zero_muon_step(zsmr_ctx* c, int32_t rank, int32_t unit, int64_t begin, i
     if (!hp || !std::isfinite(hp->lr) || !std::isfinite(hp->beta) || !std::isfinite(hp->weight_decay) || !std::isfinite(hp->scale) ||
         hp->lr < 0 || hp->beta < 0 || hp->beta >= 1 || hp->weight_decay < 0 || hp->scale < 0 || (hp->nesterov != 0 && hp->nesterov != 1))
         return ZSMR_ERR_ARG;
+    // factors that the kernels have in fp32
+    const double decay = 1.0 - hp->lr * hp->weight_decay, rate = hp->lr * hp->scale;
+    if (!(std::fabs(decay) <= FLT_MAX) || !(rate <= FLT_MAX)) return ZSMR_ERR_ARG;
     int64_t len = 0;
     piece(c, rank, unit, nullptr, &len, nullptr);
     const int64_t each = rows * cols, total = count * each;     // at most 2^53
@@ -111,8 +115,8 @@ int32_t zero_muon_step(zsmr_ctx* c, int32_t rank, int32_t unit, int64_t begin, i
     a.param_dtype = c->pdt;
     a.nesterov = hp->nesterov;
     a.beta = (float)hp->beta;
-    a.decay = (float)(1.0 - hp->lr * hp->weight_decay);
-    a.rate = (float)(hp->lr * hp->scale);
+    a.decay = (float)decay;
+    a.rate = (float)rate;
     NsOp ops[kNsMaxOps];
     const hipError_t e = launch_muon(a, ops, ns_choose(ns->coef, ns->steps, a.shape, ops), ws, stream);
     if (e != hipSuccess) return hip_fail(e);
