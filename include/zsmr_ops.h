@@ -250,7 +250,8 @@ int32_t zero_muon_step(zsmr_ctx* ctx, int32_t rank, int32_t unit, int64_t begin,
  *   lse = log sum_v exp z_v,  logprob = z_id - lse,  p_v = exp(z_v - lse),
  *   entropy = -sum_v p_v log p_v.
  * Logits of -infinity are masked: p = 0.  So are values of z below -2.3e38, which
- * the lowest values of bf16 and fp32 are.  A row with nothing else has lse
+ * the lowest values of bf16 and fp32 are unless scale makes them larger; that of fp16,
+ * -65,504, and other finite masks are ordinary logits.  A row with nothing else has lse
  * -infinity, entropy 0, log probabilities of -infinity and a gradient of zeros.  A
  * NaN makes a row's lse, logprob, entropy and gradient NaN; +infinity, or a z above
  * 2.3e38, makes its lse +infinity and leaves the rest of the row's results but the
