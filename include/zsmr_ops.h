@@ -181,7 +181,9 @@ int32_t zero_clipped_step(zsmr_ctx* ctx, int32_t rank, int32_t unit, const float
  * an odd polynomial that moves every singular value the way the triple says:
  * with a = 3.4445, b = -4.7750, c = 2.0315 five times, to about 1.  Every
  * product has fp32's accuracy (operands of 22 bits, fp32 sums), whatever the
- * formats of x and out.  For 16-bit results, and in the shard step, steps may share
+ * formats of x and out.  An operand is no finer than 2^-39 of the largest value that
+ * the steps allow its matrix, or of 1: what is that small beside it (an x far below eps,
+ * singular values that a step shrinks to nothing) has fewer bits.  For 16-bit results, and in the shard step, steps may share
  * their products with X, which leaves up to three times the error of single steps: of
  * the 2-norm 2e-6 to 6e-6 for white noise (single 1e-6 to 2e-6, products of fp32
  * operands 1e-6 to 5e-6), 2e-4 near rank one (1.7e-4, 2.7e-4).  A matrix of zeros
