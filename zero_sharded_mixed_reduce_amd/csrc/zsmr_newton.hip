@@ -302,9 +302,10 @@ struct OldTerms {
 // steps in turn and add up their sums in the end.  N_PARTIAL: some of the steps of an
 // N_INNER product, whose sums go to memory as they are.
 // Bound by the power of the matrix units where the tiles fill the CUs: X' of 4,096 x
-// 14,336, wide tiles, takes 1.08 ms, 1.34 PFLOP/s of fp16 with the units busy in 0.76 of
-// the cycles at 1.76 GHz; the inner products of 4,096 run at 1.24.  Elsewhere by one
-// round's steps (zsmr_newton_plan.h has what each form takes).
+// 14,336, wide tiles, takes 1.10 to 1.15 ms on two cards, 1.25 to 1.32 PFLOP/s of fp16 with
+// the units busy in 0.77 of the cycles at 1.66 to 1.70 GHz; the inner products of 4,096 run
+// at 1.17 to 1.22.  Elsewhere by one round's steps (zsmr_newton_plan.h has what each form
+// takes).
 constexpr int N_PARTIAL = 100;
 template <int KIND, int T, int GROUPS, int STAGES>
 __global__ __launch_bounds__(kThreads * GROUPS, T == 64 && STAGES == 2 ? 4 : 2) void ns_product_kernel(NsProduct p) {
@@ -493,8 +494,8 @@ __global__ __launch_bounds__(kThreads * GROUPS, T == 64 && STAGES == 2 ? 4 : 2) 
 }
 
 // What the parts of an N_PARTIAL product add up to, a quarter of a tile a workgroup.
-// Reads the parts once: 9.4 us for 91 tiles of 5 parts, 50 for 528 of 6 (4.7 TB/s with
-// what it writes).
+// Reads the parts once: 10 us for 91 tiles of 5 parts, 53 to 55 for 528 of 6 (5.0 TB/s
+// with what it writes).
 __global__ __launch_bounds__(kThreads) void ns_join_kernel(NsProduct p, int split) {
 #if defined(__HIP_DEVICE_COMPILE__)
     constexpr int kPitch = 68;      // rows are read along p and along q
@@ -836,7 +837,7 @@ __device__ __forceinline__ void by_dtype(int32_t dtype, F each) {
 
 // A matrix of at most MP x NP.  A product waits for the one before it, so a CU's matrix
 // units are busy 0.15 (64 x 64) to 0.29 (128 x 128) of the time; 24 of 64 x 64 take 16.1 us
-// where 15 launches of products would take 92.  The plain call reads and writes each register's four
+// where the 18 launches of larger ones took 92.  The plain call reads and writes each register's four
 // elements where they lie.  The shard's step (STEP) has nrows + 2 arrays of the matrix's
 // shape to read and three to write, so it takes memory in its own order, eight elements of
 // a row a thread, and the matrix changes hands in LDS, as fp32 rows a little longer than

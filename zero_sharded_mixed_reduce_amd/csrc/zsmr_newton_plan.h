@@ -92,7 +92,9 @@ inline int64_t ns_groups(const NsPart& p) { return ns_quarters(p.form) ? p.count
 // 7.5, 8 and 5.5 us; under full load (where the power decides) 1.22 us for two wide
 // tiles, 0.68 for a deep and 0.26 for a thin one, 0.4 for a pair (0.52
 // in each of several rounds).  364 quarters of 50 steps: thin 28.2 us, in pairs 24.6; 78
-// of 24: 9.6 and 12.3; 1,456 of 50: in pairs 77.5, 364 wide tiles 68.
+// of 24: 9.6 and 12.3; 1,456 of 50: in pairs 77.5, 364 wide tiles 68.  Between one round and
+// two this is too low: 650 and 676 wide tiles of 50 steps take 106 to 119 us and not 98.5,
+// and two products of 91 tiles in one launch, deep, 45 and not 37.
 inline double ns_cost(int form, int64_t tiles, int64_t steps) {
     const int64_t groups = ns_quarters(form) ? tiles * 4 : tiles, each = form == NS_WIDE || form == NS_PAIR ? 2 * kNsCus : kNsCus;
     const int64_t full = groups / each, rest = groups % each;
@@ -107,7 +109,7 @@ inline double ns_cost(int form, int64_t tiles, int64_t steps) {
 //
 // X X^T of a long X has more steps than tiles.  Its steps may be split: every part's tiles
 // go to memory in fp32 (into X's other copy, free at that time), and ns_join_kernel adds
-// them up.  1,600 x 6,400: 55 us and 9 to join 5 parts,
+// them up.  1,600 x 6,400: 61 us and 10 to join 5 parts,
 // 110 in one; 128 x 8,192: 9 and 7 for 16, 59 in one.
 constexpr int kNsMaxSplit = 16;
 constexpr int64_t kNsTileBytes = 128 * 128 * 4;

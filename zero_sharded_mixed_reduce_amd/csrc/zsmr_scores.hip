@@ -281,10 +281,12 @@ struct Block {
     }
 };
 
-// 8,192 rows of 128,256 bf16: 381 us, 5.5 TB/s, of which the vector units' work on every
-// logit (widen, multiply-add, power, two sums) takes nearly all cycles; 1,023 rows of 50,257
-// fp32 with 5 alternatives 41 us, 5.0 TB/s; 16 rows of 128,256 bf16 with 20 alternatives 9.3
-// and 6.7 for the join, latency.
+// 8,192 rows of 128,256 bf16: 377 to 413 us, 5.1 to 5.6 TB/s, of which the vector units' work
+// on every logit (widen, multiply-add, power, two sums) takes nearly all cycles; 4,096 of fp32
+// 360 us, 5.8 TB/s.  1,023 rows of 50,257 fp32 with 5 alternatives 41 us, 5.0 TB/s, where the
+// vector work of a logit is more than twice that without them; 16 rows of 128,256 bf16 with
+// 20 alternatives 9.6 and 7 for the join, latency.  Rows taken a second time, 8,192 of 128,256:
+// 0.85 ms, or 0.59 where all is masked.
 template <int DT, bool TOP, int kWaves>
 __global__ __launch_bounds__(kWaves * 64, 8) void scores_kernel(ForwardArgs f) {
     const ScoreArgs& a = f.a;
@@ -531,7 +533,7 @@ __global__ __launch_bounds__(kJoinWaves * 64) void scores_join_kernel(ForwardArg
 
 // ------------------------------------------------------------------ gradient --
 // A workgroup takes kGradBlock elements of a row; what is the row's own is read once.
-// 8,192 rows of 128,256 bf16: 685 us, 6.1 TB/s.
+// 8,192 rows of 128,256 bf16: 680 to 750 us, 5.6 to 6.2 TB/s; 4,096 of fp32 808, 5.2 TB/s.
 // ds = g' [v = id] - p (g' + h' (log p + H)) with g' = scale g and h' = scale h, log p in
 // the base 2 that the power needs.
 //
